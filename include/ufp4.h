@@ -426,6 +426,128 @@ ufp4_status ufp4_sign_vector(uint64_t sign_seed, int32_t n, int8_t* out_host);
 ufp4_status ufp4_round_levels(int32_t grid, int32_t rounding, int32_t scale_fmt, const float* t, const uint16_t* u16,
                               int64_t count, uint8_t* codes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The training step between the GEMMs: what a feed-forward block and the
+ * vocabulary head of a model need around the quantized GEMMs of FPROP, DGRAD
+ * and WGRAD [UFP4-method].  These calls take any row pitch and any alignment
+ * of their elements (16-byte aligned rows run the vectorized kernels) and
+ * any column count unless said otherwise; non-finite values are inside their
+ * contract.  The rules above on ownership, asynchrony and errors hold, and
+ * the kernels are launched as programmatic dependents on non-default streams.
+ *
+ * 8-bit checkpoints.  The forward calls can store what their backward calls
+ * need in 8 bits instead of keeping the bf16 or fp32 values: a qtensor of
+ * rows x cols with one E4M3 byte per element (codes_ld >= cols bytes) and one
+ * E8M0 byte per 32 elements of a row (scales_ld >= ceil(cols / 32); the last
+ * block of a row may be short), i.e. the container of UFP4_GRID_MXFP8, which
+ * ufp4_dequantize reads where cols is a multiple of 32 and codes is 16-byte
+ * aligned.  The scale is the truncation-free one [2D-block]: e the least
+ * integer with M <= 448 * 2^e (M the block's amax), clamped to at least -127,
+ * stored as e + 127; codes are v * 2^-e rounded to E4M3, nearest even, a zero
+ * code as +0.  A block holding a NaN or an infinity gets scale byte 255 and
+ * codes 0x7F and reads back as NaN; a finite value that rounds to 2^128
+ * (above 248 * 2^120) reads back as an infinity.  tensor_amax is unused. */
+typedef enum { UFP4_BF16 = 0, UFP4_F32 = 1 } ufp4_dtype;
+
+/* act(g) of the gated activation: SILU g / (1 + exp(-g)); GELU the tanh form
+ * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
+typedef enum { UFP4_ACT_SILU = 0, UFP4_ACT_GELU = 1 } ufp4_act;
+
+/* ufp4_glu -- y = act(gate) * up, elementwise over rows x cols.
+ *   gate, up   device bf16 or fp32 (in_dtype, ufp4_dtype), leading dimensions
+ *              ld_gate, ld_up (the two halves of one GEMM output, say)
+ *   y          device bf16, leading dimension ldy
+ *   ckpt_gate, ckpt_up  8-bit checkpoints of gate and up, written; both or
+ *              neither (NULL) */
+ufp4_status ufp4_glu(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int32_t in_dtype, int64_t rows,
+                     int64_t cols, int32_t act, void* y, int64_t ldy, const ufp4_qtensor* ckpt_gate,
+                     const ufp4_qtensor* ckpt_up, cudaStream_t stream);
+
+/* ufp4_glu_backward -- the gradients of ufp4_glu at the checkpointed values
+ * g, u: dgate = dy u act'(g), dup = dy act(g), and y = act(g) u again for the
+ * down projection's WGRAD.
+ *   dy          device bf16 or fp32 (dy_dtype), leading dimension ld_dy
+ *   dgate, dup  device bf16, written
+ *   y           device bf16, written unless NULL */
+ufp4_status ufp4_glu_backward(const void* dy, int64_t ld_dy, int32_t dy_dtype, const ufp4_qtensor* ckpt_gate,
+                              const ufp4_qtensor* ckpt_up, int64_t rows, int64_t cols, int32_t act, void* dgate,
+                              int64_t ld_dgate, void* dup, int64_t ld_dup, void* y, int64_t ldy, cudaStream_t stream);
+
+/* ufp4_rms_norm -- residual add and RMS norm of each row: s = x + residual
+ * (fp32), rstd = 1 / sqrt(mean(s^2) + eps), y = s rstd gamma.
+ *   x         device bf16 or fp32 (x_dtype), leading dimension ldx
+ *   residual  device bf16, leading dimension ld_residual, or NULL
+ *   gamma     device bf16 or fp32 (gamma_dtype), cols elements
+ *   eps       > 0
+ *   y         device bf16, written
+ *   total     device bf16, s rounded (the stream carried on), or NULL
+ *   rstd      device float, rows elements; NULL only without ckpt
+ *   ckpt      8-bit checkpoint of s, written, or NULL
+ * 1 <= cols <= 32768 (UFP4_ERR_UNSUPPORTED beyond). */
+ufp4_status ufp4_rms_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* residual, int64_t ld_residual,
+                          const void* gamma, int32_t gamma_dtype, int64_t rows, int64_t cols, float eps, void* y,
+                          int64_t ldy, void* total, int64_t ld_total, float* rstd, const ufp4_qtensor* ckpt,
+                          cudaStream_t stream);
+
+/* ufp4_rms_norm_backward -- the gradients of ufp4_rms_norm at the
+ * checkpointed rows s with h = s rstd: dx = rstd (dy gamma - h mean(dy gamma
+ * h)) + dtotal, which is the gradient of x and of residual alike, dgamma =
+ * sum over the rows of dy h (fp32, in an order that depends on the shape and
+ * the device only), and y = h gamma again for a WGRAD.
+ *   dy         device bf16 or fp32 (dy_dtype), leading dimension ld_dy
+ *   ckpt, rstd what ufp4_rms_norm wrote
+ *   dtotal     device bf16, the gradient of `total`, or NULL
+ *   dx         device bf16, written; dgamma device float, cols elements,
+ *              written (zeros when rows is 0)
+ *   y          device bf16, written unless NULL
+ *   workspace  at least ufp4_rms_norm_backward_workspace_size bytes,
+ *              256-byte aligned; contents on entry are ignored. */
+ufp4_status ufp4_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dtype, const ufp4_qtensor* ckpt,
+                                   const float* rstd, const void* gamma, int32_t gamma_dtype, const void* dtotal,
+                                   int64_t ld_dtotal, int64_t rows, int64_t cols, void* dx, int64_t ld_dx,
+                                   float* dgamma, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
+/* ufp4_head_loss -- softmax cross entropy of the logits l = h w^T over the
+ * vocabulary, which are never stored: lse[t] = log sum_v exp(l[t, v]) and
+ * loss[t] = lse[t] - l[t, targets[t]] + z_loss lse[t]^2.
+ *   h        device bf16 [tokens x hidden], leading dimension ldh
+ *   w        device bf16 [vocab x hidden], leading dimension ldw; both 16-byte
+ *            aligned with leading dimensions that are multiples of 8
+ *   targets  device int64, tokens elements.  A token whose target is outside
+ *            [0, vocab) is ignored: its loss and lse are 0, its row of h is
+ *            not looked at, and it costs nothing in the products.
+ *   loss, lse  device float, tokens elements, written
+ *   workspace  at least ufp4_head_loss_workspace_size bytes, 256-byte aligned
+ * Extents up to 2^30 (UFP4_ERR_UNSUPPORTED beyond). */
+ufp4_status ufp4_head_loss_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, size_t* bytes);
+ufp4_status ufp4_head_loss(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* targets,
+                           int64_t tokens, int64_t vocab, int64_t hidden, float z_loss, float* loss, float* lse,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ufp4_head_loss_backward -- the gradients of scale * sum_t token_weight[t]
+ * loss[t]: dl[t, v] = token_weight[t] ((1 + 2 z_loss lse[t]) exp(l[t, v] -
+ * lse[t]) - [v = targets[t]]), dh = scale dl w, dw = scale dl^T h.  The logits
+ * are computed again, a piece of the vocabulary at a time; dl is held in bf16
+ * (it is a tensor-core operand), dh and dw are summed in fp32.
+ *   h, w, targets, z_loss  as in ufp4_head_loss, lse as it wrote it
+ *   token_weight  device float, tokens elements, or NULL (ones)
+ *   scale      device float, one element, or NULL (one)
+ *   dh         device bf16 or fp32 (dh_dtype) [tokens x hidden], written (0 for
+ *              ignored tokens), or NULL
+ *   dw         device bf16 or fp32 (dw_dtype) [vocab x hidden], written, or
+ *              added to with accumulate_dw = 1 (fp32 only), or NULL; not both
+ *              dh and dw NULL
+ *   workspace  at least ufp4_head_loss_backward_workspace_size bytes,
+ *              256-byte aligned */
+ufp4_status ufp4_head_loss_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, size_t* bytes);
+ufp4_status ufp4_head_loss_backward(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* targets,
+                                    int64_t tokens, int64_t vocab, int64_t hidden, float z_loss, const float* lse,
+                                    const float* token_weight, const float* scale, void* dh, int64_t ld_dh,
+                                    int32_t dh_dtype, void* dw, int64_t ld_dw, int32_t dw_dtype, int32_t accumulate_dw,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* ufp4_device_error -- reads and clears the library's device error words on
  * the current device (synchronizes the device first).  Every device-side wait
  * of the library is bounded: a kernel whose wait gives up records the event,

@@ -12,6 +12,7 @@
 
 #include "../../include/ufp4.h"
 #include "internal.h"
+#include "train.h"
 
 using namespace ufp4;
 
@@ -86,6 +87,9 @@ void ensure_loaded() {
     preload_dequant_kernels();
     preload_stats_kernels();
     preload_round_levels_kernels();
+    preload_glu_kernels();
+    preload_norm_kernels();
+    preload_head_kernels();
     cudaGetLastError();  // a failed query shows up again at the launch
     done[dev] = true;
 }
@@ -410,6 +414,10 @@ ufp4_status run_prepared_gemm(const GemmArgs& g, cudaStream_t stream) {
 }
 
 }  // namespace
+
+namespace ufp4 {
+int current_num_sms() { return num_sms_current(); }
+}  // namespace ufp4
 
 extern "C" {
 

@@ -1,0 +1,172 @@
+// The 8-bit checkpoint of a row of fp32 values, and the loads and stores that
+// the operators around it share.
+//
+// A checkpoint is stored in the MXFP8 container of the quantizer (E4M3 byte
+// codes, one E8M0 scale byte per 32 elements of a row; 2D-block tutorial, the
+// format kept for the Query and Key projections), with the truncation-free
+// scale rule of the UE8M0 formats (same page, S = 2^ceil(log2(M / qmax))):
+// e is the least integer with M <= 448 * 2^e, M the block's largest magnitude.
+// Nothing saturates then: with MXFP8's floor(log2 M) - 8 an element in
+// (448, 512) * 2^e would lose up to an eighth of its value, a bias on exactly
+// the outliers that a backward pass depends on most.  Eight bits are the
+// point of a checkpoint: it halves (bf16) or quarters (fp32) what a layer
+// keeps between its forward and its backward pass, at a relative error of at
+// most 2^-4 per element.
+//
+// A block that holds a NaN or an infinity stores scale byte 255 and 0x7F
+// codes: it reads back as NaN, so an overflow is still seen in the gradients.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "train.h"
+
+namespace ufp4 {
+
+constexpr int kCkptBlock = 32;  // elements per scale
+constexpr int kVec = 8;         // elements a thread carries; four threads share a block
+
+// Bit pattern of |v|: ordered like the magnitudes, infinities and NaNs on top.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// E8M0 byte of a block whose largest magnitude has bit pattern m.  For a
+// normal M = f * 2^k (1 <= f < 2), 448 = 1.75 * 2^8 gives e = k - 8, plus one
+// when f > 1.75; the carry of the mantissa plus 0x1FFFFF into the exponent is
+// that plus one.
+__device__ __forceinline__ uint32_t ckpt_scale_byte(uint32_t m) {
+    if (m >= 0x7F800000u) return 255u;
+    const uint32_t f = (m + 0x1FFFFFu) >> 23;
+    return f > 8u ? f - 8u : 0u;
+}
+// 2^-e and 2^e of the scale byte e + 127 (bytes 0..247, or 255 in ckpt_unit:
+// an infinity, which a 0x7F code turns into NaN).
+__device__ __forceinline__ float ckpt_inv_unit(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+__device__ __forceinline__ float ckpt_unit(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
+
+// Four E4M3 bytes (round to nearest even) of v * inv; zeros as +0.
+__device__ __forceinline__ uint32_t ckpt_pack4(const float* v, float inv) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1] * inv), "f"(v[0] * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3] * inv), "f"(v[2] * inv));
+    const uint32_t c = (uint32_t)lo | ((uint32_t)hi << 16);
+    const uint32_t mag = c & 0x7F7F7F7Fu;
+    return mag | (c & (mag + 0x7F7F7F7Fu) & 0x80808080u);  // the sign only where a magnitude bit is set
+}
+
+__device__ __forceinline__ void ckpt_unpack4(uint32_t c, float unit, float* v) {
+    uint32_t a, b;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(c & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(c >> 16)));
+    const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    v[0] = fa.x * unit;
+    v[1] = fa.y * unit;
+    v[2] = fb.x * unit;
+    v[3] = fb.y * unit;
+}
+
+// The 8 elements at p (bf16 or fp32) as fp32.  VEC: p is aligned to the
+// vector and all 8 exist; otherwise the first n of them, zeros after.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load8(const void* p, int n, float v[kVec]) {
+    if (VEC) {
+        if (F32) {
+            const float4* q = reinterpret_cast<const float4*>(p);
+            const float4 a = __ldcs(q), b = __ldcs(q + 1);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            v[i] = i < n ? (F32 ? reinterpret_cast<const float*>(p)[i]
+                                : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]))
+                         : 0.0f;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8_bf16(__nv_bfloat16* p, int n, const float v[kVec]) {
+    if (VEC) {
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                       pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// Writes elements c .. c + 7 of a row; the four lanes of a quad hold one
+// block of 32 and call this together (n = 0 past the end of the row).
+template <bool VEC>
+__device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int c, int n, const float v[kVec]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) m = max(m, abs_bits(v[i]));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const uint32_t byte = ckpt_scale_byte(m);
+    uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if (byte != 255u) {
+        const float inv = ckpt_inv_unit(byte);
+        q.x = ckpt_pack4(v, inv);
+        q.y = ckpt_pack4(v + 4, inv);
+    }
+    if (n <= 0) return;
+    uint8_t* dst = k.codes + row * k.codes_ld + c;
+    if (VEC) {
+        __stcs(reinterpret_cast<uint2*>(dst), q);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i < n) dst[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    }
+    if ((c & (kCkptBlock - 1)) == 0) k.scales[row * k.scales_ld + c / kCkptBlock] = (uint8_t)byte;
+}
+
+// The values of elements c .. c + 7 of a row (zeros past n).
+template <bool VEC>
+__device__ __forceinline__ void ckpt_load8(const Ckpt& k, int64_t row, int c, int n, float v[kVec]) {
+    uint2 q = make_uint2(0u, 0u);
+    uint32_t byte = 0;
+    if (n > 0) {
+        byte = k.scales[row * k.scales_ld + c / kCkptBlock];
+        const uint8_t* src = k.codes + row * k.codes_ld + c;
+        if (VEC) {
+            q = __ldcs(reinterpret_cast<const uint2*>(src));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const uint32_t b = i < n ? (uint32_t)src[i] << (8 * (i & 3)) : 0u;
+                if (i < 4) q.x |= b; else q.y |= b;
+            }
+        }
+    }
+    const float unit = ckpt_unit(byte);
+    ckpt_unpack4(q.x, unit, v);
+    ckpt_unpack4(q.y, unit, v + 4);
+    if (!VEC && byte == 255u) {  // the zeros past the end of a row stay zeros beside a NaN block
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i >= n) v[i] = 0.0f;
+    }
+}
+
+}  // namespace ufp4

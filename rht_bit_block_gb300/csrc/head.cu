@@ -1,0 +1,901 @@
+// Softmax cross entropy of a vocabulary head, and its gradient, without the
+// logits in memory (the linear layer behind the last block of a model; its
+// three products are the FPROP, DGRAD and WGRAD of UFP4 summary, section 方法,
+// kept in bf16).
+//
+//   l = H W^T                       H: tokens x K, W: vocabulary x K
+//   lse_t = log sum_v exp l_tv      loss_t = lse_t - l_t,target + z lse_t^2
+//   dl_tv = w_t ((1 + 2 z lse_t) exp(l_tv - lse_t) - [v = target_t])
+//   dH = scale dl W                 dW = scale dl^T H
+//
+// Tokens without a target (ignored) take no part in any product: the first
+// kernel of either pass packs the rows of H that have one, so work goes with
+// the number of valid tokens, and whatever an ignored row holds stays out of
+// dW.  Forward, each 256 x 256 tile of logits leaves its rows' running maximum
+// and sum of exponentials, joined in the tiles' order by a last kernel.
+// Backward, the vocabulary is walked in pieces: a piece's logits are computed
+// again, become dl (bf16) in a workspace of two pieces, and are multiplied
+// into dH (fp32 across the pieces) and dW.  Recomputing costs 2 of the 8
+// products-and-sums per logit; keeping the logits would cost 4 bytes each.
+//
+// dl is rounded to bf16 because the tensor cores multiply it with bf16 W and H:
+// a relative error of at most 2^-8 per entry, as the outputs' own rounding,
+// and unbiased; the common factor `scale` is applied to the fp32 results, so
+// that a uniform weight does not round every entry the same way.
+//
+// All products run in one persistent kernel of CTA pairs (tcgen05.mma
+// .cta_group::2, 256 x 256 output tiles, fp32 accumulators in tensor memory,
+// two of them, so that a tile's epilogue overlaps the next tile's main loop).
+// A launch walks the tiles of up to three products (dH and dW of a piece and
+// the logits of the next), which fills the SMs where one product has few
+// tiles.  Operands are read as they lie in memory: where the summed index is
+// not the contiguous one (W in dH; dl and H in dW) the tiles are staged
+// MN-major and the instruction descriptor says so; nothing is transposed.
+#include <algorithm>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "train.h"
+
+namespace ufp4 {
+
+__device__ int g_head_error;
+
+namespace {
+
+constexpr int kTile = 256;                 // output tile of a CTA pair, both ways
+constexpr int kHalf = 128;                 // rows of A and of B that one CTA holds
+constexpr int kStep = 64;                  // summed elements per stage (one 128-byte swizzle row)
+constexpr int kBoxBytes = 64 * 64 * 2;     // one TMA box: 64 rows of 64 bf16
+constexpr int kOperand = 2 * kBoxBytes;    // one operand of one stage
+constexpr int kStages = 6;
+constexpr int kThreads = 256;
+constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sleep up to kSuspendNs
+constexpr uint32_t kSuspendNs = 1000;
+constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int kOffA = 0;
+constexpr int kOffB = kStages * kOperand;
+constexpr int kOffBars = 2 * kStages * kOperand;
+constexpr int kNumBars = 2 * kStages + 4 + 1;
+constexpr int kSmem = kOffBars + 8 * kNumBars + 16 + 1024;
+static_assert(kSmem <= 232448, "shared memory overflow");
+
+// ------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Bounded wait on an mbarrier phase; false (and the error word set) at the limit.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (ok) return true;
+    }
+    atomicExch(&g_head_error, 1);
+    return false;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+}
+// TMA box into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t cbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(cbar)
+        : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 128-byte swizzle shared-memory descriptor: 8-row groups 1024 bytes apart
+// (stride offset); MN-major operands also have their 64-element column blocks
+// one box apart (leading offset; unused K-major, where a stage is one column).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(kBoxBytes >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16: fp32 accumulator, bf16 operands, MN-major A (bit 15) and B (bit 16), N >> 3, M >> 4.
+__host__ __device__ constexpr uint32_t make_idesc(bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_local(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float r[32]) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]),
+          "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]),
+          "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]),
+          "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ------------------------------------------------------- packing the tokens
+// Per packed row, for the epilogues: its target, and backward its lse * log2(e),
+// weight * (1 + 2 z lse) and weight.
+struct RowInfo {
+    float lse2, a, weight;
+    int target;
+};
+
+struct PackParams {
+    const __nv_bfloat16* h;
+    int64_t ldh;
+    const int64_t* targets;
+    int64_t T, V, K, Kp;      // Kp: columns of the packed rows (K rounded up to 8)
+    int rows_per_cta;
+    __nv_bfloat16* packed;    // rounded-up rows x Kp
+    int* index;               // packed row -> token
+    RowInfo* info;
+    int* count;
+    float* loss;              // forward: 0 for ignored tokens
+    float* lse_out;
+    const float* lse;         // backward
+    const float* weight;
+    float z;
+    void* dh;                 // backward: 0 for ignored tokens
+    int64_t ld_dh;
+    int dh_f32;
+};
+
+// CTA b packs the valid tokens among its rows: it counts those before them,
+// then copies row by row.  Rows from the count up to the next multiple of
+// kStep are zeroed: dW sums over them.
+template <bool BACK>
+__global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
+    __shared__ int before_s, all_s;
+    griddep_wait();
+    griddep_launch();
+    const int64_t r0 = (int64_t)blockIdx.x * p.rows_per_cta;
+    const int64_t r1 = min(r0 + p.rows_per_cta, p.T);
+    if (threadIdx.x == 0) before_s = all_s = 0;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int64_t r = threadIdx.x; r < p.T; r += blockDim.x) {
+        const int64_t t = p.targets[r];
+        const int v = t >= 0 && t < p.V;
+        all += v;
+        before += v && r < r0;
+    }
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    all = __reduce_add_sync(0xFFFFFFFFu, all);
+    if ((threadIdx.x & 31) == 0) {
+        atomicAdd(&before_s, before);
+        atomicAdd(&all_s, all);
+    }
+    __syncthreads();
+    const int count = all_s;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = count;
+    auto clear_row = [&](char* row, int64_t bytes) {  // 2-byte multiples, 2-byte aligned at least
+        for (int64_t i = threadIdx.x; i < bytes / 2; i += blockDim.x) reinterpret_cast<uint16_t*>(row)[i] = 0;
+    };
+    int at = before_s;
+    for (int64_t r = r0; r < r1; ++r) {
+        const int64_t t = p.targets[r];
+        const bool valid = t >= 0 && t < p.V;
+        if (!valid) {
+            if (BACK) {
+                const int es = p.dh_f32 ? 4 : 2;
+                if (p.dh) clear_row((char*)p.dh + r * p.ld_dh * es, p.K * es);
+            } else if (threadIdx.x == 0) {
+                p.loss[r] = 0.0f;
+                p.lse_out[r] = 0.0f;
+            }
+            continue;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(p.h + r * p.ldh);
+        uint4* dst = reinterpret_cast<uint4*>(p.packed + (int64_t)at * p.Kp);
+        for (int64_t i = threadIdx.x; i < p.K / 8; i += blockDim.x) dst[i] = src[i];
+        if (threadIdx.x < p.K % 8) {  // nothing past a row's K elements is read
+            const int64_t i = p.K / 8 * 8 + threadIdx.x;
+            p.packed[(int64_t)at * p.Kp + i] = p.h[r * p.ldh + i];
+        }
+        if (threadIdx.x == 0) {
+            p.index[at] = (int)r;
+            RowInfo info = {0.0f, 0.0f, 0.0f, (int)t};
+            if (BACK) {
+                const float l = p.lse[r], w = p.weight ? p.weight[r] : 1.0f;
+                info.lse2 = l * kLog2e;
+                info.weight = w;
+                info.a = w * fmaf(2.0f * p.z, l, 1.0f);
+            }
+            p.info[at] = info;
+        }
+        ++at;
+    }
+    if (BACK) {
+        const int end = (count + kStep - 1) / kStep * kStep;
+        for (int z = count + blockIdx.x; z < end; z += gridDim.x)
+            clear_row((char*)(p.packed + (int64_t)z * p.Kp), p.Kp * 2);
+    }
+}
+
+// ------------------------------------------------------------- the products
+enum JobKind { kStats = 0, kGrad = 1, kDH = 2, kDW = 3 };
+
+// One product of a launch.
+//   kStats  logits of all of W: rows' (max, sum) per tile, target logits
+//   kGrad   logits of a piece of W -> dl of the piece
+//   kDH     dl (packed rows x piece) times the piece of W -> dH
+//   kDW     dl^T times the packed rows of H -> rows of dW
+struct Job {
+    int kind;
+    int a_map, b_map;       // tensor maps
+    int a_mn, b_mn;         // the operand's contiguous index is not the summed one
+    int m, n, k;            // extents; kernel-side: m (or k for kDW) comes from the token count
+    int v0;                 // first vocabulary row of the piece
+    int first, last;        // kDH: first and last piece
+    __nv_bfloat16* dl;      // kGrad: output
+    int64_t ld_dl;
+};
+constexpr int kMaxJobs = 3;
+constexpr int kMaps = 4;    // packed H, W, two pieces of dl
+struct HeadMaps {
+    CUtensorMap m[kMaps];
+};
+struct HeadParams {
+    Job job[kMaxJobs];
+    int jobs;
+    const int* count;
+    const int* index;
+    const RowInfo* info;
+    float2* part;           // kStats: [vocabulary tile][packed row]
+    float* target_logit;
+    int64_t Tp;
+    float* dh_acc;          // fp32 across the pieces: packed rows x Kp
+    int64_t Kp;
+    const float* scale;
+    void* dh;
+    int64_t ld_dh;
+    int dh_f32;
+    void* dw;
+    int64_t ld_dw;
+    int dw_f32, accumulate;
+};
+
+struct TileAt {
+    int job, m, n, k_steps;
+};
+
+// Tile rows that advance before the column does: the tiles in flight then
+// share a few panels of either operand, which stay in L2.
+constexpr int kGroupM = 8;
+
+struct Walk {
+    int m_tiles[kMaxJobs], n_tiles[kMaxJobs], k_steps[kMaxJobs], total;
+    __device__ __forceinline__ Walk(const HeadParams& p, int count) {
+        total = 0;
+        for (int j = 0; j < kMaxJobs; ++j) {
+            m_tiles[j] = n_tiles[j] = k_steps[j] = 0;
+            if (j >= p.jobs) continue;
+            const Job& q = p.job[j];
+            const int m = q.kind == kDW ? q.m : count, k = q.kind == kDW ? count : q.k;
+            m_tiles[j] = (m + kTile - 1) / kTile;
+            n_tiles[j] = (q.n + kTile - 1) / kTile;
+            k_steps[j] = (k + kStep - 1) / kStep;
+            total += m_tiles[j] * n_tiles[j];
+        }
+    }
+    __device__ __forceinline__ TileAt at(int tile) const {
+        TileAt t;
+        t.job = 0;
+#pragma unroll
+        for (int j = 0; j + 1 < kMaxJobs; ++j) {
+            const int here = m_tiles[j] * n_tiles[j];
+            if (t.job == j && tile >= here) {
+                tile -= here;
+                t.job = j + 1;
+            }
+        }
+        int mt = m_tiles[0], nt = n_tiles[0];
+        t.k_steps = k_steps[0];
+#pragma unroll
+        for (int j = 1; j < kMaxJobs; ++j)
+            if (t.job == j) {
+                mt = m_tiles[j];
+                nt = n_tiles[j];
+                t.k_steps = k_steps[j];
+            }
+        const int span = kGroupM * nt, g = tile / span, first = g * kGroupM;
+        const int rows = min(kGroupM, mt - first), l = tile - g * span;
+        t.n = l / rows;
+        t.m = first + (l - t.n * rows);
+        return t;
+    }
+};
+
+// Stores 32 fp32 results of one row as bf16 or fp32 (added to what is there
+// when ADD), columns c .. c + 31 of which n exist.
+__device__ __forceinline__ void store_row(void* base, int64_t off, bool f32, bool add, int n, const float r[32]) {
+    if (f32) {
+        float* d = (float*)base + off;
+        if (n >= 32 && ((uintptr_t)d & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                float4 v = make_float4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                if (add) {
+                    const float4 o = *reinterpret_cast<const float4*>(d + i);
+                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                }
+                *reinterpret_cast<float4*>(d + i) = v;
+            }
+        } else {
+            for (int i = 0; i < 32; ++i)
+                if (i < n) d[i] = add ? d[i] + r[i] : r[i];
+        }
+        return;
+    }
+    __nv_bfloat16* d = (__nv_bfloat16*)base + off;
+    if (n >= 32 && ((uintptr_t)d & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(d + i) = make_uint4(pack_bf16(r[i], r[i + 1]), pack_bf16(r[i + 2], r[i + 3]),
+                                                          pack_bf16(r[i + 4], r[i + 5]), pack_bf16(r[i + 6], r[i + 7]));
+    } else {
+        for (int i = 0; i < 32; ++i)
+            if (i < n) d[i] = __float2bfloat16_rn(r[i]);
+    }
+}
+
+// The logits epilogue of one row of a tile: running maximum and sum.
+__device__ __forceinline__ void stats_chunk(float r[32], int n, float& m, float& s) {
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (i >= n) r[i] = -INFINITY;
+        top = fmaxf(top, r[i]);
+    }
+    const float shift = top == -INFINITY ? 0.0f : top * kLog2e;
+    s *= ex2(fmaf(m, kLog2e, -shift));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += ex2(fmaf(r[i], kLog2e, -shift));
+    m = top;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const uint32_t bars = base + kOffBars;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (kStages + s); };
+    auto accf_bar = [&](int b) { return bars + 8u * (2 * kStages + b); };
+    auto acce_bar = [&](int b) { return bars + 8u * (2 * kStages + 2 + b); };
+    const uint32_t drain_bar = bars + 8u * (2 * kStages + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kOffBars + 8 * kNumBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kOffBars + 8 * kNumBars + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int peer = (int)(rank & 1u);      // 0: leader (even CTA)
+    const uint32_t leader = rank & ~1u;
+    const int cluster_id = blockIdx.x >> 1;
+    const int num_clusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full_bar(s), 1);   // the leader's expect_tx arrival (both CTAs' bytes)
+            mbar_init(empty_bar(s), 1);  // the leader's commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf_bar(b), 1);   // the leader's commit
+            mbar_init(acce_bar(b), 8);   // four epilogue warps of each CTA
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any copy or commit targets them
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    griddep_launch();
+
+    const int count = *p.count;
+    const Walk walk(p, count);
+
+    if (warp == 0 && lane == 0) {
+        // ---------------------------------------------------- TMA producer (both CTAs)
+        int s = 0;
+        uint32_t ph = 0;
+        for (int tile = cluster_id; tile < walk.total && !*abort_flag; tile += num_clusters) {
+            const TileAt t = walk.at(tile);
+            const Job& q = p.job[t.job];
+            const CUtensorMap* am = &maps.m[q.a_map];
+            const CUtensorMap* bm = &maps.m[q.b_map];
+            // W's rows are the whole vocabulary, a piece starts at v0; dl's columns are the piece's own
+            const int a0 = t.m * kTile + peer * kHalf;
+            const int b0 = t.n * kTile + peer * kHalf + (q.b_mn ? 0 : q.v0);
+            const int kb = q.kind == kDH ? q.v0 : 0;  // first summed row of B
+            for (int ks = 0; ks < t.k_steps; ++ks) {
+                if (!mbar_wait(empty_bar(s), ph ^ 1u)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                const uint32_t fb = map_to_rank(full_bar(s), leader);
+                if (peer == 0) mbar_expect_tx(full_bar(s), 4 * kOperand);
+                const uint32_t sa = base + kOffA + s * kOperand, sb = base + kOffB + s * kOperand;
+                const int k = ks * kStep;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (q.a_mn)
+                        tma_load(sa + j * kBoxBytes, am, a0 + 64 * j, k, fb);
+                    else
+                        tma_load(sa + j * kBoxBytes, am, k, a0 + 64 * j, fb);
+                    if (q.b_mn)
+                        tma_load(sb + j * kBoxBytes, bm, b0 + 64 * j, kb + k, fb);
+                    else
+                        tma_load(sb + j * kBoxBytes, bm, k, b0 + 64 * j, fb);
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && peer == 0) {
+        // ------------------------------------------------ MMA issuer (leader only)
+        int s = 0, tc = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = cluster_id; tile < walk.total && ok; tile += num_clusters, ++tc) {
+            const TileAt t = walk.at(tile);
+            const Job& q = p.job[t.job];
+            const int buf = tc & 1;
+            if (!mbar_wait(acce_bar(buf), ((tc >> 1) & 1) ^ 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * kTile;
+            const uint32_t idesc = make_idesc(q.a_mn, q.b_mn);
+            // 16 summed elements: 32 bytes along a swizzle row, or 16 rows of 128 bytes
+            const int astep = q.a_mn ? 2048 >> 4 : 32 >> 4, bstep = q.b_mn ? 2048 >> 4 : 32 >> 4;
+            for (int ks = 0; ks < t.k_steps; ++ks) {
+                if (!mbar_wait(full_bar(s), ph) || *abort_flag) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = sw128_desc(base + kOffA + s * kOperand);
+                const uint64_t db = sw128_desc(base + kOffB + s * kOperand);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_pair(acc, da + i * astep, db + i * bstep, idesc, (ks > 0 || i > 0) ? 1u : 0u);
+                tc_commit_both(empty_bar(s));  // frees stage s in both CTAs
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (ok) tc_commit_both(accf_bar(buf));
+        }
+        if (!ok) *abort_flag = 1;
+        tc_commit_local(drain_bar);
+        mbar_wait(drain_bar, 0);
+    } else if (warp >= 4) {
+        // ------------------------------------------------- epilogue (both CTAs)
+        const int q4 = warp - 4;
+        const float scale = p.scale ? *p.scale : 1.0f;
+        int tc = 0;
+        for (int tile = cluster_id; tile < walk.total; tile += num_clusters, ++tc) {
+            const int buf = tc & 1;
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(accf_bar(buf), (tc >> 1) & 1));
+            if (!ok || *abort_flag) break;
+            tc_fence_after();
+            const TileAt t = walk.at(tile);
+            const Job& q = p.job[t.job];
+            const int row = t.m * kTile + peer * kHalf + q4 * 32 + lane;
+            const int n0 = t.n * kTile;
+            const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + buf * kTile;
+            float r[32];
+            if (q.kind == kStats) {
+                const int target = row < count ? p.info[row].target : -1;
+                float m = -INFINITY, sum = 0.0f, hit = 0.0f;
+                for (int c = 0; c < kTile; c += 32) {
+                    tmem_ld32(acc + c, r);
+                    const int at = target - (n0 + c);
+                    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (at == i) hit = r[i];
+                    }
+                    stats_chunk(r, q.n - (n0 + c), m, sum);
+                }
+                if (row < count) {
+                    p.part[(int64_t)t.n * p.Tp + row] = make_float2(m, sum);
+                    if (target >= n0 && target < n0 + kTile) p.target_logit[row] = hit;
+                }
+            } else if (q.kind == kGrad) {
+                RowInfo info = {0.0f, 0.0f, 0.0f, -1};
+                if (row < count) info = p.info[row];
+                uint4* dst = reinterpret_cast<uint4*>(q.dl + (int64_t)row * q.ld_dl + n0);
+                for (int c = 0; c < kTile; c += 32) {
+                    tmem_ld32(acc + c, r);
+                    const int at = info.target - q.v0 - (n0 + c);
+                    const int n = row < count ? q.n - (n0 + c) : 0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float v = info.a * ex2(fmaf(r[i], kLog2e, -info.lse2));
+                        if (at == i) v -= info.weight;
+                        r[i] = i < n ? v : 0.0f;  // ignored rows and columns past the vocabulary
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[c / 8 + i] = make_uint4(pack_bf16(r[8 * i], r[8 * i + 1]), pack_bf16(r[8 * i + 2], r[8 * i + 3]),
+                                                    pack_bf16(r[8 * i + 4], r[8 * i + 5]), pack_bf16(r[8 * i + 6], r[8 * i + 7]));
+                }
+            } else if (q.kind == kDH) {
+                const int64_t token = row < count ? p.index[row] : 0;
+                for (int c = 0; c < kTile; c += 32) {
+                    tmem_ld32(acc + c, r);
+                    const int n = row < count ? q.n - (n0 + c) : 0;
+                    if (n <= 0) continue;
+                    float* keep = p.dh_acc + (int64_t)row * p.Kp + n0 + c;
+                    if (!q.first) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < n) r[i] += keep[i];
+                    }
+                    if (q.last) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] *= scale;
+                        store_row(p.dh, token * p.ld_dh + n0 + c, p.dh_f32, false, n, r);
+                    } else {
+                        store_row(keep, 0, true, false, n, r);
+                    }
+                }
+            } else {
+                for (int c = 0; c < kTile; c += 32) {
+                    tmem_ld32(acc + c, r);
+                    const int n = row < q.m ? q.n - (n0 + c) : 0;
+                    if (n <= 0) continue;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = t.k_steps ? r[i] * scale : 0.0f;  // no valid token: no product
+                    store_row(p.dw, (int64_t)(q.v0 + row) * p.ld_dw + n0 + c, p.dw_f32, p.accumulate, n, r);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(buf), leader));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // neither CTA leaves while the other may still use its memory or barriers
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// ------------------------------------------------------------ joining tiles
+// lse and loss of 32 packed rows a CTA: 8 slices of the vocabulary tiles, each
+// in the tiles' order, then the slices.
+__global__ void __launch_bounds__(256) head_join_kernel(const float2* part, int64_t Tp, int tiles, const int* count,
+                                                        const int* index, const float* target_logit, float z,
+                                                        float* loss, float* lse) {
+    __shared__ float2 slice[8][32];
+    griddep_wait();
+    griddep_launch();
+    const int row = blockIdx.x * 32 + (threadIdx.x & 31), j = threadIdx.x >> 5;
+    if (blockIdx.x * 32 >= *count) return;
+    auto join = [](float2& a, float2 b) {
+        const float m = fmaxf(a.x, b.x);
+        const float shift = m == -INFINITY ? 0.0f : m * kLog2e;
+        a.y = a.y * ex2(fmaf(a.x, kLog2e, -shift)) + b.y * ex2(fmaf(b.x, kLog2e, -shift));
+        a.x = m;
+    };
+    float2 a = make_float2(-INFINITY, 0.0f);
+    for (int t = j; t < tiles; t += 8) join(a, part[(int64_t)t * Tp + row]);
+    slice[j][threadIdx.x & 31] = a;
+    __syncthreads();
+    if (j || row >= *count) return;
+    for (int k = 1; k < 8; ++k) join(a, slice[k][threadIdx.x]);
+    const float l = a.x + logf(a.y);
+    const int token = index[row];
+    lse[token] = l;
+    loss[token] = fmaf(z * l, l, l - target_logit[row]);
+}
+
+// ------------------------------------------------------------------- host
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Regions of the workspace, 256-byte aligned.
+struct Plan {
+    int64_t Tp, Kp;          // packed rows and columns
+    int64_t pieces, piece;   // backward: vocabulary pieces and their width (a multiple of kTile)
+    size_t count, index, info, packed, part, target, dl[2], acc, total;
+};
+
+// A piece's dl takes about kPieceBytes: small enough to stay in the 129 MB L2
+// between the kernel that writes it and the ones that read it.
+constexpr int64_t kPieceBytes = 64ll << 20;
+
+Plan make_plan(int64_t T, int64_t V, int64_t K, bool back) {
+    Plan p = {};
+    p.Tp = std::max<int64_t>(up(T, kTile), kTile);
+    p.Kp = up(K, 8);
+    size_t off = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t at = off;
+        off += (size_t)up(bytes, 256);
+        return at;
+    };
+    p.count = take(4);
+    p.index = take(4 * p.Tp);
+    p.info = take((int64_t)sizeof(RowInfo) * p.Tp);
+    p.packed = take(2 * p.Tp * p.Kp);
+    if (back) {
+        const int64_t want = std::max<int64_t>(kTile, kPieceBytes / (2 * p.Tp) / kTile * kTile);
+        p.pieces = (V + want - 1) / want;
+        p.piece = up((V + p.pieces - 1) / p.pieces, kTile);
+        p.pieces = (V + p.piece - 1) / p.piece;
+        p.dl[0] = take(2 * p.Tp * p.piece);
+        p.dl[1] = p.pieces > 1 ? take(2 * p.Tp * p.piece) : p.dl[0];
+        p.acc = p.pieces > 1 ? take(4 * p.Tp * p.Kp) : 0;
+    } else {
+        p.part = take((int64_t)sizeof(float2) * p.Tp * up(V, kTile) / kTile);
+        p.target = take(4 * p.Tp);
+    }
+    p.total = off;
+    return p;
+}
+
+bool bf16_map(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t ld) {
+    return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, (uint64_t)inner, (uint64_t)outer, (uint64_t)ld * 2,
+                         64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Clusters that fit the device at once (per device, from the first launch on it).
+int max_clusters(const cudaLaunchConfig_t& cfg) {
+    static int cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cached[dev] > 0) return cached[dev];
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel, &cfg) != cudaSuccess) return 0;
+    cached[dev] = n;
+    return n;
+}
+
+cudaError_t run_gemm(const HeadMaps& maps, const HeadParams& p, int64_t T, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int most = max_clusters(cfg);
+    if (most <= 0) return cudaErrorLaunchOutOfResources;
+    int64_t tiles = 0;  // with every token valid
+    for (int j = 0; j < p.jobs; ++j) {
+        const Job& q = p.job[j];
+        tiles += up(q.kind == kDW ? q.m : T, kTile) / kTile * (up(q.n, kTile) / kTile);
+    }
+    if (tiles > 0x3FFFFFFF) return cudaErrorNotSupported;
+    cfg.gridDim = dim3(2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, most)));
+    cfg.numAttrs = st ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, head_gemm_kernel, maps, p);
+}
+
+cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, cudaStream_t st) {
+    uint8_t* ws = (uint8_t*)a.workspace;
+    PackParams p = {};
+    p.h = (const __nv_bfloat16*)a.h;
+    p.ldh = a.ldh;
+    p.targets = a.targets;
+    p.T = a.T;
+    p.V = a.V;
+    p.K = a.K;
+    p.Kp = pl.Kp;
+    p.packed = (__nv_bfloat16*)(ws + pl.packed);
+    p.index = (int*)(ws + pl.index);
+    p.info = (RowInfo*)(ws + pl.info);
+    p.count = (int*)(ws + pl.count);
+    p.loss = a.loss;
+    p.lse_out = a.lse;
+    p.lse = a.lse;
+    p.weight = a.weight;
+    p.z = a.z;
+    p.dh = a.dh;
+    p.ld_dh = a.ld_dh;
+    p.dh_f32 = a.dh_f32;
+    p.rows_per_cta = (int)std::max<int64_t>(1, (a.T + 4ll * num_sms - 1) / (4ll * num_sms));
+    const unsigned grid = (unsigned)std::max<int64_t>(1, (a.T + p.rows_per_cta - 1) / p.rows_per_cta);
+    return back ? launch_pdl(head_pack_kernel<true>, dim3(grid), dim3(256), 0, st, p)
+                : launch_pdl(head_pack_kernel<false>, dim3(grid), dim3(256), 0, st, p);
+}
+
+cudaError_t make_maps(const HeadArgs& a, const Plan& pl, bool back, HeadMaps& maps) {
+    uint8_t* ws = (uint8_t*)a.workspace;
+    bool ok = bf16_map(&maps.m[0], ws + pl.packed, a.K, pl.Tp, pl.Kp) && bf16_map(&maps.m[1], a.w, a.K, a.V, a.ldw);
+    maps.m[2] = maps.m[3] = maps.m[0];
+    if (back)
+        ok = ok && bf16_map(&maps.m[2], ws + pl.dl[0], pl.piece, pl.Tp, pl.piece) &&
+             bf16_map(&maps.m[3], ws + pl.dl[1], pl.piece, pl.Tp, pl.piece);
+    return ok ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+HeadParams make_params(const HeadArgs& a, const Plan& pl) {
+    uint8_t* ws = (uint8_t*)a.workspace;
+    HeadParams p = {};
+    p.count = (const int*)(ws + pl.count);
+    p.index = (const int*)(ws + pl.index);
+    p.info = (const RowInfo*)(ws + pl.info);
+    p.part = (float2*)(ws + pl.part);
+    p.target_logit = (float*)(ws + pl.target);
+    p.Tp = pl.Tp;
+    p.dh_acc = (float*)(ws + pl.acc);
+    p.Kp = pl.Kp;
+    p.scale = a.scale;
+    p.dh = a.dh;
+    p.ld_dh = a.ld_dh;
+    p.dh_f32 = a.dh_f32;
+    p.dw = a.dw;
+    p.ld_dw = a.ld_dw;
+    p.dw_f32 = a.dw_f32;
+    p.accumulate = a.accumulate;
+    return p;
+}
+
+}  // namespace
+
+size_t head_loss_bytes(int64_t T, int64_t V, int64_t K) { return make_plan(T, V, K, false).total; }
+size_t head_loss_backward_bytes(int64_t T, int64_t V, int64_t K) { return make_plan(T, V, K, true).total; }
+
+cudaError_t launch_head_loss(const HeadArgs& a, int num_sms, cudaStream_t st) {
+    if (a.T == 0) return cudaSuccess;
+    const Plan pl = make_plan(a.T, a.V, a.K, false);
+    HeadMaps maps;
+    cudaError_t e = make_maps(a, pl, false, maps);
+    if (e == cudaSuccess) e = run_pack(a, pl, false, num_sms, st);
+    if (e != cudaSuccess) return e;
+    HeadParams p = make_params(a, pl);
+    p.jobs = 1;
+    p.job[0].kind = kStats;
+    p.job[0].b_map = 1;
+    p.job[0].n = (int)a.V;
+    p.job[0].k = (int)a.K;
+    e = run_gemm(maps, p, a.T, st);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(head_join_kernel, dim3((unsigned)((a.T + 31) / 32)), dim3(256), 0, st, (const float2*)p.part, pl.Tp,
+                      (int)(up(a.V, kTile) / kTile), p.count, p.index, (const float*)p.target_logit, a.z, a.loss, a.lse);
+}
+
+cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream_t st) {
+    const Plan pl = make_plan(a.T, a.V, a.K, true);
+    uint8_t* ws = (uint8_t*)a.workspace;
+    HeadMaps maps;
+    cudaError_t e = make_maps(a, pl, true, maps);
+    if (e == cudaSuccess) e = run_pack(a, pl, true, num_sms, st);
+    auto width = [&](int64_t i) { return (int)std::min(pl.piece, a.V - i * pl.piece); };
+    for (int64_t i = -1; i < pl.pieces && e == cudaSuccess; ++i) {
+        HeadParams p = make_params(a, pl);
+        if (i >= 0 && a.dh) {  // dH and dW of piece i
+            Job& h = p.job[p.jobs++];
+            h.kind = kDH;
+            h.a_map = 2 + (int)(i & 1);
+            h.b_map = 1;
+            h.b_mn = 1;
+            h.n = (int)a.K;
+            h.k = width(i);
+            h.v0 = (int)(i * pl.piece);
+            h.first = i == 0;
+            h.last = i == pl.pieces - 1;
+        }
+        if (i >= 0 && a.dw) {
+            Job& w = p.job[p.jobs++];
+            w.kind = kDW;
+            w.a_map = 2 + (int)(i & 1);
+            w.b_map = 0;
+            w.a_mn = w.b_mn = 1;
+            w.m = width(i);
+            w.n = (int)a.K;
+            w.v0 = (int)(i * pl.piece);
+        }
+        if (i + 1 < pl.pieces) {  // dl of the next piece
+            Job& g = p.job[p.jobs++];
+            g.kind = kGrad;
+            g.b_map = 1;
+            g.n = width(i + 1);
+            g.k = (int)a.K;
+            g.v0 = (int)((i + 1) * pl.piece);
+            g.dl = (__nv_bfloat16*)(ws + pl.dl[(i + 1) & 1]);
+            g.ld_dl = pl.piece;
+        }
+        if (p.jobs) e = run_gemm(maps, p, a.T, st);
+    }
+    return e;
+}
+
+cudaError_t head_error_read_clear(int* value) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_head_error, sizeof(int));
+    const int zero = 0;
+    if (e == cudaSuccess && *value) e = cudaMemcpyToSymbol(g_head_error, &zero, sizeof(int));
+    return e;
+}
+
+cudaError_t preload_head_kernels() {
+    cudaFuncAttributes at;
+    cudaFuncGetAttributes(&at, head_pack_kernel<false>);
+    cudaFuncGetAttributes(&at, head_pack_kernel<true>);
+    cudaFuncGetAttributes(&at, head_gemm_kernel);
+    return cudaFuncGetAttributes(&at, head_join_kernel);
+}
+
+}  // namespace ufp4

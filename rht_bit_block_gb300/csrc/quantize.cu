@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "train.h"
 #include "quantize_general.cuh"
 
 namespace ufp4 {
@@ -83,13 +84,15 @@ cudaError_t set_quant_wait_limit(uint32_t polls) {
     return e != cudaSuccess ? e : set_rows_wait_limit(polls);
 }
 
-// The first nonzero error word of the three quantizer units (each is cleared).
+// The first nonzero error word of the three quantizer units and the vocabulary
+// head's (each is cleared).
 cudaError_t quant_error_read_clear(int* value) {
-    int v = 0, w = 0, r = 0;
+    int v = 0, w = 0, r = 0, h = 0;
     cudaError_t e = general_error_read_clear(&v);
     if (e == cudaSuccess) e = sr_error_read_clear(&w);
     if (e == cudaSuccess) e = rows_error_read_clear(&r);
-    *value = v ? v : (w ? w : r);
+    if (e == cudaSuccess) e = head_error_read_clear(&h);
+    *value = v ? v : (w ? w : (r ? r : h));
     return e;
 }
 

@@ -24,6 +24,10 @@ GRIDS = {"e1m2": GRID_E1M2, "int4": GRID_INT4, "e2m1": GRID_E2M1, "e2m1r2": GRID
 ROUND_RTNE, ROUND_SR = 0, 1
 SCALE_FP32, SCALE_UE8M0, SCALE_E4M3 = 0, 1, 2
 OUT_ROWWISE, OUT_COLWISE = 1, 2
+BF16, F32 = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
+ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
+CKPT_BLOCK = 32  # elements of a row that share one checkpoint scale
 
 # Every symbol include/ufp4.h declares (checked by the tests).
 EXPORTED = (
@@ -32,7 +36,9 @@ EXPORTED = (
     "ufp4_sign_vector", "ufp4_device_error", "ufp4_status_string", "ufp4_gemm_noalloc",
     "ufp4_gemm_grouped_workspace_size", "ufp4_gemm_grouped", "ufp4_gemm_prepare", "ufp4_gemm_prepared",
     "ufp4_rht_quantize_batch", "ufp4_quant_error_stats", "ufp4_error_stats", "ufp4_set_quantize_wait_limit",
-    "ufp4_rht_quantize_prepare", "ufp4_round_levels",
+    "ufp4_rht_quantize_prepare", "ufp4_round_levels", "ufp4_glu", "ufp4_glu_backward", "ufp4_rms_norm",
+    "ufp4_rms_norm_backward_workspace_size", "ufp4_rms_norm_backward", "ufp4_head_loss_workspace_size",
+    "ufp4_head_loss", "ufp4_head_loss_backward_workspace_size", "ufp4_head_loss_backward",
 )
 MAX_BATCH = 4
 
@@ -94,7 +100,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ufp4_set_quantize_wait_limit.restype = ctypes.c_int
     L.ufp4_status_string.argtypes = [ctypes.c_int]
     L.ufp4_status_string.restype = ctypes.c_char_p
-    for name in ("ufp4_rht_quantize", "ufp4_rht_quantize_grouped", "ufp4_rht_transform", "ufp4_dequantize",
+    SZ, f32 = ctypes.c_size_t, ctypes.c_float
+    L.ufp4_glu.argtypes = [P, i64, P, i64, i32, i64, i64, i32, P, i64, QT, QT, P]
+    L.ufp4_glu_backward.argtypes = [P, i64, i32, QT, QT, i64, i64, i32, P, i64, P, i64, P, i64, P]
+    L.ufp4_rms_norm.argtypes = [P, i64, i32, P, i64, P, i32, i64, i64, f32, P, i64, P, i64, P, QT, P]
+    L.ufp4_rms_norm_backward_workspace_size.argtypes = [i64, i64, ctypes.POINTER(SZ)]
+    L.ufp4_rms_norm_backward.argtypes = [P, i64, i32, QT, P, P, i32, P, i64, i64, i64, P, i64, P, P, i64, P, SZ, P]
+    L.ufp4_head_loss_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(SZ)]
+    L.ufp4_head_loss.argtypes = [P, i64, P, i64, P, i64, i64, i64, f32, P, P, P, SZ, P]
+    L.ufp4_head_loss_backward_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(SZ)]
+    L.ufp4_head_loss_backward.argtypes = [P, i64, P, i64, P, i64, i64, i64, f32, P, P, P, P, i64, i32, P, i64, i32, i32,
+                                          P, SZ, P]
+    for name in ("ufp4_glu", "ufp4_glu_backward", "ufp4_rms_norm", "ufp4_rms_norm_backward_workspace_size",
+                 "ufp4_rms_norm_backward", "ufp4_head_loss_workspace_size", "ufp4_head_loss",
+                 "ufp4_head_loss_backward_workspace_size", "ufp4_head_loss_backward",
+                 "ufp4_rht_quantize", "ufp4_rht_quantize_grouped", "ufp4_rht_transform", "ufp4_dequantize",
                  "ufp4_gemm_workspace_size", "ufp4_gemm", "ufp4_sign_vector", "ufp4_device_error",
                  "ufp4_gemm_noalloc", "ufp4_gemm_grouped_workspace_size", "ufp4_gemm_grouped",
                  "ufp4_gemm_prepare", "ufp4_gemm_prepared", "ufp4_rht_quantize_prepare", "ufp4_round_levels"):
@@ -296,7 +316,150 @@ def ufp4_status_string(status: int) -> str:
     return load().ufp4_status_string(status).decode()
 
 
+# ------------------------------------------- the training step between the GEMMs
+def _dtype(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise TypeError(f"{what} is {t.dtype}: bfloat16 or float32 is wanted")
+
+
+def _matrix(t, what: str, rows: int, cols: int, dtype=None):
+    """(pointer, leading dimension) of a 2-D tensor with unit column stride; (None, 0) of None."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}: ({rows}, {cols}) is wanted")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}'s rows are not contiguous")
+    if dtype is not None and _dtype(t, what) != dtype:
+        raise TypeError(f"{what} is {t.dtype}")
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _vector(t, what: str, n: int, dtype: str):
+    """Pointer of a contiguous 1-D tensor of n elements; None of None."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} is not {n} contiguous elements")
+    if str(t.dtype) != "torch." + dtype:
+        raise TypeError(f"{what} is {t.dtype}: {dtype} is wanted")
+    return t.data_ptr()
+
+
+def _ref(q: QTensor | None):
+    return ctypes.byref(q) if q is not None else None
+
+
+def _act(act) -> int:
+    return ACTS[act] if isinstance(act, str) else int(act)
+
+
+def ufp4_glu(gate, up, y, act="silu", ckpt_gate: QTensor | None = None, ckpt_up: QTensor | None = None, stream=None):
+    """y = act(gate) * up; the 8-bit checkpoints of gate and up are written if both are given."""
+    rows, cols = gate.shape
+    dt = _dtype(gate, "gate")
+    _check(load().ufp4_glu(*_matrix(gate, "gate", rows, cols), *_matrix(up, "up", rows, cols, dt), dt, rows, cols,
+                           _act(act), *_matrix(y, "y", rows, cols, BF16), _ref(ckpt_gate), _ref(ckpt_up),
+                           _stream(stream)), "ufp4_glu")
+
+
+def ufp4_glu_backward(dy, ckpt_gate: QTensor, ckpt_up: QTensor, dgate, dup, act="silu", y=None, stream=None):
+    """dgate and dup of ufp4_glu at the checkpointed values, and act(gate) * up again into y if given."""
+    rows, cols = dy.shape
+    _check(load().ufp4_glu_backward(*_matrix(dy, "dy", rows, cols), _dtype(dy, "dy"), _ref(ckpt_gate), _ref(ckpt_up),
+                                    rows, cols, _act(act), *_matrix(dgate, "dgate", rows, cols, BF16),
+                                    *_matrix(dup, "dup", rows, cols, BF16), *_matrix(y, "y", rows, cols, BF16),
+                                    _stream(stream)), "ufp4_glu_backward")
+
+
+def ufp4_rms_norm(x, gamma, y, rstd=None, residual=None, total=None, ckpt: QTensor | None = None, eps=1e-6,
+                  stream=None):
+    """y = RMS norm of x + residual times gamma; total (the bf16 sum), rstd and the 8-bit checkpoint of the sum are
+    written if given."""
+    rows, cols = x.shape
+    dt = _dtype(gamma, "gamma")
+    _check(load().ufp4_rms_norm(*_matrix(x, "x", rows, cols), _dtype(x, "x"),
+                                *_matrix(residual, "residual", rows, cols, BF16),
+                                _vector(gamma, "gamma", cols, "float32" if dt == F32 else "bfloat16"), dt, rows, cols,
+                                eps, *_matrix(y, "y", rows, cols, BF16), *_matrix(total, "total", rows, cols, BF16),
+                                _vector(rstd, "rstd", rows, "float32"), _ref(ckpt), _stream(stream)), "ufp4_rms_norm")
+
+
+def ufp4_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ufp4_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(out)),
+           "ufp4_rms_norm_backward_workspace_size")
+    return int(out.value)
+
+
+def ufp4_rms_norm_backward(dy, ckpt: QTensor, rstd, gamma, dx, dgamma, workspace, dtotal=None, y=None, stream=None):
+    """dx and dgamma of ufp4_rms_norm at the checkpointed rows, dtotal added to dx if given, and the normalised rows
+    again into y if given."""
+    rows, cols = dy.shape
+    dt = _dtype(gamma, "gamma")
+    _check(load().ufp4_rms_norm_backward(*_matrix(dy, "dy", rows, cols), _dtype(dy, "dy"), _ref(ckpt),
+                                         _vector(rstd, "rstd", rows, "float32"),
+                                         _vector(gamma, "gamma", cols, "float32" if dt == F32 else "bfloat16"), dt,
+                                         *_matrix(dtotal, "dtotal", rows, cols, BF16), rows, cols,
+                                         *_matrix(dx, "dx", rows, cols, BF16), _vector(dgamma, "dgamma", cols, "float32"),
+                                         *_matrix(y, "y", rows, cols, BF16), workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)),
+           "ufp4_rms_norm_backward")
+
+
+def ufp4_head_loss_workspace_size(tokens: int, vocab: int, hidden: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ufp4_head_loss_workspace_size(tokens, vocab, hidden, ctypes.byref(out)),
+           "ufp4_head_loss_workspace_size")
+    return int(out.value)
+
+
+def ufp4_head_loss_backward_workspace_size(tokens: int, vocab: int, hidden: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ufp4_head_loss_backward_workspace_size(tokens, vocab, hidden, ctypes.byref(out)),
+           "ufp4_head_loss_backward_workspace_size")
+    return int(out.value)
+
+
+def ufp4_head_loss(h, w, targets, loss, lse, workspace, z_loss=0.0, stream=None):
+    """Per-token cross entropy (plus z_loss * lse^2) and log-sum-exp of the logits h w^T, which are not stored.
+    targets: int64; a target outside [0, vocab) gives loss and lse 0."""
+    tokens, hidden = h.shape
+    vocab = w.shape[0]
+    _check(load().ufp4_head_loss(*_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
+                                 _vector(targets, "targets", tokens, "int64"), tokens, vocab, hidden, z_loss,
+                                 _vector(loss, "loss", tokens, "float32"), _vector(lse, "lse", tokens, "float32"),
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
+           "ufp4_head_loss")
+
+
+def ufp4_head_loss_backward(h, w, targets, lse, dh, dw, workspace, token_weight=None, scale=None, z_loss=0.0,
+                            accumulate_dw=False, stream=None):
+    """dh and dw of scale * sum(token_weight * loss); either may be None.  dw is added to with accumulate_dw (float32)."""
+    tokens, hidden = h.shape
+    vocab = w.shape[0]
+    _check(load().ufp4_head_loss_backward(
+        *_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
+        _vector(targets, "targets", tokens, "int64"), tokens, vocab, hidden, z_loss,
+        _vector(lse, "lse", tokens, "float32"), _vector(token_weight, "token_weight", tokens, "float32"),
+        _vector(scale, "scale", 1, "float32"), *_matrix(dh, "dh", tokens, hidden),
+        BF16 if dh is None else _dtype(dh, "dh"), *_matrix(dw, "dw", vocab, hidden),
+        BF16 if dw is None else _dtype(dw, "dw"), int(accumulate_dw), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "ufp4_head_loss_backward")
+
+
 # ------------------------------------------------------------- conveniences
+def alloc_checkpoint(rows: int, cols: int, device):
+    """torch buffers (codes, scales) of one 8-bit checkpoint; describe them with qtensor(codes, scales, rows, cols)."""
+    import torch
+    codes = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+    return codes, torch.empty((rows, (cols + CKPT_BLOCK - 1) // CKPT_BLOCK), dtype=torch.uint8, device=device)
+
+
 def alloc_quantized(rows: int, cols: int, desc: QuantDesc, device):
     """torch buffers for one quantized matrix (rows x cols in its own layout)."""
     import torch
