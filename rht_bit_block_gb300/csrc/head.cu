@@ -45,23 +45,40 @@ __device__ int g_head_error;
 
 namespace {
 
-constexpr int kTile = 256;                 // output tile of a CTA pair, both ways
-constexpr int kHalf = 128;                 // rows of A and of B that one CTA holds
-constexpr int kStep = 64;                  // summed elements per stage (one 128-byte swizzle row)
-constexpr int kBoxBytes = 64 * 64 * 2;     // one TMA box: 64 rows of 64 bf16
-constexpr int kOperand = 2 * kBoxBytes;    // one operand of one stage
-constexpr int kStages = 6;
+constexpr int kTile = 256;                 // output columns of a tile, and rows of a CTA pair's tile
+constexpr int kHalf = 128;                 // rows of A that one CTA holds
+constexpr int kStep = 64;                  // summed elements per step (one 128-byte swizzle row)
+constexpr int kBlockBytes = 64 * 64 * 2;   // 64 rows of 64 bf16: one column block of an MN-major operand
+constexpr int kAtom = 2 * kBlockBytes;     // 128 rows of one step
 constexpr int kThreads = 256;
+constexpr int kRing = 3;                   // tiles handed out ahead
 constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sleep up to kSuspendNs
 constexpr uint32_t kSuspendNs = 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kOffA = 0;
-constexpr int kOffB = kStages * kOperand;
-constexpr int kOffBars = 2 * kStages * kOperand;
-constexpr int kNumBars = 2 * kStages + 4 + 1;
-constexpr int kSmem = kOffBars + 8 * kNumBars + 16 + 1024;
-static_assert(kSmem <= 232448, "shared memory overflow");
+// A CTA pair's 256 x 256 tile, or a single CTA's 128 x 256 tile.  A pair
+// holds 128 rows of A and half the rows of B per CTA, so it moves two thirds
+// of the single CTA's bytes per product; its stages hold two steps, which
+// halves the hand-offs between the copies and the tensor core (one-step
+// stages: 4096 x 16384 x 2048 logits 193 us, two-step stages 174 us).
+template <bool PAIR>
+struct Cfg {
+    static constexpr int kRows = PAIR ? kTile : kHalf;   // rows of a tile
+    static constexpr int kKps = PAIR ? 2 : 1;            // steps per stage
+    static constexpr int kStages = PAIR ? 3 : 4;
+    static constexpr int kBRows = PAIR ? kHalf : kTile;  // rows of B per CTA
+    static constexpr int kAtomB = kBRows * 128;
+    static constexpr int kA = kKps * kAtom, kB = kKps * kAtomB;
+    static constexpr int kOffA = 0;
+    static constexpr int kOffB = kStages * kA;
+    static constexpr int kOffBars = kOffB + kStages * kB;
+    // full, empty; accumulators full x2, empty x2; ring full, empty; drain
+    static constexpr int kNumBars = 2 * kStages + 4 + 2 * kRing + 1;
+    static constexpr int kOffWords = kOffBars + 8 * kNumBars;  // tensor memory address, abort flag, ring of tiles
+    static constexpr int kSmem = kOffWords + 4 * (2 + kRing) + 1024;
+    static constexpr int kTx = (PAIR ? 2 : 1) * (kAtom + kAtomB);  // bytes of one step, counted by the leader
+    static_assert(kSmem <= 232448, "shared memory overflow");
+};
 
 // ------------------------------------------------------------ PTX wrappers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -86,6 +103,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     atomicExch(&g_head_error, 1);
     return false;
 }
+// The same for what a thread of either CTA of the pair wrote before it arrived.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;"
+            " selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (ok) return true;
+    }
+    atomicExch(&g_head_error, 1);
+    return false;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -102,13 +134,23 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
+__device__ __forceinline__ void st_cluster(uint32_t caddr, int v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
+}
 // TMA box into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t cbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(cbar)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(cbar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(cbar)
+            : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -117,29 +159,64 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // (stride offset); MN-major operands also have their 64-element column blocks
 // one box apart (leading offset; unused K-major, where a stage is one column).
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(kBoxBytes >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(kBlockBytes >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // kind::f16: fp32 accumulator, bf16 operands, MN-major A (bit 15) and B (bit 16), N >> 3, M >> 4.
-__host__ __device__ constexpr uint32_t make_idesc(bool a_mn, bool b_mn) {
+__host__ __device__ constexpr uint32_t make_idesc(int rows, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(rows >> 4) << 24);
 }
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }"
-        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if (PAIR)
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }"
+            ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+            ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
-__device__ __forceinline__ void tc_commit_both(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
+// Arrives on the barrier once this thread's MMAs so far are done: in both CTAs of a pair ...
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// ... or in this CTA alone.
+template <bool PAIR>
 __device__ __forceinline__ void tc_commit_local(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot) {
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t tmem) {
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float r[32]) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
@@ -182,6 +259,8 @@ struct PackParams {
     int* index;               // packed row -> token
     RowInfo* info;
     int* count;
+    int* next;                // tile counters of the launches that follow, zeroed
+    int launches;
     float* loss;              // forward: 0 for ignored tokens
     float* lse_out;
     const float* lse;         // backward
@@ -219,7 +298,10 @@ __global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
     }
     __syncthreads();
     const int count = all_s;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = count;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *p.count = count;
+        for (int i = threadIdx.x; i < p.launches; i += blockDim.x) p.next[i] = 0;
+    }
     auto clear_row = [&](char* row, int64_t bytes) {  // 2-byte multiples, 2-byte aligned at least
         for (int64_t i = threadIdx.x; i < bytes / 2; i += blockDim.x) reinterpret_cast<uint16_t*>(row)[i] = 0;
     };
@@ -274,7 +356,7 @@ enum JobKind { kStats = 0, kGrad = 1, kDH = 2, kDW = 3 };
 //   kDW     dl^T times the packed rows of H -> rows of dW
 struct Job {
     int kind;
-    int a_map, b_map;       // tensor maps
+    int a, b;               // operands (Operand)
     int a_mn, b_mn;         // the operand's contiguous index is not the summed one
     int m, n, k;            // extents; kernel-side: m (or k for kDW) comes from the token count
     int v0;                 // first vocabulary row of the piece
@@ -283,14 +365,17 @@ struct Job {
     int64_t ld_dl;
 };
 constexpr int kMaxJobs = 3;
-constexpr int kMaps = 4;    // packed H, W, two pieces of dl
+enum Operand { kOpH = 0, kOpW = 1, kOpDl = 2, kOperands = 4 };  // packed H, W, two pieces of dl
+// Each operand's tensor map with boxes of 128 rows (K-major: a CTA's half of
+// a tile) and of 64 rows (MN-major: one column block).
 struct HeadMaps {
-    CUtensorMap m[kMaps];
+    CUtensorMap m[kOperands][2];
 };
 struct HeadParams {
     Job job[kMaxJobs];
     int jobs;
     const int* count;
+    int* next;              // tiles handed out beyond one per cluster
     const int* index;
     const RowInfo* info;
     float2* part;           // kStats: [vocabulary tile][packed row]
@@ -315,6 +400,7 @@ struct TileAt {
 // share a few panels of either operand, which stay in L2.
 constexpr int kGroupM = 8;
 
+template <int ROWS>
 struct Walk {
     int m_tiles[kMaxJobs], n_tiles[kMaxJobs], k_steps[kMaxJobs], total;
     __device__ __forceinline__ Walk(const HeadParams& p, int count) {
@@ -324,7 +410,7 @@ struct Walk {
             if (j >= p.jobs) continue;
             const Job& q = p.job[j];
             const int m = q.kind == kDW ? q.m : count, k = q.kind == kDW ? count : q.k;
-            m_tiles[j] = (m + kTile - 1) / kTile;
+            m_tiles[j] = (m + ROWS - 1) / ROWS;
             n_tiles[j] = (q.n + kTile - 1) / kTile;
             k_steps[j] = (k + kStep - 1) / kStep;
             total += m_tiles[j] * n_tiles[j];
@@ -406,92 +492,136 @@ __device__ __forceinline__ void stats_chunk(float r[32], int n, float& m, float&
     m = top;
 }
 
+// Warps 0 and 2 copy A and B (one thread each: a single thread issuing both is
+// 5 % slower), warp 1 of the leader issues the MMAs, warp 3 of the leader hands
+// out tiles, warps 4 to 7 run the epilogue.  Tiles differ in length by an order
+// of magnitude between products, so clusters take the next one from a counter
+// in global memory when they have room for it; which cluster computes a tile
+// changes nothing in its result.
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p) {
+    using C = Cfg<PAIR>;
+    constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
-    const uint32_t bars = base + kOffBars;
+    const uint32_t bars = base + C::kOffBars;
     auto full_bar = [&](int s) { return bars + 8u * s; };
-    auto empty_bar = [&](int s) { return bars + 8u * (kStages + s); };
-    auto accf_bar = [&](int b) { return bars + 8u * (2 * kStages + b); };
-    auto acce_bar = [&](int b) { return bars + 8u * (2 * kStages + 2 + b); };
-    const uint32_t drain_bar = bars + 8u * (2 * kStages + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kOffBars + 8 * kNumBars);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + kOffBars + 8 * kNumBars + 4);
+    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto accf_bar = [&](int b) { return bars + 8u * (2 * S + b); };
+    auto acce_bar = [&](int b) { return bars + 8u * (2 * S + 2 + b); };
+    auto ringf_bar = [&](int i) { return bars + 8u * (2 * S + 4 + i); };
+    auto ringe_bar = [&](int i) { return bars + 8u * (2 * S + 4 + kRing + i); };
+    const uint32_t drain_bar = bars + 8u * (2 * S + 4 + 2 * kRing);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffWords);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffWords + 4);
+    volatile int* ring = reinterpret_cast<volatile int*>(gbase + C::kOffWords + 8);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
     const int peer = (int)(rank & 1u);      // 0: leader (even CTA)
     const uint32_t leader = rank & ~1u;
-    const int cluster_id = blockIdx.x >> 1;
-    const int num_clusters = gridDim.x >> 1;
+    const int cluster_id = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    const int num_clusters = PAIR ? gridDim.x >> 1 : gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);   // the leader's expect_tx arrival (both CTAs' bytes)
             mbar_init(empty_bar(s), 1);  // the leader's commit
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(accf_bar(b), 1);   // the leader's commit
-            mbar_init(acce_bar(b), 8);   // four epilogue warps of each CTA
+            mbar_init(accf_bar(b), 1);             // the leader's commit
+            mbar_init(acce_bar(b), PAIR ? 8 : 4);  // the epilogue warps
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(ringf_bar(i), 1);               // the leader's warp 3
+            mbar_init(ringe_bar(i), PAIR ? 13 : 7);   // two copiers and four epilogue warps a CTA, the MMA issuer
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(512));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    }
+    if (warp == 1) tmem_alloc<PAIR>(smem_u32(tmem_slot));
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // both CTAs' barriers exist before any copy or commit targets them
+    if (PAIR) cluster_sync_all();  // both CTAs' barriers exist before any copy or commit targets them
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
     griddep_launch();
 
     const int count = *p.count;
-    const Walk walk(p, count);
+    const Walk<C::kRows> walk(p, count);
 
-    if (warp == 0 && lane == 0) {
-        // ---------------------------------------------------- TMA producer (both CTAs)
+    // The tile number i of this cluster, or -1 when there is none (or a wait gave up).  `arrive`: this
+    // thread speaks for its reader (a copier, the issuer, an epilogue warp).
+    auto take = [&](int i, bool arrive) {
+        const int at = i % kRing;
+        if (!mbar_wait_cluster(ringf_bar(at), (i / kRing) & 1)) {
+            *abort_flag = 1;
+            return -1;
+        }
+        const int tile = ring[at];
+        if (arrive) mbar_arrive_cluster(map_to_rank(ringe_bar(at), leader));
+        return tile < walk.total ? tile : -1;
+    };
+
+    if (warp == 3 && lane == 0 && peer == 0) {
+        // ------------------------------------------------ hands out tiles (leader only)
+        for (int i = 0;; ++i) {
+            const int at = i % kRing;
+            if (!mbar_wait_cluster(ringe_bar(at), ((i / kRing) & 1) ^ 1)) {
+                *abort_flag = 1;
+                break;
+            }
+            const int tile = i == 0 ? cluster_id : num_clusters + atomicAdd(p.next, 1);
+            const uint32_t slot = smem_u32(const_cast<int*>(ring + at));
+            for (uint32_t r = leader; r <= leader + (PAIR ? 1 : 0); ++r) {
+                st_cluster(map_to_rank(slot, r), tile);
+                mbar_arrive_cluster(map_to_rank(ringf_bar(at), r));
+            }
+            if (tile >= walk.total || *abort_flag) break;
+        }
+    } else if ((warp == 0 || warp == 2) && lane == 0) {
+        // ---------------------------------------------------- TMA copies (both CTAs)
+        const bool is_a = warp == 0;
         int s = 0;
         uint32_t ph = 0;
-        for (int tile = cluster_id; tile < walk.total && !*abort_flag; tile += num_clusters) {
+        for (int i = 0;; ++i) {
+            const int tile = take(i, true);
+            if (tile < 0 || *abort_flag) break;
             const TileAt t = walk.at(tile);
             const Job& q = p.job[t.job];
-            const CUtensorMap* am = &maps.m[q.a_map];
-            const CUtensorMap* bm = &maps.m[q.b_map];
+            const bool mn = is_a ? q.a_mn : q.b_mn;
+            const CUtensorMap* map = &maps.m[is_a ? q.a : q.b][mn];
             // W's rows are the whole vocabulary, a piece starts at v0; dl's columns are the piece's own
-            const int a0 = t.m * kTile + peer * kHalf;
-            const int b0 = t.n * kTile + peer * kHalf + (q.b_mn ? 0 : q.v0);
-            const int kb = q.kind == kDH ? q.v0 : 0;  // first summed row of B
-            for (int ks = 0; ks < t.k_steps; ++ks) {
+            const int r0 = is_a ? t.m * C::kRows + peer * kHalf
+                                : t.n * kTile + peer * C::kBRows + (q.b_mn ? 0 : q.v0);
+            const int kb = !is_a && q.kind == kDH ? q.v0 : 0;  // first summed row of W
+            for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
                 if (!mbar_wait(empty_bar(s), ph ^ 1u)) {
                     *abort_flag = 1;
                     break;
                 }
-                const uint32_t fb = map_to_rank(full_bar(s), leader);
-                if (peer == 0) mbar_expect_tx(full_bar(s), 4 * kOperand);
-                const uint32_t sa = base + kOffA + s * kOperand, sb = base + kOffB + s * kOperand;
-                const int k = ks * kStep;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (q.a_mn)
-                        tma_load(sa + j * kBoxBytes, am, a0 + 64 * j, k, fb);
-                    else
-                        tma_load(sa + j * kBoxBytes, am, k, a0 + 64 * j, fb);
-                    if (q.b_mn)
-                        tma_load(sb + j * kBoxBytes, bm, b0 + 64 * j, kb + k, fb);
-                    else
-                        tma_load(sb + j * kBoxBytes, bm, k, b0 + 64 * j, fb);
+                const int nk = min(C::kKps, t.k_steps - ks);
+                const uint32_t fb = PAIR ? map_to_rank(full_bar(s), leader) : full_bar(s);
+                if (is_a && peer == 0) mbar_expect_tx(full_bar(s), nk * C::kTx);
+                for (int j = 0; j < nk; ++j) {
+                    const uint32_t dst =
+                        is_a ? base + C::kOffA + s * C::kA + j * kAtom : base + C::kOffB + s * C::kB + j * C::kAtomB;
+                    const int k = kb + (ks + j) * kStep;
+                    if (mn) {
+                        tma_load<PAIR>(dst, map, r0, k, fb);
+                        tma_load<PAIR>(dst + kBlockBytes, map, r0 + 64, k, fb);
+                    } else {
+                        tma_load<PAIR>(dst, map, k, r0, fb);
+                        if (!PAIR && !is_a) tma_load<PAIR>(dst + kAtom, map, k, r0 + kHalf, fb);
+                    }
                 }
-                if (++s == kStages) {
+                if (++s == S) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -499,10 +629,12 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         }
     } else if (warp == 1 && lane == 0 && peer == 0) {
         // ------------------------------------------------ MMA issuer (leader only)
-        int s = 0, tc = 0;
+        int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int tile = cluster_id; tile < walk.total && ok; tile += num_clusters, ++tc) {
+        for (int tc = 0; ok; ++tc) {
+            const int tile = take(tc, true);
+            if (tile < 0) break;
             const TileAt t = walk.at(tile);
             const Job& q = p.job[t.job];
             const int buf = tc & 1;
@@ -512,44 +644,50 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             }
             tc_fence_after();
             const uint32_t acc = tmem + buf * kTile;
-            const uint32_t idesc = make_idesc(q.a_mn, q.b_mn);
+            const uint32_t idesc = make_idesc(C::kRows, q.a_mn, q.b_mn);
             // 16 summed elements: 32 bytes along a swizzle row, or 16 rows of 128 bytes
             const int astep = q.a_mn ? 2048 >> 4 : 32 >> 4, bstep = q.b_mn ? 2048 >> 4 : 32 >> 4;
-            for (int ks = 0; ks < t.k_steps; ++ks) {
-                if (!mbar_wait(full_bar(s), ph) || *abort_flag) {
+            for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
+                if (!mbar_wait(full_bar(s), ph)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t da = sw128_desc(base + kOffA + s * kOperand);
-                const uint64_t db = sw128_desc(base + kOffB + s * kOperand);
+                const int nk = min(C::kKps, t.k_steps - ks);
+                for (int j = 0; j < nk; ++j) {
+                    const uint64_t da = sw128_desc(base + C::kOffA + s * C::kA + j * kAtom);
+                    const uint64_t db = sw128_desc(base + C::kOffB + s * C::kB + j * C::kAtomB);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_pair(acc, da + i * astep, db + i * bstep, idesc, (ks > 0 || i > 0) ? 1u : 0u);
-                tc_commit_both(empty_bar(s));  // frees stage s in both CTAs
-                if (++s == kStages) {
+                    for (int i = 0; i < 4; ++i)
+                        mma<PAIR>(acc, da + i * astep, db + i * bstep, idesc, (ks + j > 0 || i > 0) ? 1u : 0u);
+                }
+                tc_commit<PAIR>(empty_bar(s));  // frees stage s in both CTAs
+                if (++s == S) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
-            if (ok) tc_commit_both(accf_bar(buf));
+            if (ok) tc_commit<PAIR>(accf_bar(buf));
         }
         if (!ok) *abort_flag = 1;
-        tc_commit_local(drain_bar);
+        tc_commit_local<PAIR>(drain_bar);
         mbar_wait(drain_bar, 0);
     } else if (warp >= 4) {
         // ------------------------------------------------- epilogue (both CTAs)
         const int q4 = warp - 4;
         const float scale = p.scale ? *p.scale : 1.0f;
-        int tc = 0;
-        for (int tile = cluster_id; tile < walk.total; tile += num_clusters, ++tc) {
+        for (int tc = 0;; ++tc) {
+            const int tile = take(tc, false);  // every lane reads the tile, then one arrives
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(ringe_bar(tc % kRing), leader));
             const int buf = tc & 1;
+            if (__any_sync(0xFFFFFFFFu, tile < 0)) break;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(accf_bar(buf), (tc >> 1) & 1));
             if (!ok || *abort_flag) break;
             tc_fence_after();
             const TileAt t = walk.at(tile);
             const Job& q = p.job[t.job];
-            const int row = t.m * kTile + peer * kHalf + q4 * 32 + lane;
+            const int row = t.m * C::kRows + peer * kHalf + q4 * 32 + lane;
             const int n0 = t.n * kTile;
             const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + buf * kTile;
             float r[32];
@@ -626,10 +764,10 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();  // neither CTA leaves while the other may still use its memory or barriers
+    if (PAIR) cluster_sync_all();  // neither CTA leaves while the other may still use its memory or barriers
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        tmem_free<PAIR>(tmem);
     }
 }
 
@@ -669,12 +807,16 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 struct Plan {
     int64_t Tp, Kp;          // packed rows and columns
     int64_t pieces, piece;   // backward: vocabulary pieces and their width (a multiple of kTile)
-    size_t count, index, info, packed, part, target, dl[2], acc, total;
+    int64_t launches;        // of the product kernel
+    size_t count, next, index, info, packed, part, target, dl[2], acc, total;
 };
 
-// A piece's dl takes about kPieceBytes: small enough to stay in the 129 MB L2
-// between the kernel that writes it and the ones that read it.
-constexpr int64_t kPieceBytes = 64ll << 20;
+// A piece's dl takes about kPieceBytes.  Wider pieces mean fewer launches,
+// longer sums and fewer passes over the fp32 dH; narrower ones a smaller
+// workspace, and below 129 MB a dl that L2 holds, which measures no faster:
+// loss + gradients of 4096 x 65536 x 7168 take 8.9, 8.7 and 8.65 ms with 64,
+// 128 and 256 MB, of 2047 x 50001 x 2048 (a third ignored) 887, 815 and 780 us.
+constexpr int64_t kPieceBytes = 256ll << 20;
 
 Plan make_plan(int64_t T, int64_t V, int64_t K, bool back) {
     Plan p = {};
@@ -686,15 +828,19 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back) {
         off += (size_t)up(bytes, 256);
         return at;
     };
-    p.count = take(4);
-    p.index = take(4 * p.Tp);
-    p.info = take((int64_t)sizeof(RowInfo) * p.Tp);
-    p.packed = take(2 * p.Tp * p.Kp);
     if (back) {
         const int64_t want = std::max<int64_t>(kTile, kPieceBytes / (2 * p.Tp) / kTile * kTile);
         p.pieces = (V + want - 1) / want;
         p.piece = up((V + p.pieces - 1) / p.pieces, kTile);
         p.pieces = (V + p.piece - 1) / p.piece;
+    }
+    p.launches = p.pieces + 1;
+    p.count = take(4);
+    p.next = take(4 * p.launches);
+    p.index = take(4 * p.Tp);
+    p.info = take((int64_t)sizeof(RowInfo) * p.Tp);
+    p.packed = take(2 * p.Tp * p.Kp);
+    if (back) {
         p.dl[0] = take(2 * p.Tp * p.piece);
         p.dl[1] = p.pieces > 1 ? take(2 * p.Tp * p.piece) : p.dl[0];
         p.acc = p.pieces > 1 ? take(4 * p.Tp * p.Kp) : 0;
@@ -706,51 +852,57 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back) {
     return p;
 }
 
-bool bf16_map(CUtensorMap* map, const void* ptr, int64_t inner, int64_t outer, int64_t ld) {
-    return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, (uint64_t)inner, (uint64_t)outer, (uint64_t)ld * 2,
-                         64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+bool bf16_maps(CUtensorMap map[2], const void* ptr, int64_t inner, int64_t outer, int64_t ld) {
+    return encode_map_2d(&map[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, (uint64_t)inner, (uint64_t)outer,
+                         (uint64_t)ld * 2, 64, kHalf, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode_map_2d(&map[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, (uint64_t)inner, (uint64_t)outer,
+                         (uint64_t)ld * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Clusters that fit the device at once (per device, from the first launch on it).
+template <bool PAIR>
 int max_clusters(const cudaLaunchConfig_t& cfg) {
     static int cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     if (cached[dev] > 0) return cached[dev];
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel<PAIR>, &cfg) != cudaSuccess) return 0;
     cached[dev] = n;
     return n;
 }
 
+template <bool PAIR>
 cudaError_t run_gemm(const HeadMaps& maps, const HeadParams& p, int64_t T, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    using C = Cfg<PAIR>;
+    cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    constexpr unsigned ctas = PAIR ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int most = max_clusters(cfg);
+    const int most = max_clusters<PAIR>(cfg);
     if (most <= 0) return cudaErrorLaunchOutOfResources;
     int64_t tiles = 0;  // with every token valid
     for (int j = 0; j < p.jobs; ++j) {
         const Job& q = p.job[j];
-        tiles += up(q.kind == kDW ? q.m : T, kTile) / kTile * (up(q.n, kTile) / kTile);
+        tiles += up(q.kind == kDW ? q.m : T, C::kRows) / C::kRows * (up(q.n, kTile) / kTile);
     }
     if (tiles > 0x3FFFFFFF) return cudaErrorNotSupported;
-    cfg.gridDim = dim3(2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, most)));
+    cfg.gridDim = dim3(ctas * (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, most)));
     cfg.numAttrs = st ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, head_gemm_kernel, maps, p);
+    return cudaLaunchKernelEx(&cfg, head_gemm_kernel<PAIR>, maps, p);
 }
 
 cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, cudaStream_t st) {
@@ -767,6 +919,8 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
     p.index = (int*)(ws + pl.index);
     p.info = (RowInfo*)(ws + pl.info);
     p.count = (int*)(ws + pl.count);
+    p.next = (int*)(ws + pl.next);
+    p.launches = (int)pl.launches;
     p.loss = a.loss;
     p.lse_out = a.lse;
     p.lse = a.lse;
@@ -783,11 +937,13 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
 
 cudaError_t make_maps(const HeadArgs& a, const Plan& pl, bool back, HeadMaps& maps) {
     uint8_t* ws = (uint8_t*)a.workspace;
-    bool ok = bf16_map(&maps.m[0], ws + pl.packed, a.K, pl.Tp, pl.Kp) && bf16_map(&maps.m[1], a.w, a.K, a.V, a.ldw);
-    maps.m[2] = maps.m[3] = maps.m[0];
-    if (back)
-        ok = ok && bf16_map(&maps.m[2], ws + pl.dl[0], pl.piece, pl.Tp, pl.piece) &&
-             bf16_map(&maps.m[3], ws + pl.dl[1], pl.piece, pl.Tp, pl.piece);
+    bool ok = bf16_maps(maps.m[kOpH], ws + pl.packed, a.K, pl.Tp, pl.Kp) && bf16_maps(maps.m[kOpW], a.w, a.K, a.V, a.ldw);
+    for (int i = 0; i < 2; ++i) {
+        if (back)
+            ok = ok && bf16_maps(maps.m[kOpDl + i], ws + pl.dl[i], pl.piece, pl.Tp, pl.piece);
+        else
+            maps.m[kOpDl + i][0] = maps.m[kOpDl + i][1] = maps.m[kOpH][0];  // not used
+    }
     return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -795,6 +951,7 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
     uint8_t* ws = (uint8_t*)a.workspace;
     HeadParams p = {};
     p.count = (const int*)(ws + pl.count);
+    p.next = (int*)(ws + pl.next);
     p.index = (const int*)(ws + pl.index);
     p.info = (const RowInfo*)(ws + pl.info);
     p.part = (float2*)(ws + pl.part);
@@ -828,10 +985,13 @@ cudaError_t launch_head_loss(const HeadArgs& a, int num_sms, cudaStream_t st) {
     HeadParams p = make_params(a, pl);
     p.jobs = 1;
     p.job[0].kind = kStats;
-    p.job[0].b_map = 1;
+    p.job[0].a = kOpH;
+    p.job[0].b = kOpW;
     p.job[0].n = (int)a.V;
     p.job[0].k = (int)a.K;
-    e = run_gemm(maps, p, a.T, st);
+    // A pair's tile costs the same for 16 tokens as for 256, and with up to 128 the reading of W is what
+    // should bound the call: a single CTA's tile leaves twice the tensor time to spare.
+    e = a.T <= kHalf ? run_gemm<false>(maps, p, a.T, st) : run_gemm<true>(maps, p, a.T, st);
     if (e != cudaSuccess) return e;
     return launch_pdl(head_join_kernel, dim3((unsigned)((a.T + 31) / 32)), dim3(256), 0, st, (const float2*)p.part, pl.Tp,
                       (int)(up(a.V, kTile) / kTile), p.count, p.index, (const float*)p.target_logit, a.z, a.loss, a.lse);
@@ -849,8 +1009,8 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
         if (i >= 0 && a.dh) {  // dH and dW of piece i
             Job& h = p.job[p.jobs++];
             h.kind = kDH;
-            h.a_map = 2 + (int)(i & 1);
-            h.b_map = 1;
+            h.a = kOpDl + (int)(i & 1);
+            h.b = kOpW;
             h.b_mn = 1;
             h.n = (int)a.K;
             h.k = width(i);
@@ -861,8 +1021,8 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
         if (i >= 0 && a.dw) {
             Job& w = p.job[p.jobs++];
             w.kind = kDW;
-            w.a_map = 2 + (int)(i & 1);
-            w.b_map = 0;
+            w.a = kOpDl + (int)(i & 1);
+            w.b = kOpH;
             w.a_mn = w.b_mn = 1;
             w.m = width(i);
             w.n = (int)a.K;
@@ -871,14 +1031,20 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
         if (i + 1 < pl.pieces) {  // dl of the next piece
             Job& g = p.job[p.jobs++];
             g.kind = kGrad;
-            g.b_map = 1;
+            g.a = kOpH;
+            g.b = kOpW;
             g.n = width(i + 1);
             g.k = (int)a.K;
             g.v0 = (int)((i + 1) * pl.piece);
             g.dl = (__nv_bfloat16*)(ws + pl.dl[(i + 1) & 1]);
             g.ld_dl = pl.piece;
         }
-        if (p.jobs) e = run_gemm(maps, p, a.T, st);
+        p.next += i + 1;
+        // the longest tiles first, so that the launch ends on short ones
+        std::sort(p.job, p.job + p.jobs, [&](const Job& x, const Job& y) {
+            return (x.kind == kDW ? a.T : x.k) > (y.kind == kDW ? a.T : y.k);
+        });
+        if (p.jobs) e = run_gemm<true>(maps, p, a.T, st);
     }
     return e;
 }
@@ -894,7 +1060,8 @@ cudaError_t preload_head_kernels() {
     cudaFuncAttributes at;
     cudaFuncGetAttributes(&at, head_pack_kernel<false>);
     cudaFuncGetAttributes(&at, head_pack_kernel<true>);
-    cudaFuncGetAttributes(&at, head_gemm_kernel);
+    cudaFuncGetAttributes(&at, head_gemm_kernel<true>);
+    cudaFuncGetAttributes(&at, head_gemm_kernel<false>);
     return cudaFuncGetAttributes(&at, head_join_kernel);
 }
 

@@ -128,11 +128,20 @@ def _check(status: int, what: str):
         raise Ufp4Error(status, what)
 
 
+_raw_stream = None  # (device index) -> cudaStream_t of torch's current stream
+
+
 def _stream(stream):
-    if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    return ctypes.c_void_p(int(stream))
+    """The cudaStream_t of `stream`, by default torch's current one (asked for by its handle: a Stream object
+    costs as much host time as a launch)."""
+    global _raw_stream
+    if stream is not None:
+        return int(stream)
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def make_desc(grid="e1m2", block=(1, 16), n=16, sign_seed=0, rounding=ROUND_RTNE, sr_seed=0,
@@ -317,26 +326,32 @@ def ufp4_status_string(status: int) -> str:
 
 
 # ------------------------------------------- the training step between the GEMMs
+_DTYPES = {}  # torch dtype -> UFP4 code
+
+
 def _dtype(t, what: str) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float32:
-        return F32
-    raise TypeError(f"{what} is {t.dtype}: bfloat16 or float32 is wanted")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float32: F32})
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{what} is {t.dtype}: bfloat16 or float32 is wanted")
+    return code
 
 
 def _matrix(t, what: str, rows: int, cols: int, dtype=None):
     """(pointer, leading dimension) of a 2-D tensor with unit column stride; (None, 0) of None."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{what} has shape {tuple(t.shape)}: ({rows}, {cols}) is wanted")
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}'s rows are not contiguous")
     if dtype is not None and _dtype(t, what) != dtype:
         raise TypeError(f"{what} is {t.dtype}")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    return t.data_ptr(), ld if rows > 1 or ld > cols else cols
 
 
 def _vector(t, what: str, n: int, dtype: str):
@@ -345,7 +360,7 @@ def _vector(t, what: str, n: int, dtype: str):
         return None
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} is not {n} contiguous elements")
-    if str(t.dtype) != "torch." + dtype:
+    if str(t.dtype) != dtype:
         raise TypeError(f"{what} is {t.dtype}: {dtype} is wanted")
     return t.data_ptr()
 
@@ -384,9 +399,9 @@ def ufp4_rms_norm(x, gamma, y, rstd=None, residual=None, total=None, ckpt: QTens
     dt = _dtype(gamma, "gamma")
     _check(load().ufp4_rms_norm(*_matrix(x, "x", rows, cols), _dtype(x, "x"),
                                 *_matrix(residual, "residual", rows, cols, BF16),
-                                _vector(gamma, "gamma", cols, "float32" if dt == F32 else "bfloat16"), dt, rows, cols,
+                                _vector(gamma, "gamma", cols, "torch.float32" if dt == F32 else "torch.bfloat16"), dt, rows, cols,
                                 eps, *_matrix(y, "y", rows, cols, BF16), *_matrix(total, "total", rows, cols, BF16),
-                                _vector(rstd, "rstd", rows, "float32"), _ref(ckpt), _stream(stream)), "ufp4_rms_norm")
+                                _vector(rstd, "rstd", rows, "torch.float32"), _ref(ckpt), _stream(stream)), "ufp4_rms_norm")
 
 
 def ufp4_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -402,10 +417,10 @@ def ufp4_rms_norm_backward(dy, ckpt: QTensor, rstd, gamma, dx, dgamma, workspace
     rows, cols = dy.shape
     dt = _dtype(gamma, "gamma")
     _check(load().ufp4_rms_norm_backward(*_matrix(dy, "dy", rows, cols), _dtype(dy, "dy"), _ref(ckpt),
-                                         _vector(rstd, "rstd", rows, "float32"),
-                                         _vector(gamma, "gamma", cols, "float32" if dt == F32 else "bfloat16"), dt,
+                                         _vector(rstd, "rstd", rows, "torch.float32"),
+                                         _vector(gamma, "gamma", cols, "torch.float32" if dt == F32 else "torch.bfloat16"), dt,
                                          *_matrix(dtotal, "dtotal", rows, cols, BF16), rows, cols,
-                                         *_matrix(dx, "dx", rows, cols, BF16), _vector(dgamma, "dgamma", cols, "float32"),
+                                         *_matrix(dx, "dx", rows, cols, BF16), _vector(dgamma, "dgamma", cols, "torch.float32"),
                                          *_matrix(y, "y", rows, cols, BF16), workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(), _stream(stream)),
            "ufp4_rms_norm_backward")
@@ -431,8 +446,8 @@ def ufp4_head_loss(h, w, targets, loss, lse, workspace, z_loss=0.0, stream=None)
     tokens, hidden = h.shape
     vocab = w.shape[0]
     _check(load().ufp4_head_loss(*_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
-                                 _vector(targets, "targets", tokens, "int64"), tokens, vocab, hidden, z_loss,
-                                 _vector(loss, "loss", tokens, "float32"), _vector(lse, "lse", tokens, "float32"),
+                                 _vector(targets, "targets", tokens, "torch.int64"), tokens, vocab, hidden, z_loss,
+                                 _vector(loss, "loss", tokens, "torch.float32"), _vector(lse, "lse", tokens, "torch.float32"),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
            "ufp4_head_loss")
 
@@ -444,9 +459,9 @@ def ufp4_head_loss_backward(h, w, targets, lse, dh, dw, workspace, token_weight=
     vocab = w.shape[0]
     _check(load().ufp4_head_loss_backward(
         *_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
-        _vector(targets, "targets", tokens, "int64"), tokens, vocab, hidden, z_loss,
-        _vector(lse, "lse", tokens, "float32"), _vector(token_weight, "token_weight", tokens, "float32"),
-        _vector(scale, "scale", 1, "float32"), *_matrix(dh, "dh", tokens, hidden),
+        _vector(targets, "targets", tokens, "torch.int64"), tokens, vocab, hidden, z_loss,
+        _vector(lse, "lse", tokens, "torch.float32"), _vector(token_weight, "token_weight", tokens, "torch.float32"),
+        _vector(scale, "scale", 1, "torch.float32"), *_matrix(dh, "dh", tokens, hidden),
         BF16 if dh is None else _dtype(dh, "dh"), *_matrix(dw, "dw", vocab, hidden),
         BF16 if dw is None else _dtype(dw, "dw"), int(accumulate_dw), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream)), "ufp4_head_loss_backward")
