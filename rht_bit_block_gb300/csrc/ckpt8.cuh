@@ -56,16 +56,30 @@ __device__ __forceinline__ uint32_t ckpt_pack4(const float* v, float inv) {
     return mag | (c & (mag + 0x7F7F7F7Fu) & 0x80808080u);  // the sign only where a magnitude bit is set
 }
 
-__device__ __forceinline__ void ckpt_unpack4(uint32_t c, float unit, float* v) {
+// The values of four codes, without their block's unit.
+__device__ __forceinline__ void ckpt_unpack4(uint32_t c, float* v) {
     uint32_t a, b;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(c & 0xFFFFu)));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(c >> 16)));
     const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
     const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    v[0] = fa.x * unit;
-    v[1] = fa.y * unit;
-    v[2] = fb.x * unit;
-    v[3] = fb.y * unit;
+    v[0] = fa.x;
+    v[1] = fa.y;
+    v[2] = fb.x;
+    v[3] = fb.y;
+}
+
+__device__ __forceinline__ void widen8(const uint4& a, float v[kVec]) {  // 8 bf16
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void widen8(const float4& a, const float4& b, float v[kVec]) {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 // The 8 elements at p (bf16 or fp32) as fp32.  VEC: p is aligned to the
@@ -75,17 +89,9 @@ __device__ __forceinline__ void load8(const void* p, int n, float v[kVec]) {
     if (VEC) {
         if (F32) {
             const float4* q = reinterpret_cast<const float4*>(p);
-            const float4 a = __ldcs(q), b = __ldcs(q + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            widen8(__ldcs(q), __ldcs(q + 1), v);
         } else {
-            const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
+            widen8(__ldcs(reinterpret_cast<const uint4*>(p)), v);
         }
     } else {
 #pragma unroll
@@ -160,8 +166,10 @@ __device__ __forceinline__ void ckpt_load8(const Ckpt& k, int64_t row, int c, in
         }
     }
     const float unit = ckpt_unit(byte);
-    ckpt_unpack4(q.x, unit, v);
-    ckpt_unpack4(q.y, unit, v + 4);
+    ckpt_unpack4(q.x, v);
+    ckpt_unpack4(q.y, v + 4);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] *= unit;
     if (!VEC && byte == 255u) {  // the zeros past the end of a row stay zeros beside a NaN block
 #pragma unroll
         for (int i = 0; i < kVec; ++i)

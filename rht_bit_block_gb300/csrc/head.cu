@@ -56,10 +56,10 @@ constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sle
 constexpr uint32_t kSuspendNs = 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A CTA pair's 256 x 256 tile, or a single CTA's 128 x 256 tile.  A pair
-// holds 128 rows of A and half the rows of B per CTA, so it moves two thirds
-// of the single CTA's bytes per product; its stages hold two steps, which
-// halves the hand-offs between the copies and the tensor core (one-step
+// A CTA pair's 256 x 256 tile, or a single CTA's 128 x (up to 256) tile.  A
+// pair holds 128 rows of A and half the rows of B per CTA, so it moves two
+// thirds of the single CTA's bytes per product; its stages hold two steps,
+// which halves the hand-offs between the copies and the tensor core (one-step
 // stages: 4096 x 16384 x 2048 logits 193 us, two-step stages 174 us).
 template <bool PAIR>
 struct Cfg {
@@ -76,7 +76,6 @@ struct Cfg {
     static constexpr int kNumBars = 2 * kStages + 4 + 2 * kRing + 1;
     static constexpr int kOffWords = kOffBars + 8 * kNumBars;  // tensor memory address, abort flag, ring of tiles
     static constexpr int kSmem = kOffWords + 4 * (2 + kRing) + 1024;
-    static constexpr int kTx = (PAIR ? 2 : 1) * (kAtom + kAtomB);  // bytes of one step, counted by the leader
     static_assert(kSmem <= 232448, "shared memory overflow");
 };
 
@@ -163,9 +162,9 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // kind::f16: fp32 accumulator, bf16 operands, MN-major A (bit 15) and B (bit 16), N >> 3, M >> 4.
-__host__ __device__ constexpr uint32_t make_idesc(int rows, bool a_mn, bool b_mn) {
+__host__ __device__ constexpr uint32_t make_idesc(int rows, int cols, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(rows >> 4) << 24);
+           ((uint32_t)(cols >> 3) << 17) | ((uint32_t)(rows >> 4) << 24);
 }
 template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -358,6 +357,7 @@ struct Job {
     int kind;
     int a, b;               // operands (Operand)
     int a_mn, b_mn;         // the operand's contiguous index is not the summed one
+    int width;              // columns of a tile: kTile, or less for single CTAs (a multiple of 16)
     int m, n, k;            // extents; kernel-side: m (or k for kDW) comes from the token count
     int v0;                 // first vocabulary row of the piece
     int first, last;        // kDH: first and last piece
@@ -367,20 +367,24 @@ struct Job {
 constexpr int kMaxJobs = 3;
 enum Operand { kOpH = 0, kOpW = 1, kOpDl = 2, kOperands = 4 };  // packed H, W, two pieces of dl
 // Each operand's tensor map with boxes of 128 rows (K-major: a CTA's half of
-// a tile) and of 64 rows (MN-major: one column block).
+// a tile) and of 64 rows (MN-major: one column block).  For single CTAs W's
+// K-major boxes have half a tile's columns.
 struct HeadMaps {
     CUtensorMap m[kOperands][2];
 };
 struct HeadParams {
     Job job[kMaxJobs];
     int jobs;
-    const int* count;
-    int* next;              // tiles handed out beyond one per cluster
+    const int* count;       // null: all `tokens`, in place
+    int tokens;
+    const int64_t* targets; // with tokens in place
+    int vocab;
+    int* next;              // tiles handed out beyond one per cluster; null: a fixed share each
     const int* index;
     const RowInfo* info;
-    float2* part;           // kStats: [vocabulary tile][packed row]
+    float2* part;           // kStats: [row][vocabulary tile]
+    int64_t ld_part;
     float* target_logit;
-    int64_t Tp;
     float* dh_acc;          // fp32 across the pieces: packed rows x Kp
     int64_t Kp;
     const float* scale;
@@ -411,7 +415,7 @@ struct Walk {
             const Job& q = p.job[j];
             const int m = q.kind == kDW ? q.m : count, k = q.kind == kDW ? count : q.k;
             m_tiles[j] = (m + ROWS - 1) / ROWS;
-            n_tiles[j] = (q.n + kTile - 1) / kTile;
+            n_tiles[j] = (q.n + q.width - 1) / q.width;
             k_steps[j] = (k + kStep - 1) / kStep;
             total += m_tiles[j] * n_tiles[j];
         }
@@ -553,7 +557,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
     griddep_wait();
     griddep_launch();
 
-    const int count = *p.count;
+    const int count = p.count ? *p.count : p.tokens;
     const Walk<C::kRows> walk(p, count);
 
     // The tile number i of this cluster, or -1 when there is none (or a wait gave up).  `arrive`: this
@@ -577,7 +581,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 *abort_flag = 1;
                 break;
             }
-            const int tile = i == 0 ? cluster_id : num_clusters + atomicAdd(p.next, 1);
+            const int tile = i == 0 || !p.next ? cluster_id + i * num_clusters : num_clusters + atomicAdd(p.next, 1);
             const uint32_t slot = smem_u32(const_cast<int*>(ring + at));
             for (uint32_t r = leader; r <= leader + (PAIR ? 1 : 0); ++r) {
                 st_cluster(map_to_rank(slot, r), tile);
@@ -599,7 +603,8 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             const CUtensorMap* map = &maps.m[is_a ? q.a : q.b][mn];
             // W's rows are the whole vocabulary, a piece starts at v0; dl's columns are the piece's own
             const int r0 = is_a ? t.m * C::kRows + peer * kHalf
-                                : t.n * kTile + peer * C::kBRows + (q.b_mn ? 0 : q.v0);
+                                : t.n * q.width + peer * C::kBRows + (q.b_mn ? 0 : q.v0);
+            const int tx = PAIR ? 4 * kAtom : kAtom + q.width * 128;  // bytes of one step, of both CTAs
             const int kb = !is_a && q.kind == kDH ? q.v0 : 0;  // first summed row of W
             for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
                 if (!mbar_wait(empty_bar(s), ph ^ 1u)) {
@@ -608,7 +613,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 }
                 const int nk = min(C::kKps, t.k_steps - ks);
                 const uint32_t fb = PAIR ? map_to_rank(full_bar(s), leader) : full_bar(s);
-                if (is_a && peer == 0) mbar_expect_tx(full_bar(s), nk * C::kTx);
+                if (is_a && peer == 0) mbar_expect_tx(full_bar(s), nk * tx);
                 for (int j = 0; j < nk; ++j) {
                     const uint32_t dst =
                         is_a ? base + C::kOffA + s * C::kA + j * kAtom : base + C::kOffB + s * C::kB + j * C::kAtomB;
@@ -618,7 +623,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                         tma_load<PAIR>(dst + kBlockBytes, map, r0 + 64, k, fb);
                     } else {
                         tma_load<PAIR>(dst, map, k, r0, fb);
-                        if (!PAIR && !is_a) tma_load<PAIR>(dst + kAtom, map, k, r0 + kHalf, fb);
+                        if (!PAIR && !is_a) tma_load<PAIR>(dst + q.width * 64, map, k, r0 + q.width / 2, fb);
                     }
                 }
                 if (++s == S) {
@@ -644,7 +649,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             }
             tc_fence_after();
             const uint32_t acc = tmem + buf * kTile;
-            const uint32_t idesc = make_idesc(C::kRows, q.a_mn, q.b_mn);
+            const uint32_t idesc = make_idesc(C::kRows, q.width, q.a_mn, q.b_mn);
             // 16 summed elements: 32 bytes along a swizzle row, or 16 rows of 128 bytes
             const int astep = q.a_mn ? 2048 >> 4 : 32 >> 4, bstep = q.b_mn ? 2048 >> 4 : 32 >> 4;
             for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
@@ -688,13 +693,21 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             const TileAt t = walk.at(tile);
             const Job& q = p.job[t.job];
             const int row = t.m * C::kRows + peer * kHalf + q4 * 32 + lane;
-            const int n0 = t.n * kTile;
+            const int n0 = t.n * q.width;
             const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + buf * kTile;
             float r[32];
             if (q.kind == kStats) {
-                const int target = row < count ? p.info[row].target : -1;
+                int target = -1;
+                if (row < count) {
+                    if (p.targets) {
+                        const int64_t v = p.targets[row];
+                        target = v >= 0 && v < p.vocab ? (int)v : -1;
+                    } else {
+                        target = p.info[row].target;
+                    }
+                }
                 float m = -INFINITY, sum = 0.0f, hit = 0.0f;
-                for (int c = 0; c < kTile; c += 32) {
+                for (int c = 0; c < q.width; c += 32) {
                     tmem_ld32(acc + c, r);
                     const int at = target - (n0 + c);
                     if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
@@ -702,11 +715,11 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                         for (int i = 0; i < 32; ++i)
                             if (at == i) hit = r[i];
                     }
-                    stats_chunk(r, q.n - (n0 + c), m, sum);
+                    stats_chunk(r, min(q.n - n0, q.width) - c, m, sum);
                 }
                 if (row < count) {
-                    p.part[(int64_t)t.n * p.Tp + row] = make_float2(m, sum);
-                    if (target >= n0 && target < n0 + kTile) p.target_logit[row] = hit;
+                    p.part[row * p.ld_part + t.n] = make_float2(m, sum);
+                    if (target >= n0 && target < n0 + q.width) p.target_logit[row] = hit;
                 }
             } else if (q.kind == kGrad) {
                 RowInfo info = {0.0f, 0.0f, 0.0f, -1};
@@ -772,16 +785,13 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
 }
 
 // ------------------------------------------------------------ joining tiles
-// lse and loss of 32 packed rows a CTA: 8 slices of the vocabulary tiles, each
-// in the tiles' order, then the slices.
-__global__ void __launch_bounds__(256) head_join_kernel(const float2* part, int64_t Tp, int tiles, const int* count,
-                                                        const int* index, const float* target_logit, float z,
-                                                        float* loss, float* lse) {
-    __shared__ float2 slice[8][32];
+// lse and loss of a row from its tiles, a warp a row: 32 slices of the tiles,
+// each in order, then the slices pairwise.
+__global__ void __launch_bounds__(256) head_join_kernel(const HeadParams p, int tiles, float z, float* loss, float* lse) {
     griddep_wait();
     griddep_launch();
-    const int row = blockIdx.x * 32 + (threadIdx.x & 31), j = threadIdx.x >> 5;
-    if (blockIdx.x * 32 >= *count) return;
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= (p.count ? *p.count : p.tokens)) return;
     auto join = [](float2& a, float2 b) {
         const float m = fmaxf(a.x, b.x);
         const float shift = m == -INFINITY ? 0.0f : m * kLog2e;
@@ -789,15 +799,24 @@ __global__ void __launch_bounds__(256) head_join_kernel(const float2* part, int6
         a.x = m;
     };
     float2 a = make_float2(-INFINITY, 0.0f);
-    for (int t = j; t < tiles; t += 8) join(a, part[(int64_t)t * Tp + row]);
-    slice[j][threadIdx.x & 31] = a;
-    __syncthreads();
-    if (j || row >= *count) return;
-    for (int k = 1; k < 8; ++k) join(a, slice[k][threadIdx.x]);
+    const float2* part = p.part + row * p.ld_part;
+#pragma unroll 4
+    for (int t = lane; t < tiles; t += 32) join(a, part[t]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        join(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, o), __shfl_xor_sync(0xFFFFFFFFu, a.y, o)));
+    if (lane) return;
     const float l = a.x + logf(a.y);
-    const int token = index[row];
-    lse[token] = l;
-    loss[token] = fmaf(z * l, l, l - target_logit[row]);
+    int token = row;
+    bool valid = true;
+    if (p.targets) {
+        const int64_t v = p.targets[row];
+        valid = v >= 0 && v < p.vocab;
+    } else {
+        token = p.index[row];
+    }
+    lse[token] = valid ? l : 0.0f;
+    loss[token] = valid ? fmaf(z * l, l, l - p.target_logit[row]) : 0.0f;
 }
 
 // ------------------------------------------------------------------- host
@@ -808,6 +827,8 @@ struct Plan {
     int64_t Tp, Kp;          // packed rows and columns
     int64_t pieces, piece;   // backward: vocabulary pieces and their width (a multiple of kTile)
     int64_t launches;        // of the product kernel
+    bool direct;             // forward: tokens in place, none packed
+    int64_t width, tiles;    // forward: columns of a tile, tiles of the vocabulary
     size_t count, next, index, info, packed, part, target, dl[2], acc, total;
 };
 
@@ -818,7 +839,7 @@ struct Plan {
 // 128 and 256 MB, of 2047 x 50001 x 2048 (a third ignored) 887, 815 and 780 us.
 constexpr int64_t kPieceBytes = 256ll << 20;
 
-Plan make_plan(int64_t T, int64_t V, int64_t K, bool back) {
+Plan make_plan(int64_t T, int64_t V, int64_t K, bool back, int num_sms) {
     Plan p = {};
     p.Tp = std::max<int64_t>(up(T, kTile), kTile);
     p.Kp = up(K, 8);
@@ -834,7 +855,7 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back) {
         p.piece = up((V + p.pieces - 1) / p.pieces, kTile);
         p.pieces = (V + p.piece - 1) / p.piece;
     }
-    p.launches = p.pieces + 1;
+    p.launches = p.pieces + 1;  // forward: one
     p.count = take(4);
     p.next = take(4 * p.launches);
     p.index = take(4 * p.Tp);
@@ -845,16 +866,21 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back) {
         p.dl[1] = p.pieces > 1 ? take(2 * p.Tp * p.piece) : p.dl[0];
         p.acc = p.pieces > 1 ? take(4 * p.Tp * p.Kp) : 0;
     } else {
-        p.part = take((int64_t)sizeof(float2) * p.Tp * up(V, kTile) / kTile);
+        // up to kHalf tokens: one tile a CTA and round, all CTAs busy
+        p.direct = T <= kHalf;
+        const int64_t rounds = (V + (int64_t)kTile * num_sms - 1) / ((int64_t)kTile * num_sms);
+        p.width = p.direct ? std::max<int64_t>(32, up((V + rounds * num_sms - 1) / (rounds * num_sms), 16)) : kTile;
+        p.tiles = (V + p.width - 1) / p.width;
+        p.part = take((int64_t)sizeof(float2) * p.Tp * p.tiles);
         p.target = take(4 * p.Tp);
     }
     p.total = off;
     return p;
 }
 
-bool bf16_maps(CUtensorMap map[2], const void* ptr, int64_t inner, int64_t outer, int64_t ld) {
+bool bf16_maps(CUtensorMap map[2], const void* ptr, int64_t inner, int64_t outer, int64_t ld, int rows = kHalf) {
     return encode_map_2d(&map[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, (uint64_t)inner, (uint64_t)outer,
-                         (uint64_t)ld * 2, 64, kHalf, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                         (uint64_t)ld * 2, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B) &&
            encode_map_2d(&map[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, (uint64_t)inner, (uint64_t)outer,
                          (uint64_t)ld * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
 }
@@ -897,7 +923,7 @@ cudaError_t run_gemm(const HeadMaps& maps, const HeadParams& p, int64_t T, cudaS
     int64_t tiles = 0;  // with every token valid
     for (int j = 0; j < p.jobs; ++j) {
         const Job& q = p.job[j];
-        tiles += up(q.kind == kDW ? q.m : T, C::kRows) / C::kRows * (up(q.n, kTile) / kTile);
+        tiles += up(q.kind == kDW ? q.m : T, C::kRows) / C::kRows * (up(q.n, q.width) / q.width);
     }
     if (tiles > 0x3FFFFFFF) return cudaErrorNotSupported;
     cfg.gridDim = dim3(ctas * (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, most)));
@@ -937,7 +963,9 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
 
 cudaError_t make_maps(const HeadArgs& a, const Plan& pl, bool back, HeadMaps& maps) {
     uint8_t* ws = (uint8_t*)a.workspace;
-    bool ok = bf16_maps(maps.m[kOpH], ws + pl.packed, a.K, pl.Tp, pl.Kp) && bf16_maps(maps.m[kOpW], a.w, a.K, a.V, a.ldw);
+    bool ok = (pl.direct ? bf16_maps(maps.m[kOpH], a.h, a.K, a.T, a.ldh)
+                         : bf16_maps(maps.m[kOpH], ws + pl.packed, a.K, pl.Tp, pl.Kp)) &&
+              bf16_maps(maps.m[kOpW], a.w, a.K, a.V, a.ldw, pl.direct ? (int)pl.width / 2 : kHalf);
     for (int i = 0; i < 2; ++i) {
         if (back)
             ok = ok && bf16_maps(maps.m[kOpDl + i], ws + pl.dl[i], pl.piece, pl.Tp, pl.piece);
@@ -956,7 +984,7 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
     p.info = (const RowInfo*)(ws + pl.info);
     p.part = (float2*)(ws + pl.part);
     p.target_logit = (float*)(ws + pl.target);
-    p.Tp = pl.Tp;
+    p.ld_part = pl.tiles;
     p.dh_acc = (float*)(ws + pl.acc);
     p.Kp = pl.Kp;
     p.scale = a.scale;
@@ -967,20 +995,31 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
     p.ld_dw = a.ld_dw;
     p.dw_f32 = a.dw_f32;
     p.accumulate = a.accumulate;
+    for (Job& q : p.job) q.width = kTile;
+    if (pl.direct) {
+        p.count = nullptr;
+        p.tokens = (int)a.T;
+        p.targets = a.targets;
+        p.vocab = (int)a.V;
+        p.next = nullptr;
+        p.job[0].width = (int)pl.width;
+    }
     return p;
 }
 
 }  // namespace
 
-size_t head_loss_bytes(int64_t T, int64_t V, int64_t K) { return make_plan(T, V, K, false).total; }
-size_t head_loss_backward_bytes(int64_t T, int64_t V, int64_t K) { return make_plan(T, V, K, true).total; }
+size_t head_loss_bytes(int64_t T, int64_t V, int64_t K, int num_sms) { return make_plan(T, V, K, false, num_sms).total; }
+size_t head_loss_backward_bytes(int64_t T, int64_t V, int64_t K, int num_sms) {
+    return make_plan(T, V, K, true, num_sms).total;
+}
 
 cudaError_t launch_head_loss(const HeadArgs& a, int num_sms, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
-    const Plan pl = make_plan(a.T, a.V, a.K, false);
+    const Plan pl = make_plan(a.T, a.V, a.K, false, num_sms);
     HeadMaps maps;
     cudaError_t e = make_maps(a, pl, false, maps);
-    if (e == cudaSuccess) e = run_pack(a, pl, false, num_sms, st);
+    if (e == cudaSuccess && !pl.direct) e = run_pack(a, pl, false, num_sms, st);
     if (e != cudaSuccess) return e;
     HeadParams p = make_params(a, pl);
     p.jobs = 1;
@@ -991,14 +1030,14 @@ cudaError_t launch_head_loss(const HeadArgs& a, int num_sms, cudaStream_t st) {
     p.job[0].k = (int)a.K;
     // A pair's tile costs the same for 16 tokens as for 256, and with up to 128 the reading of W is what
     // should bound the call: a single CTA's tile leaves twice the tensor time to spare.
-    e = a.T <= kHalf ? run_gemm<false>(maps, p, a.T, st) : run_gemm<true>(maps, p, a.T, st);
+    e = pl.direct ? run_gemm<false>(maps, p, a.T, st) : run_gemm<true>(maps, p, a.T, st);
     if (e != cudaSuccess) return e;
-    return launch_pdl(head_join_kernel, dim3((unsigned)((a.T + 31) / 32)), dim3(256), 0, st, (const float2*)p.part, pl.Tp,
-                      (int)(up(a.V, kTile) / kTile), p.count, p.index, (const float*)p.target_logit, a.z, a.loss, a.lse);
+    return launch_pdl(head_join_kernel, dim3((unsigned)((a.T + 7) / 8)), dim3(256), 0, st, p, (int)pl.tiles, a.z, a.loss,
+                      a.lse);
 }
 
 cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream_t st) {
-    const Plan pl = make_plan(a.T, a.V, a.K, true);
+    const Plan pl = make_plan(a.T, a.V, a.K, true, num_sms);
     uint8_t* ws = (uint8_t*)a.workspace;
     HeadMaps maps;
     cudaError_t e = make_maps(a, pl, true, maps);

@@ -91,8 +91,8 @@ struct HeadArgs {
     bool dw_f32, accumulate;
     void* workspace;
 };
-size_t head_loss_bytes(int64_t T, int64_t V, int64_t K);
-size_t head_loss_backward_bytes(int64_t T, int64_t V, int64_t K);
+size_t head_loss_bytes(int64_t T, int64_t V, int64_t K, int num_sms);
+size_t head_loss_backward_bytes(int64_t T, int64_t V, int64_t K, int num_sms);
 cudaError_t launch_head_loss(const HeadArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream_t st);
 cudaError_t head_error_read_clear(int* value);

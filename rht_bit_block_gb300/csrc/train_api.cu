@@ -207,11 +207,11 @@ static ufp4_status check_workspace(const void* workspace, size_t bytes, size_t n
     return (uintptr_t)workspace % 256 ? UFP4_ERR_ALIGNMENT : UFP4_OK;
 }
 
-static ufp4_status head_bytes(int64_t tokens, int64_t vocab, int64_t hidden, size_t (*f)(int64_t, int64_t, int64_t),
-                              size_t* bytes) {
+static ufp4_status head_bytes(int64_t tokens, int64_t vocab, int64_t hidden,
+                              size_t (*f)(int64_t, int64_t, int64_t, int), size_t* bytes) {
     if (tokens < 0 || vocab < 1 || hidden < 1 || !bytes) return UFP4_ERR_INVALID_ARG;
     if (tokens > kMaxExtent || vocab > kMaxExtent || hidden > kMaxExtent) return UFP4_ERR_UNSUPPORTED;
-    *bytes = f(tokens, vocab, hidden);
+    *bytes = f(tokens, vocab, hidden, current_num_sms());
     return UFP4_OK;
 }
 
@@ -230,7 +230,7 @@ ufp4_status ufp4_head_loss(const void* h, int64_t ldh, const void* w, int64_t ld
     if (tokens == 0) return UFP4_OK;
     UFP4_CHECK(check_matrix(loss, 1, 1, 4, false));
     UFP4_CHECK(check_matrix(lse, 1, 1, 4, false));
-    UFP4_CHECK(check_workspace(workspace, workspace_bytes, head_loss_bytes(tokens, vocab, hidden)));
+    UFP4_CHECK(check_workspace(workspace, workspace_bytes, head_loss_bytes(tokens, vocab, hidden, current_num_sms())));
     HeadArgs a = {};
     a.h = h;
     a.ldh = ldh;
@@ -263,7 +263,7 @@ ufp4_status ufp4_head_loss_backward(const void* h, int64_t ldh, const void* w, i
     }
     UFP4_CHECK(check_matrix(scale, 1, 1, 4, true));
     UFP4_CHECK(check_matrix(dw, hidden, ld_dw, size_of(dw_dtype), true));
-    UFP4_CHECK(check_workspace(workspace, workspace_bytes, head_loss_backward_bytes(tokens, vocab, hidden)));
+    UFP4_CHECK(check_workspace(workspace, workspace_bytes, head_loss_backward_bytes(tokens, vocab, hidden, current_num_sms())));
     HeadArgs a = {};
     a.h = h;
     a.ldh = ldh;
