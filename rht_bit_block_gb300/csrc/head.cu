@@ -47,6 +47,7 @@ namespace {
 
 constexpr int kTile = 256;                 // output columns of a tile, and rows of a CTA pair's tile
 constexpr int kHalf = 128;                 // rows of A that one CTA holds
+constexpr int kAlone = 224;                // most columns of a single CTA's tile
 constexpr int kStep = 64;                  // summed elements per step (one 128-byte swizzle row)
 constexpr int kBlockBytes = 64 * 64 * 2;   // 64 rows of 64 bf16: one column block of an MN-major operand
 constexpr int kAtom = 2 * kBlockBytes;     // 128 rows of one step
@@ -56,17 +57,20 @@ constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sle
 constexpr uint32_t kSuspendNs = 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A CTA pair's 256 x 256 tile, or a single CTA's 128 x (up to 256) tile.  A
+// A CTA pair's 256 x 256 tile, or a single CTA's 128 x (up to 224) tile.  A
 // pair holds 128 rows of A and half the rows of B per CTA, so it moves two
 // thirds of the single CTA's bytes per product; its stages hold two steps,
 // which halves the hand-offs between the copies and the tensor core (one-step
-// stages: 4096 x 16384 x 2048 logits 193 us, two-step stages 174 us).
+// stages: 4096 x 16384 x 2048 logits 193 us, two-step stages 174 us).  A
+// single CTA's tile is for reading W once: 224 columns leave room for a fifth
+// stage (16 tokens, 131072 x 2048: 256 columns and four stages 124 us, 224 and
+// five 111 us, 96 and eight 173 us).
 template <bool PAIR>
 struct Cfg {
     static constexpr int kRows = PAIR ? kTile : kHalf;   // rows of a tile
     static constexpr int kKps = PAIR ? 2 : 1;            // steps per stage
-    static constexpr int kStages = PAIR ? 3 : 4;
-    static constexpr int kBRows = PAIR ? kHalf : kTile;  // rows of B per CTA
+    static constexpr int kStages = PAIR ? 3 : 5;
+    static constexpr int kBRows = PAIR ? kHalf : kAlone;  // rows of B per CTA
     static constexpr int kAtomB = kBRows * 128;
     static constexpr int kA = kKps * kAtom, kB = kKps * kAtomB;
     static constexpr int kOffA = 0;
@@ -357,7 +361,8 @@ struct Job {
     int kind;
     int a, b;               // operands (Operand)
     int a_mn, b_mn;         // the operand's contiguous index is not the summed one
-    int width;              // columns of a tile: kTile, or less for single CTAs (a multiple of 16)
+    int group;              // tile rows that advance before the column does
+    int width;              // columns of a tile: kTile, or less for single CTAs (a multiple of 16, up to kAlone)
     int m, n, k;            // extents; kernel-side: m (or k for kDW) comes from the token count
     int v0;                 // first vocabulary row of the piece
     int first, last;        // kDH: first and last piece
@@ -400,9 +405,12 @@ struct TileAt {
     int job, m, n, k_steps;
 };
 
-// Tile rows that advance before the column does: the tiles in flight then
-// share a few panels of either operand, which stay in L2.
+// Tile rows that advance before the column does.  Tiles in flight walk the
+// summed index together, so eight by about nine of them share few panels of
+// either operand; where all of A stays in L2, all its rows go first, and B is
+// read once.
 constexpr int kGroupM = 8;
+constexpr int64_t kResidentA = 48ll << 20;
 
 template <int ROWS>
 struct Walk {
@@ -420,7 +428,7 @@ struct Walk {
             total += m_tiles[j] * n_tiles[j];
         }
     }
-    __device__ __forceinline__ TileAt at(int tile) const {
+    __device__ __forceinline__ TileAt at(const HeadParams& p, int tile) const {
         TileAt t;
         t.job = 0;
 #pragma unroll
@@ -440,8 +448,9 @@ struct Walk {
                 nt = n_tiles[j];
                 t.k_steps = k_steps[j];
             }
-        const int span = kGroupM * nt, g = tile / span, first = g * kGroupM;
-        const int rows = min(kGroupM, mt - first), l = tile - g * span;
+        const int group = min(p.job[t.job].group, mt);
+        const int span = group * nt, g = tile / span, first = g * group;
+        const int rows = min(group, mt - first), l = tile - g * span;
         t.n = l / rows;
         t.m = first + (l - t.n * rows);
         return t;
@@ -597,7 +606,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         for (int i = 0;; ++i) {
             const int tile = take(i, true);
             if (tile < 0 || *abort_flag) break;
-            const TileAt t = walk.at(tile);
+            const TileAt t = walk.at(p, tile);
             const Job& q = p.job[t.job];
             const bool mn = is_a ? q.a_mn : q.b_mn;
             const CUtensorMap* map = &maps.m[is_a ? q.a : q.b][mn];
@@ -640,7 +649,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         for (int tc = 0; ok; ++tc) {
             const int tile = take(tc, true);
             if (tile < 0) break;
-            const TileAt t = walk.at(tile);
+            const TileAt t = walk.at(p, tile);
             const Job& q = p.job[t.job];
             const int buf = tc & 1;
             if (!mbar_wait(acce_bar(buf), ((tc >> 1) & 1) ^ 1)) {
@@ -690,7 +699,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(accf_bar(buf), (tc >> 1) & 1));
             if (!ok || *abort_flag) break;
             tc_fence_after();
-            const TileAt t = walk.at(tile);
+            const TileAt t = walk.at(p, tile);
             const Job& q = p.job[t.job];
             const int row = t.m * C::kRows + peer * kHalf + q4 * 32 + lane;
             const int n0 = t.n * q.width;
@@ -868,7 +877,7 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back, int num_sms) {
     } else {
         // up to kHalf tokens: one tile a CTA and round, all CTAs busy
         p.direct = T <= kHalf;
-        const int64_t rounds = (V + (int64_t)kTile * num_sms - 1) / ((int64_t)kTile * num_sms);
+        const int64_t rounds = (V + (int64_t)kAlone * num_sms - 1) / ((int64_t)kAlone * num_sms);
         p.width = p.direct ? std::max<int64_t>(32, up((V + rounds * num_sms - 1) / (rounds * num_sms), 16)) : kTile;
         p.tiles = (V + p.width - 1) / p.width;
         p.part = take((int64_t)sizeof(float2) * p.Tp * p.tiles);
@@ -899,7 +908,7 @@ int max_clusters(const cudaLaunchConfig_t& cfg) {
 }
 
 template <bool PAIR>
-cudaError_t run_gemm(const HeadMaps& maps, const HeadParams& p, int64_t T, cudaStream_t st) {
+cudaError_t run_gemm(const HeadMaps& maps, HeadParams& p, int64_t T, cudaStream_t st) {
     using C = Cfg<PAIR>;
     cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
@@ -920,6 +929,11 @@ cudaError_t run_gemm(const HeadMaps& maps, const HeadParams& p, int64_t T, cudaS
     cfg.numAttrs = 1;
     const int most = max_clusters<PAIR>(cfg);
     if (most <= 0) return cudaErrorLaunchOutOfResources;
+    for (int j = 0; j < p.jobs; ++j) {
+        Job& q = p.job[j];
+        const int64_t m = q.kind == kDW ? q.m : T, k = q.kind == kDW ? T : q.k;
+        q.group = 2 * m * k <= kResidentA ? 1 << 30 : kGroupM;
+    }
     int64_t tiles = 0;  // with every token valid
     for (int j = 0; j < p.jobs; ++j) {
         const Job& q = p.job[j];

@@ -326,17 +326,22 @@ def ufp4_status_string(status: int) -> str:
 
 
 # ------------------------------------------- the training step between the GEMMs
-_DTYPES = {}  # torch dtype -> UFP4 code
+_DTYPES = {}  # torch dtype -> UFP4 code (bfloat16, float32), or -1 for int64
+
+
+def _code(t):
+    code = _DTYPES.get(t.dtype)
+    if code is None and not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float32: F32, torch.int64: -1})
+        code = _DTYPES.get(t.dtype)
+    return code
 
 
 def _dtype(t, what: str) -> int:
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        import torch
-        _DTYPES.update({torch.bfloat16: BF16, torch.float32: F32})
-        code = _DTYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{what} is {t.dtype}: bfloat16 or float32 is wanted")
+    code = _code(t)
+    if code is None or code < 0:
+        raise TypeError(f"{what} is {t.dtype}: bfloat16 or float32 is wanted")
     return code
 
 
@@ -349,19 +354,19 @@ def _matrix(t, what: str, rows: int, cols: int, dtype=None):
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what}'s rows are not contiguous")
-    if dtype is not None and _dtype(t, what) != dtype:
+    if dtype is not None and _code(t) != dtype:
         raise TypeError(f"{what} is {t.dtype}")
     return t.data_ptr(), ld if rows > 1 or ld > cols else cols
 
 
-def _vector(t, what: str, n: int, dtype: str):
-    """Pointer of a contiguous 1-D tensor of n elements; None of None."""
+def _vector(t, what: str, n: int, code: int):
+    """Pointer of a contiguous 1-D tensor of n elements (code -1: int64); None of None."""
     if t is None:
         return None
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} is not {n} contiguous elements")
-    if str(t.dtype) != dtype:
-        raise TypeError(f"{what} is {t.dtype}: {dtype} is wanted")
+    if _code(t) != code:
+        raise TypeError(f"{what} is {t.dtype}")
     return t.data_ptr()
 
 
@@ -399,9 +404,9 @@ def ufp4_rms_norm(x, gamma, y, rstd=None, residual=None, total=None, ckpt: QTens
     dt = _dtype(gamma, "gamma")
     _check(load().ufp4_rms_norm(*_matrix(x, "x", rows, cols), _dtype(x, "x"),
                                 *_matrix(residual, "residual", rows, cols, BF16),
-                                _vector(gamma, "gamma", cols, "torch.float32" if dt == F32 else "torch.bfloat16"), dt, rows, cols,
+                                _vector(gamma, "gamma", cols, dt), dt, rows, cols,
                                 eps, *_matrix(y, "y", rows, cols, BF16), *_matrix(total, "total", rows, cols, BF16),
-                                _vector(rstd, "rstd", rows, "torch.float32"), _ref(ckpt), _stream(stream)), "ufp4_rms_norm")
+                                _vector(rstd, "rstd", rows, F32), _ref(ckpt), _stream(stream)), "ufp4_rms_norm")
 
 
 def ufp4_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -417,10 +422,10 @@ def ufp4_rms_norm_backward(dy, ckpt: QTensor, rstd, gamma, dx, dgamma, workspace
     rows, cols = dy.shape
     dt = _dtype(gamma, "gamma")
     _check(load().ufp4_rms_norm_backward(*_matrix(dy, "dy", rows, cols), _dtype(dy, "dy"), _ref(ckpt),
-                                         _vector(rstd, "rstd", rows, "torch.float32"),
-                                         _vector(gamma, "gamma", cols, "torch.float32" if dt == F32 else "torch.bfloat16"), dt,
+                                         _vector(rstd, "rstd", rows, F32),
+                                         _vector(gamma, "gamma", cols, dt), dt,
                                          *_matrix(dtotal, "dtotal", rows, cols, BF16), rows, cols,
-                                         *_matrix(dx, "dx", rows, cols, BF16), _vector(dgamma, "dgamma", cols, "torch.float32"),
+                                         *_matrix(dx, "dx", rows, cols, BF16), _vector(dgamma, "dgamma", cols, F32),
                                          *_matrix(y, "y", rows, cols, BF16), workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(), _stream(stream)),
            "ufp4_rms_norm_backward")
@@ -446,8 +451,8 @@ def ufp4_head_loss(h, w, targets, loss, lse, workspace, z_loss=0.0, stream=None)
     tokens, hidden = h.shape
     vocab = w.shape[0]
     _check(load().ufp4_head_loss(*_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
-                                 _vector(targets, "targets", tokens, "torch.int64"), tokens, vocab, hidden, z_loss,
-                                 _vector(loss, "loss", tokens, "torch.float32"), _vector(lse, "lse", tokens, "torch.float32"),
+                                 _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss,
+                                 _vector(loss, "loss", tokens, F32), _vector(lse, "lse", tokens, F32),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
            "ufp4_head_loss")
 
@@ -459,9 +464,9 @@ def ufp4_head_loss_backward(h, w, targets, lse, dh, dw, workspace, token_weight=
     vocab = w.shape[0]
     _check(load().ufp4_head_loss_backward(
         *_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
-        _vector(targets, "targets", tokens, "torch.int64"), tokens, vocab, hidden, z_loss,
-        _vector(lse, "lse", tokens, "torch.float32"), _vector(token_weight, "token_weight", tokens, "torch.float32"),
-        _vector(scale, "scale", 1, "torch.float32"), *_matrix(dh, "dh", tokens, hidden),
+        _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss,
+        _vector(lse, "lse", tokens, F32), _vector(token_weight, "token_weight", tokens, F32),
+        _vector(scale, "scale", 1, F32), *_matrix(dh, "dh", tokens, hidden),
         BF16 if dh is None else _dtype(dh, "dh"), *_matrix(dw, "dw", vocab, hidden),
         BF16 if dw is None else _dtype(dw, "dw"), int(accumulate_dw), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream)), "ufp4_head_loss_backward")

@@ -244,3 +244,38 @@ def test_reproducible_on_another_stream():
     side.synchronize()
     for a, b in ((loss, loss2), (lse, lse2), (dh, dh2), (dw, dw2)):
         assert torch.equal(a, b)
+
+
+def test_in_a_graph():
+    """Forward and backward captured, replayed on new inputs (the count of valid tokens is read on the device)."""
+    tokens, vocab, hidden = 300, 900, 128
+    h, w, t = _inputs(tokens, vocab, hidden, seed=13)
+    h2, w2, t2 = _inputs(tokens, vocab, hidden, seed=14, ignored=0.6)
+    loss, lse = torch.empty(tokens, device=DEV), torch.empty(tokens, device=DEV)
+    dh, dw = torch.empty_like(h), torch.empty_like(w)
+    ws = torch.empty(max(ufp4.ufp4_head_loss_workspace_size(tokens, vocab, hidden),
+                         ufp4.ufp4_head_loss_backward_workspace_size(tokens, vocab, hidden)), dtype=torch.uint8, device=DEV)
+
+    def run():
+        ufp4.ufp4_head_loss(h, w, t, loss, lse, ws)
+        ufp4.ufp4_head_loss_backward(h, w, t, lse, dh, dw, ws)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for a, b in ((h, h2), (w, w2), (t, t2)):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    _check_forward(h2, w2, t2, loss, lse)
+    _check_backward(h2, w2, t2, dh, dw)
+
+
+@pytest.mark.parametrize("tokens", [1, 31, 127, 128, 129])
+@pytest.mark.parametrize("vocab", [33, 4000, 40001])
+def test_few_tokens(tokens, vocab):
+    """The tiles of up to 128 tokens: one or several per CTA, ragged widths, tokens in place."""
+    h, w, t = _inputs(tokens, vocab, 192, seed=tokens, ignored=0.3)
+    loss, lse = _forward(h, w, t)
+    _check_forward(h, w, t, loss, lse)
