@@ -275,48 +275,64 @@ struct PackParams {
 };
 
 // CTA b packs the valid tokens among its rows: it counts those before them,
-// then copies row by row.  Rows from the count up to the next multiple of
-// kStep are zeroed: dW sums over them.
+// then each warp copies a row at a time.  Rows from the count up to the next
+// multiple of kStep are zeroed: dW sums over them.
+constexpr int kPackRows = 64;  // most rows a CTA takes
 template <bool BACK>
 __global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
     __shared__ int before_s, all_s;
+    __shared__ int place[kPackRows];  // packed row of each of the CTA's rows, or -1
     griddep_wait();
     griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = (int64_t)blockIdx.x * p.rows_per_cta;
-    const int64_t r1 = min(r0 + p.rows_per_cta, p.T);
+    const int rows = (int)min((int64_t)p.rows_per_cta, p.T - r0);
+    auto valid = [&](int64_t r) {
+        const int64_t t = p.targets[r];
+        return t >= 0 && t < p.V;
+    };
     if (threadIdx.x == 0) before_s = all_s = 0;
     __syncthreads();
     int before = 0, all = 0;
+#pragma unroll 8
     for (int64_t r = threadIdx.x; r < p.T; r += blockDim.x) {
-        const int64_t t = p.targets[r];
-        const int v = t >= 0 && t < p.V;
+        const int v = valid(r);
         all += v;
         before += v && r < r0;
     }
     before = __reduce_add_sync(0xFFFFFFFFu, before);
     all = __reduce_add_sync(0xFFFFFFFFu, all);
-    if ((threadIdx.x & 31) == 0) {
+    if (lane == 0) {
         atomicAdd(&before_s, before);
         atomicAdd(&all_s, all);
     }
     __syncthreads();
     const int count = all_s;
+    if (warp == 0) {
+        int at = before_s;
+        for (int i = 0; i < rows; i += 32) {
+            const bool v = i + lane < rows && valid(r0 + i + lane);
+            const uint32_t which = __ballot_sync(0xFFFFFFFFu, v);
+            if (i + lane < rows) place[i + lane] = v ? at + __popc(which & ((1u << lane) - 1)) : -1;
+            at += __popc(which);
+        }
+    }
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0) *p.count = count;
         for (int i = threadIdx.x; i < p.launches; i += blockDim.x) p.next[i] = 0;
     }
-    auto clear_row = [&](char* row, int64_t bytes) {  // 2-byte multiples, 2-byte aligned at least
-        for (int64_t i = threadIdx.x; i < bytes / 2; i += blockDim.x) reinterpret_cast<uint16_t*>(row)[i] = 0;
+    __syncthreads();
+    auto clear_row = [&](char* row, int64_t bytes) {  // a warp's; 2-byte multiples, 2-byte aligned at least
+        for (int64_t i = lane; i < bytes / 2; i += 32) reinterpret_cast<uint16_t*>(row)[i] = 0;
     };
-    int at = before_s;
-    for (int64_t r = r0; r < r1; ++r) {
-        const int64_t t = p.targets[r];
-        const bool valid = t >= 0 && t < p.V;
-        if (!valid) {
+    for (int i = warp; i < rows; i += 8) {
+        const int64_t r = r0 + i;
+        const int at = place[i];
+        if (at < 0) {
             if (BACK) {
                 const int es = p.dh_f32 ? 4 : 2;
                 if (p.dh) clear_row((char*)p.dh + r * p.ld_dh * es, p.K * es);
-            } else if (threadIdx.x == 0) {
+            } else if (lane == 0) {
                 p.loss[r] = 0.0f;
                 p.lse_out[r] = 0.0f;
             }
@@ -324,14 +340,15 @@ __global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
         }
         const uint4* src = reinterpret_cast<const uint4*>(p.h + r * p.ldh);
         uint4* dst = reinterpret_cast<uint4*>(p.packed + (int64_t)at * p.Kp);
-        for (int64_t i = threadIdx.x; i < p.K / 8; i += blockDim.x) dst[i] = src[i];
-        if (threadIdx.x < p.K % 8) {  // nothing past a row's K elements is read
-            const int64_t i = p.K / 8 * 8 + threadIdx.x;
-            p.packed[(int64_t)at * p.Kp + i] = p.h[r * p.ldh + i];
+#pragma unroll 8
+        for (int64_t j = lane; j < p.K / 8; j += 32) dst[j] = src[j];
+        if (lane < p.K % 8) {  // nothing past a row's K elements is read
+            const int64_t j = p.K / 8 * 8 + lane;
+            p.packed[(int64_t)at * p.Kp + j] = p.h[r * p.ldh + j];
         }
-        if (threadIdx.x == 0) {
+        if (lane == 0) {
             p.index[at] = (int)r;
-            RowInfo info = {0.0f, 0.0f, 0.0f, (int)t};
+            RowInfo info = {0.0f, 0.0f, 0.0f, (int)p.targets[r]};
             if (BACK) {
                 const float l = p.lse[r], w = p.weight ? p.weight[r] : 1.0f;
                 info.lse2 = l * kLog2e;
@@ -340,11 +357,10 @@ __global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
             }
             p.info[at] = info;
         }
-        ++at;
     }
     if (BACK) {
         const int end = (count + kStep - 1) / kStep * kStep;
-        for (int z = count + blockIdx.x; z < end; z += gridDim.x)
+        for (int z = count + blockIdx.x * 8 + warp; z < end; z += gridDim.x * 8)
             clear_row((char*)(p.packed + (int64_t)z * p.Kp), p.Kp * 2);
     }
 }
@@ -969,7 +985,7 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
     p.dh = a.dh;
     p.ld_dh = a.ld_dh;
     p.dh_f32 = a.dh_f32;
-    p.rows_per_cta = (int)std::max<int64_t>(1, (a.T + 4ll * num_sms - 1) / (4ll * num_sms));
+    p.rows_per_cta = (int)std::min<int64_t>(kPackRows, std::max<int64_t>(8, (a.T + 2ll * num_sms - 1) / (2ll * num_sms)));
     const unsigned grid = (unsigned)std::max<int64_t>(1, (a.T + p.rows_per_cta - 1) / p.rows_per_cta);
     return back ? launch_pdl(head_pack_kernel<true>, dim3(grid), dim3(256), 0, st, p)
                 : launch_pdl(head_pack_kernel<false>, dim3(grid), dim3(256), 0, st, p);
