@@ -15,7 +15,7 @@
 // and sum of exponentials, joined in the tiles' order by a last kernel.
 // Backward, the vocabulary is walked in pieces: a piece's logits are computed
 // again, become dl (bf16) in a workspace of two pieces, and are multiplied
-// into dH (fp32 across the pieces) and dW.  Recomputing costs 2 of the 8
+// into dH (fp32 until the last piece) and dW.  Recomputing costs 2 of the 8
 // products-and-sums per logit; keeping the logits would cost 4 bytes each.
 //
 // dl is rounded to bf16 because the tensor cores multiply it with bf16 W and H:
@@ -75,7 +75,9 @@ struct Cfg {
     static constexpr int kA = kKps * kAtom, kB = kKps * kAtomB;
     static constexpr int kOffA = 0;
     static constexpr int kOffB = kStages * kA;
-    static constexpr int kOffBars = kOffB + kStages * kB;
+    static constexpr int kOffOut = kOffB + kStages * kB;  // 4 KB of results for each epilogue warp
+    static constexpr int kOut = PAIR ? 4 * 4096 : 0;
+    static constexpr int kOffBars = kOffOut + kOut;
     // full, empty; accumulators full x2, empty x2; ring full, empty; drain
     static constexpr int kNumBars = 2 * kStages + 4 + 2 * kRing + 1;
     static constexpr int kOffWords = kOffBars + 8 * kNumBars;  // tensor memory address, abort flag, ring of tiles
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = (int64_t)blockIdx.x * p.rows_per_cta;
-    const int rows = (int)min((int64_t)p.rows_per_cta, p.T - r0);
+    const int rows = (int)min((int64_t)p.rows_per_cta, p.T - r0);  // none in CTAs past the tokens
     auto valid = [&](int64_t r) {
         const int64_t t = p.targets[r];
         return t >= 0 && t < p.V;
@@ -323,7 +325,9 @@ __global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
     }
     __syncthreads();
     auto clear_row = [&](char* row, int64_t bytes) {  // a warp's; 2-byte multiples, 2-byte aligned at least
-        for (int64_t i = lane; i < bytes / 2; i += 32) reinterpret_cast<uint16_t*>(row)[i] = 0;
+        const int64_t wide = (uintptr_t)row % 16 == 0 ? bytes / 16 : 0;
+        for (int64_t i = lane; i < wide; i += 32) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+        for (int64_t i = wide * 8 + lane; i < bytes / 2; i += 32) reinterpret_cast<uint16_t*>(row)[i] = 0;
     };
     for (int i = warp; i < rows; i += 8) {
         const int64_t r = r0 + i;
@@ -381,7 +385,9 @@ struct Job {
     int width;              // columns of a tile: kTile, or less for single CTAs (a multiple of 16, up to kAlone)
     int m, n, k;            // extents; kernel-side: m (or k for kDW) comes from the token count
     int v0;                 // first vocabulary row of the piece
-    int first, last;        // kDH: first and last piece
+    int add;                // kDH: add to what earlier pieces left
+    int slices, per;        // kDH: shares of the sum that tiles of their own take, and steps in each
+    int slice0;             // kDH: index of the piece's first share
     __nv_bfloat16* dl;      // kGrad: output
     int64_t ld_dl;
 };
@@ -406,8 +412,9 @@ struct HeadParams {
     float2* part;           // kStats: [row][vocabulary tile]
     int64_t ld_part;
     float* target_logit;
-    float* dh_acc;          // fp32 across the pieces: packed rows x Kp
-    int64_t Kp;
+    float* dh_acc;          // fp32 dH of the packed rows (x Kp), or each share of it; null: dH is written at once
+    int64_t Kp, Tp;
+    int shares;
     const float* scale;
     void* dh;
     int64_t ld_dh;
@@ -418,7 +425,8 @@ struct HeadParams {
 };
 
 struct TileAt {
-    int job, m, n, k_steps;
+    int job, m, n, k0, k_steps;  // k0: first step
+    int slice;
 };
 
 // Tile rows that advance before the column does.  Tiles in flight walk the
@@ -441,7 +449,7 @@ struct Walk {
             m_tiles[j] = (m + ROWS - 1) / ROWS;
             n_tiles[j] = (q.n + q.width - 1) / q.width;
             k_steps[j] = (k + kStep - 1) / kStep;
-            total += m_tiles[j] * n_tiles[j];
+            total += m_tiles[j] * n_tiles[j] * q.slices;
         }
     }
     __device__ __forceinline__ TileAt at(const HeadParams& p, int tile) const {
@@ -449,7 +457,7 @@ struct Walk {
         t.job = 0;
 #pragma unroll
         for (int j = 0; j + 1 < kMaxJobs; ++j) {
-            const int here = m_tiles[j] * n_tiles[j];
+            const int here = m_tiles[j] * n_tiles[j] * p.job[j].slices;
             if (t.job == j && tile >= here) {
                 tile -= here;
                 t.job = j + 1;
@@ -464,7 +472,12 @@ struct Walk {
                 nt = n_tiles[j];
                 t.k_steps = k_steps[j];
             }
-        const int group = min(p.job[t.job].group, mt);
+        const Job& q = p.job[t.job];
+        t.slice = q.slices > 1 ? tile / (mt * nt) : 0;
+        tile -= t.slice * mt * nt;
+        t.k0 = t.slice * q.per;
+        if (q.slices > 1) t.k_steps = max(0, min(q.per, t.k_steps - t.k0));
+        const int group = min(q.group, mt);
         const int span = group * nt, g = tile / span, first = g * group;
         const int rows = min(group, mt - first), l = tile - g * span;
         t.n = l / rows;
@@ -473,38 +486,104 @@ struct Walk {
     }
 };
 
-// Stores 32 fp32 results of one row as bf16 or fp32 (added to what is there
-// when ADD), columns c .. c + 31 of which n exist.
-__device__ __forceinline__ void store_row(void* base, int64_t off, bool f32, bool add, int n, const float r[32]) {
-    if (f32) {
-        float* d = (float*)base + off;
-        if (n >= 32 && ((uintptr_t)d & 15) == 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                float4 v = make_float4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-                if (add) {
-                    const float4 o = *reinterpret_cast<const float4*>(d + i);
-                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-                }
-                *reinterpret_cast<float4*>(d + i) = v;
-            }
-        } else {
-            for (int i = 0; i < 32; ++i)
-                if (i < n) d[i] = add ? d[i] + r[i] : r[i];
-        }
-        return;
-    }
-    __nv_bfloat16* d = (__nv_bfloat16*)base + off;
-    if (n >= 32 && ((uintptr_t)d & 15) == 0) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(d + i) = make_uint4(pack_bf16(r[i], r[i + 1]), pack_bf16(r[i + 2], r[i + 3]),
-                                                          pack_bf16(r[i + 4], r[i + 5]), pack_bf16(r[i + 6], r[i + 7]));
-    } else {
-        for (int i = 0; i < 32; ++i)
-            if (i < n) d[i] = __float2bfloat16_rn(r[i]);
-    }
+// Where a tile's results go: rows of `ld` bytes (row i at index[i], where
+// given) up to `limit`, columns up to `cols`, as bf16 or fp32, added to what is
+// there with `add` (fp32).
+struct Dest {
+    char* base;
+    int64_t ld;
+    int limit, cols;
+    bool f32, add, fast;  // fast: rows are 16-byte aligned
+    const int* index;
+    __device__ __forceinline__ char* row(int r) const { return base + (index ? index[r] : r) * ld; }
+};
+__device__ __forceinline__ Dest make_dest(void* base, int64_t ld, int limit, int cols, bool f32, bool add,
+                                          const int* index) {
+    const int64_t bytes = ld * (f32 ? 4 : 2);
+    return {(char*)base, bytes, limit, cols, f32, add, (((uintptr_t)base | (uintptr_t)bytes) & 15) == 0, index};
 }
+
+// Writes a warp's 32 rows of a tile.  A lane holds a row, so its own stores
+// would touch 32 rows at a time, half a sector each; instead 128 bytes of every
+// row are turned around in `stage` (16-byte units, unit u of row i at
+// u ^ (i & 7)) and stored four whole rows of them an instruction.  Ragged or
+// unaligned columns go out of the lanes' registers.
+struct Writer {
+    Dest d;
+    uint8_t* stage;
+    char* rows[8];  // the rows that this lane stores, from its 16 bytes on; null past the limit
+    char* mine;     // the lane's own row
+    __device__ __forceinline__ Writer(const Dest& dest, uint8_t* stage_, int row0) : d(dest), stage(stage_) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = row0 + i * 4 + (lane >> 3);
+            rows[i] = r < d.limit ? d.row(r) + (lane & 7) * 16 : nullptr;
+        }
+        mine = row0 + lane < d.limit ? d.row(row0 + lane) : nullptr;
+    }
+    // 128 bytes of each row from the stage, at byte `at` of the rows.
+    __device__ __forceinline__ void flush(int64_t at) const {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + (lane >> 3);
+            v[i] = reinterpret_cast<const uint4*>(stage + row * 128)[(lane & 7) ^ (row & 7)];
+        }
+        if (d.add) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (rows[i]) {
+                    const uint4 o = *reinterpret_cast<const uint4*>(rows[i] + at);
+                    v[i] = make_uint4(__float_as_uint(__uint_as_float(v[i].x) + __uint_as_float(o.x)),
+                                      __float_as_uint(__uint_as_float(v[i].y) + __uint_as_float(o.y)),
+                                      __float_as_uint(__uint_as_float(v[i].z) + __uint_as_float(o.z)),
+                                      __float_as_uint(__uint_as_float(v[i].w) + __uint_as_float(o.w)));
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (rows[i]) *reinterpret_cast<uint4*>(rows[i] + at) = v[i];
+        __syncwarp();
+    }
+    // Columns c .. c + 31 of the tile from column n0 on, in turn for c = 0, 32, ... (r: of the lane's row).
+    __device__ __forceinline__ void columns(int n0, int c, const float r[32]) const {
+        const int lane = threadIdx.x & 31;
+        uint4* unit = reinterpret_cast<uint4*>(stage + lane * 128);
+        if (d.f32) {
+            if (d.fast && n0 + c + 32 <= d.cols) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    unit[u ^ (lane & 7)] = make_uint4(__float_as_uint(r[4 * u]), __float_as_uint(r[4 * u + 1]),
+                                                      __float_as_uint(r[4 * u + 2]), __float_as_uint(r[4 * u + 3]));
+                flush((int64_t)(n0 + c) * 4);
+                return;
+            }
+        } else if (d.fast && n0 + (c & ~63) + 64 <= d.cols) {
+            const int half = c & 32 ? 4 : 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                unit[(half + u) ^ (lane & 7)] =
+                    make_uint4(pack_bf16(r[8 * u], r[8 * u + 1]), pack_bf16(r[8 * u + 2], r[8 * u + 3]),
+                               pack_bf16(r[8 * u + 4], r[8 * u + 5]), pack_bf16(r[8 * u + 6], r[8 * u + 7]));
+            if (half) flush((int64_t)(n0 + c - 32) * 2);
+            return;
+        }
+        if (!mine) return;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int col = n0 + c + i;
+            if (col < d.cols) {
+                if (d.f32)
+                    ((float*)mine)[col] = d.add ? ((float*)mine)[col] + r[i] : r[i];
+                else
+                    ((__nv_bfloat16*)mine)[col] = __float2bfloat16_rn(r[i]);
+            }
+        }
+    }
+};
 
 // The logits epilogue of one row of a tile: running maximum and sum.
 __device__ __forceinline__ void stats_chunk(float r[32], int n, float& m, float& s) {
@@ -630,7 +709,8 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             const int r0 = is_a ? t.m * C::kRows + peer * kHalf
                                 : t.n * q.width + peer * C::kBRows + (q.b_mn ? 0 : q.v0);
             const int tx = PAIR ? 4 * kAtom : kAtom + q.width * 128;  // bytes of one step, of both CTAs
-            const int kb = !is_a && q.kind == kDH ? q.v0 : 0;  // first summed row of W
+            // first summed element; of W, counted from its first row
+            const int kb = t.k0 * kStep + (!is_a && q.kind == kDH ? q.v0 : 0);
             for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
                 if (!mbar_wait(empty_bar(s), ph ^ 1u)) {
                     *abort_flag = 1;
@@ -746,53 +826,43 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                     p.part[row * p.ld_part + t.n] = make_float2(m, sum);
                     if (target >= n0 && target < n0 + q.width) p.target_logit[row] = hit;
                 }
-            } else if (q.kind == kGrad) {
-                RowInfo info = {0.0f, 0.0f, 0.0f, -1};
-                if (row < count) info = p.info[row];
-                uint4* dst = reinterpret_cast<uint4*>(q.dl + (int64_t)row * q.ld_dl + n0);
-                for (int c = 0; c < kTile; c += 32) {
-                    tmem_ld32(acc + c, r);
-                    const int at = info.target - q.v0 - (n0 + c);
-                    const int n = row < count ? q.n - (n0 + c) : 0;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float v = info.a * ex2(fmaf(r[i], kLog2e, -info.lse2));
-                        if (at == i) v -= info.weight;
-                        r[i] = i < n ? v : 0.0f;  // ignored rows and columns past the vocabulary
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[c / 8 + i] = make_uint4(pack_bf16(r[8 * i], r[8 * i + 1]), pack_bf16(r[8 * i + 2], r[8 * i + 3]),
-                                                    pack_bf16(r[8 * i + 4], r[8 * i + 5]), pack_bf16(r[8 * i + 6], r[8 * i + 7]));
-                }
-            } else if (q.kind == kDH) {
-                const int64_t token = row < count ? p.index[row] : 0;
-                for (int c = 0; c < kTile; c += 32) {
-                    tmem_ld32(acc + c, r);
-                    const int n = row < count ? q.n - (n0 + c) : 0;
-                    if (n <= 0) continue;
-                    float* keep = p.dh_acc + (int64_t)row * p.Kp + n0 + c;
-                    if (!q.first) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < n) r[i] += keep[i];
-                    }
-                    if (q.last) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] *= scale;
-                        store_row(p.dh, token * p.ld_dh + n0 + c, p.dh_f32, false, n, r);
-                    } else {
-                        store_row(keep, 0, true, false, n, r);
-                    }
-                }
             } else {
+                // a piece's dl whole (zeros beside the valid rows and columns: dH and dW sum over them);
+                // dH of the valid rows; rows of dW
+                RowInfo info = {0.0f, 0.0f, 0.0f, -1};
+                float factor = scale;
+                Dest d;
+                if (q.kind == kGrad) {
+                    if (row < count) info = p.info[row];
+                    d = make_dest(q.dl, q.ld_dl, 1 << 30, 1 << 30, false, false, nullptr);
+                } else if (q.kind == kDW) {
+                    d = make_dest((char*)p.dw + (int64_t)q.v0 * p.ld_dw * (p.dw_f32 ? 4 : 2), p.ld_dw, q.m, q.n, p.dw_f32,
+                                  p.accumulate, nullptr);
+                } else if (p.dh_acc) {
+                    factor = 1.0f;
+                    d = make_dest(p.dh_acc + (int64_t)(q.slice0 + t.slice) * p.Tp * p.Kp, p.Kp, count, q.n, true, q.add,
+                                  nullptr);
+                } else {
+                    d = make_dest(p.dh, p.ld_dh, count, q.n, p.dh_f32, false, p.index);
+                }
+                const Writer out(d, gbase + C::kOffOut + q4 * 4096, row - lane);
+                const bool empty = t.k_steps == 0;  // a sum of nothing: 0, whatever tensor memory holds
                 for (int c = 0; c < kTile; c += 32) {
                     tmem_ld32(acc + c, r);
-                    const int n = row < q.m ? q.n - (n0 + c) : 0;
-                    if (n <= 0) continue;
+                    if (q.kind == kGrad) {
+                        const int at = info.target - q.v0 - (n0 + c);
+                        const int n = row < count ? q.n - (n0 + c) : 0;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = t.k_steps ? r[i] * scale : 0.0f;  // no valid token: no product
-                    store_row(p.dw, (int64_t)(q.v0 + row) * p.ld_dw + n0 + c, p.dw_f32, p.accumulate, n, r);
+                        for (int i = 0; i < 32; ++i) {
+                            float v = info.a * ex2(fmaf(r[i], kLog2e, -info.lse2));
+                            if (at == i) v -= info.weight;
+                            r[i] = i < n ? v : 0.0f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = empty ? 0.0f : r[i] * factor;
+                    }
+                    if (PAIR) out.columns(n0, c, r);
                 }
             }
             tc_fence_before();
@@ -844,6 +914,26 @@ __global__ void __launch_bounds__(256) head_join_kernel(const HeadParams p, int 
     loss[token] = valid ? fmaf(z * l, l, l - p.target_logit[row]) : 0.0f;
 }
 
+// dH from the fp32 sums of the packed rows, or their shares in order, 256
+// columns of a row a CTA.
+__global__ void __launch_bounds__(256) head_dh_kernel(const HeadParams p, int cols) {
+    griddep_wait();
+    griddep_launch();
+    const int row = blockIdx.x, c = blockIdx.y * 256 + threadIdx.x;
+    if (row >= *p.count || c >= cols) return;
+    const float* part = p.dh_acc + row * p.Kp + c;
+    const int64_t step = p.Tp * p.Kp;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < p.shares; ++i) s += part[i * step];
+    if (p.scale) s *= *p.scale;
+    const int64_t out = (int64_t)p.index[row] * p.ld_dh + c;
+    if (p.dh_f32)
+        ((float*)p.dh)[out] = s;
+    else
+        ((__nv_bfloat16*)p.dh)[out] = __float2bfloat16_rn(s);
+}
+
 // ------------------------------------------------------------------- host
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
@@ -852,6 +942,7 @@ struct Plan {
     int64_t Tp, Kp;          // packed rows and columns
     int64_t pieces, piece;   // backward: vocabulary pieces and their width (a multiple of kTile)
     int64_t launches;        // of the product kernel
+    int64_t slices;          // backward: shares of a piece's dH
     bool direct;             // forward: tokens in place, none packed
     int64_t width, tiles;    // forward: columns of a tile, tiles of the vocabulary
     size_t count, next, index, info, packed, part, target, dl[2], acc, total;
@@ -863,6 +954,20 @@ struct Plan {
 // loss + gradients of 4096 x 65536 x 7168 take 8.9, 8.7 and 8.65 ms with 64,
 // 128 and 256 MB, of 2047 x 50001 x 2048 (a third ignored) 887, 815 and 780 us.
 constexpr int64_t kPieceBytes = 256ll << 20;
+
+// dH has few tiles, each with a long sum, where there are few tokens (16
+// tokens, K = 2048: 8 tiles of 500 steps for a vocabulary of 32000).  The sum
+// is then shared out so that no tile takes more than half of what a cluster
+// takes of the launch, up to kMostShares and 256 MB of fp32 shares.
+constexpr int64_t kMostShares = 32;
+int64_t dh_slices(int64_t T, int64_t K, int64_t piece, int64_t pieces, int num_sms) {
+    const int64_t mt = up(T, kTile) / kTile, vt = piece / kTile, kt = up(K, kTile) / kTile;
+    const int64_t ts = up(T, kStep) / kStep, vs = piece / kStep, ks = up(K, kStep) / kStep;
+    const int64_t steps = mt * kt * vs + vt * kt * ts + (pieces > 1 ? mt * vt * ks : 0);
+    const int64_t share = std::max<int64_t>(8, steps / std::max(1, num_sms / 2) / 2);  // of a cluster, halved
+    const int64_t most = std::min<int64_t>(kMostShares, (256ll << 20) / std::max<int64_t>(1, 4 * pieces * mt * kTile * up(K, 8)));
+    return std::max<int64_t>(1, std::min((vs + share - 1) / share, most));
+}
 
 Plan make_plan(int64_t T, int64_t V, int64_t K, bool back, int num_sms) {
     Plan p = {};
@@ -889,7 +994,9 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back, int num_sms) {
     if (back) {
         p.dl[0] = take(2 * p.Tp * p.piece);
         p.dl[1] = p.pieces > 1 ? take(2 * p.Tp * p.piece) : p.dl[0];
-        p.acc = p.pieces > 1 ? take(4 * p.Tp * p.Kp) : 0;
+        p.slices = dh_slices(T, K, p.piece, p.pieces, num_sms);
+        const int64_t shares = p.slices > 1 ? p.slices * p.pieces : (p.pieces > 1 ? 1 : 0);
+        p.acc = shares ? take(4 * p.Tp * p.Kp * shares) : 0;
     } else {
         // up to kHalf tokens: one tile a CTA and round, all CTAs busy
         p.direct = T <= kHalf;
@@ -953,7 +1060,7 @@ cudaError_t run_gemm(const HeadMaps& maps, HeadParams& p, int64_t T, cudaStream_
     int64_t tiles = 0;  // with every token valid
     for (int j = 0; j < p.jobs; ++j) {
         const Job& q = p.job[j];
-        tiles += up(q.kind == kDW ? q.m : T, C::kRows) / C::kRows * (up(q.n, q.width) / q.width);
+        tiles += up(q.kind == kDW ? q.m : T, C::kRows) / C::kRows * (up(q.n, q.width) / q.width) * q.slices;
     }
     if (tiles > 0x3FFFFFFF) return cudaErrorNotSupported;
     cfg.gridDim = dim3(ctas * (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, most)));
@@ -985,8 +1092,8 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
     p.dh = a.dh;
     p.ld_dh = a.ld_dh;
     p.dh_f32 = a.dh_f32;
-    p.rows_per_cta = (int)std::min<int64_t>(kPackRows, std::max<int64_t>(8, (a.T + 2ll * num_sms - 1) / (2ll * num_sms)));
-    const unsigned grid = (unsigned)std::max<int64_t>(1, (a.T + p.rows_per_cta - 1) / p.rows_per_cta);
+    p.rows_per_cta = (int)std::min<int64_t>(kPackRows, std::max<int64_t>(2, (a.T + 2ll * num_sms - 1) / (2ll * num_sms)));
+    const unsigned grid = (unsigned)std::max<int64_t>(8, (a.T + p.rows_per_cta - 1) / p.rows_per_cta);
     return back ? launch_pdl(head_pack_kernel<true>, dim3(grid), dim3(256), 0, st, p)
                 : launch_pdl(head_pack_kernel<false>, dim3(grid), dim3(256), 0, st, p);
 }
@@ -1015,7 +1122,7 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
     p.part = (float2*)(ws + pl.part);
     p.target_logit = (float*)(ws + pl.target);
     p.ld_part = pl.tiles;
-    p.dh_acc = (float*)(ws + pl.acc);
+    p.dh_acc = pl.pieces > 1 || pl.slices > 1 ? (float*)(ws + pl.acc) : nullptr;
     p.Kp = pl.Kp;
     p.scale = a.scale;
     p.dh = a.dh;
@@ -1025,7 +1132,12 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
     p.ld_dw = a.ld_dw;
     p.dw_f32 = a.dw_f32;
     p.accumulate = a.accumulate;
-    for (Job& q : p.job) q.width = kTile;
+    p.Tp = pl.Tp;
+    p.shares = pl.slices > 1 ? (int)(pl.slices * pl.pieces) : 1;
+    for (Job& q : p.job) {
+        q.width = kTile;
+        q.slices = 1;
+    }
     if (pl.direct) {
         p.count = nullptr;
         p.tokens = (int)a.T;
@@ -1084,8 +1196,10 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
             h.n = (int)a.K;
             h.k = width(i);
             h.v0 = (int)(i * pl.piece);
-            h.first = i == 0;
-            h.last = i == pl.pieces - 1;
+            h.add = i > 0 && pl.slices == 1;
+            h.slices = (int)pl.slices;
+            h.per = (int)((up(width(i), kStep) / kStep + pl.slices - 1) / pl.slices);
+            h.slice0 = pl.slices > 1 ? (int)(i * pl.slices) : 0;
         }
         if (i >= 0 && a.dw) {
             Job& w = p.job[p.jobs++];
@@ -1111,10 +1225,12 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
         p.next += i + 1;
         // the longest tiles first, so that the launch ends on short ones
         std::sort(p.job, p.job + p.jobs, [&](const Job& x, const Job& y) {
-            return (x.kind == kDW ? a.T : x.k) > (y.kind == kDW ? a.T : y.k);
+            return (x.kind == kDW ? a.T : x.k / x.slices) > (y.kind == kDW ? a.T : y.k / y.slices);
         });
         if (p.jobs) e = run_gemm<true>(maps, p, a.T, st);
     }
+    if (e == cudaSuccess && a.dh && (pl.pieces > 1 || pl.slices > 1))
+        e = launch_pdl(head_dh_kernel, dim3((unsigned)a.T, (unsigned)((a.K + 255) / 256)), dim3(256), 0, st, make_params(a, pl), (int)a.K);
     return e;
 }
 
@@ -1131,6 +1247,7 @@ cudaError_t preload_head_kernels() {
     cudaFuncGetAttributes(&at, head_pack_kernel<true>);
     cudaFuncGetAttributes(&at, head_gemm_kernel<true>);
     cudaFuncGetAttributes(&at, head_gemm_kernel<false>);
+    cudaFuncGetAttributes(&at, head_dh_kernel);
     return cudaFuncGetAttributes(&at, head_join_kernel);
 }
 
