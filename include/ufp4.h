@@ -474,7 +474,8 @@ ufp4_status ufp4_glu_backward(const void* dy, int64_t ld_dy, int32_t dy_dtype, c
                               int64_t ld_dgate, void* dup, int64_t ld_dup, void* y, int64_t ldy, cudaStream_t stream);
 
 /* ufp4_rms_norm -- residual add and RMS norm of each row: s = x + residual
- * (fp32), rstd = 1 / sqrt(mean(s^2) + eps), y = s rstd gamma.
+ * (fp32), rstd = 1 / sqrt(mean(s^2) + eps) (the mean in fp32: squares beyond its
+ * range make rstd 0), y = s rstd gamma.
  *   x         device bf16 or fp32 (x_dtype), leading dimension ldx
  *   residual  device bf16, leading dimension ld_residual, or NULL
  *   gamma     device bf16 or fp32 (gamma_dtype), cols elements

@@ -13,7 +13,11 @@
 // Every element is read and written once, so memory bounds both passes:
 // 8.06 bytes an element forward (bf16), 8.06 backward.  A thread carries 8
 // elements, four threads a checkpoint block, so a block's scale takes two
-// shuffles and nothing goes through shared memory.
+// shuffles and nothing goes through shared memory; no element waits for
+// another, so one short-lived thread an octet is enough to keep memory busy.
+// Measured on a GB300: forward 8192 x 5632 from fp32 83.9 us, 6.64 TB/s;
+// backward 16384 x 7168 from fp32 with y again 209.7 us, 6.75 TB/s (a plain
+// copy there: 6.78).  4109 x 1408 backward takes 12 us, 5 of them the launch.
 #include "ckpt8.cuh"
 #include "internal.h"
 #include "train.h"

@@ -11,7 +11,8 @@
 // Tokens without a target (ignored) take no part in any product: the first
 // kernel of either pass packs the rows of H that have one, so work goes with
 // the number of valid tokens, and whatever an ignored row holds stays out of
-// dW.  Forward, each 256 x 256 tile of logits leaves its rows' running maximum
+// dW.  (Up to 128 tokens, forward, are read where they lie: W is what that call
+// reads, and a logit's row meets no other.)  Forward, each 256 x 256 tile of logits leaves its rows' running maximum
 // and sum of exponentials, joined in the tiles' order by a last kernel.
 // Backward, the vocabulary is walked in pieces: a piece's logits are computed
 // again, become dl (bf16) in a workspace of two pieces, and are multiplied
@@ -826,7 +827,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                     p.part[row * p.ld_part + t.n] = make_float2(m, sum);
                     if (target >= n0 && target < n0 + q.width) p.target_logit[row] = hit;
                 }
-            } else {
+            } else if (PAIR) {  // single CTAs only take logits
                 // a piece's dl whole (zeros beside the valid rows and columns: dH and dW sum over them);
                 // dH of the valid rows; rows of dW
                 RowInfo info = {0.0f, 0.0f, 0.0f, -1};
@@ -862,7 +863,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] = empty ? 0.0f : r[i] * factor;
                     }
-                    if (PAIR) out.columns(n0, c, r);
+                    out.columns(n0, c, r);
                 }
             }
             tc_fence_before();
@@ -914,24 +915,26 @@ __global__ void __launch_bounds__(256) head_join_kernel(const HeadParams p, int 
     loss[token] = valid ? fmaf(z * l, l, l - p.target_logit[row]) : 0.0f;
 }
 
-// dH from the fp32 sums of the packed rows, or their shares in order, 256
-// columns of a row a CTA.
+// dH from the fp32 sums of the packed rows, or their shares in order: a row's
+// columns 256 at a time over the grid's second dimension.
 __global__ void __launch_bounds__(256) head_dh_kernel(const HeadParams p, int cols) {
     griddep_wait();
     griddep_launch();
-    const int row = blockIdx.x, c = blockIdx.y * 256 + threadIdx.x;
-    if (row >= *p.count || c >= cols) return;
-    const float* part = p.dh_acc + row * p.Kp + c;
-    const int64_t step = p.Tp * p.Kp;
-    float s = 0.0f;
+    const int row = blockIdx.x;
+    if (row >= *p.count) return;
+    const float scale = p.scale ? *p.scale : 1.0f;
+    const int64_t out = (int64_t)p.index[row] * p.ld_dh, step = p.Tp * p.Kp;
+    for (int64_t c = blockIdx.y * 256 + threadIdx.x; c < cols; c += gridDim.y * 256) {
+        const float* part = p.dh_acc + row * p.Kp + c;
+        float s = 0.0f;
 #pragma unroll 8
-    for (int i = 0; i < p.shares; ++i) s += part[i * step];
-    if (p.scale) s *= *p.scale;
-    const int64_t out = (int64_t)p.index[row] * p.ld_dh + c;
-    if (p.dh_f32)
-        ((float*)p.dh)[out] = s;
-    else
-        ((__nv_bfloat16*)p.dh)[out] = __float2bfloat16_rn(s);
+        for (int i = 0; i < p.shares; ++i) s += part[i * step];
+        s *= scale;
+        if (p.dh_f32)
+            ((float*)p.dh)[out + c] = s;
+        else
+            ((__nv_bfloat16*)p.dh)[out + c] = __float2bfloat16_rn(s);
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -961,11 +964,11 @@ constexpr int64_t kPieceBytes = 256ll << 20;
 // takes of the launch, up to kMostShares and 256 MB of fp32 shares.
 constexpr int64_t kMostShares = 32;
 int64_t dh_slices(int64_t T, int64_t K, int64_t piece, int64_t pieces, int num_sms) {
-    const int64_t mt = up(T, kTile) / kTile, vt = piece / kTile, kt = up(K, kTile) / kTile;
+    const int64_t mt = std::max<int64_t>(1, up(T, kTile) / kTile), vt = piece / kTile, kt = up(K, kTile) / kTile;
     const int64_t ts = up(T, kStep) / kStep, vs = piece / kStep, ks = up(K, kStep) / kStep;
     const int64_t steps = mt * kt * vs + vt * kt * ts + (pieces > 1 ? mt * vt * ks : 0);
     const int64_t share = std::max<int64_t>(8, steps / std::max(1, num_sms / 2) / 2);  // of a cluster, halved
-    const int64_t most = std::min<int64_t>(kMostShares, (256ll << 20) / std::max<int64_t>(1, 4 * pieces * mt * kTile * up(K, 8)));
+    const int64_t most = std::min<int64_t>(kMostShares, (256ll << 20) / (4 * pieces * mt * kTile * up(K, 8)));
     return std::max<int64_t>(1, std::min((vs + share - 1) / share, most));
 }
 
@@ -1230,7 +1233,8 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
         if (p.jobs) e = run_gemm<true>(maps, p, a.T, st);
     }
     if (e == cudaSuccess && a.dh && (pl.pieces > 1 || pl.slices > 1))
-        e = launch_pdl(head_dh_kernel, dim3((unsigned)a.T, (unsigned)((a.K + 255) / 256)), dim3(256), 0, st, make_params(a, pl), (int)a.K);
+        e = launch_pdl(head_dh_kernel, dim3((unsigned)a.T, (unsigned)std::min<int64_t>((a.K + 255) / 256, 65535)), dim3(256),
+                       0, st, make_params(a, pl), (int)a.K);
     return e;
 }
 

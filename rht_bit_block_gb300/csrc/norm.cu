@@ -182,6 +182,7 @@ struct Stage {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
     }
 };
+
 // THREADS: the most a CTA has.
 template <bool F32, bool VEC, int ITER, int THREADS>
 __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) norm_kernel(const NormParams p) {
@@ -257,9 +258,9 @@ __device__ __forceinline__ void pair8(const float v[kVec], uint64_t o[4]) {
 
 // The backward pass has about twice the arithmetic of the forward one per byte,
 // so it works on pairs of fp32.
-
 template <bool F32, bool VEC, int ITER, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > kBackwardThreads ? 1 : kBackwardThreads / THREADS) norm_backward_kernel(const NormParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS > kBackwardThreads ? 1 : kBackwardThreads / THREADS)
+norm_backward_kernel(const NormParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float slots[32];
     griddep_wait();
