@@ -19,6 +19,13 @@
 // into dH (fp32 until the last piece) and dW.  Recomputing costs 2 of the 8
 // products-and-sums per logit; keeping the logits would cost 4 bytes each.
 //
+// The tensor cores bound it from about a thousand tokens on: 8192 tokens (a
+// tenth ignored) x 50001 x 2048 forward 0.88 ms when run without a pause, 1720
+// TFLOP/s, and 4096 x 65536 x 7168 with the gradients 9.0 ms, 1710 TFLOP/s with
+// the recomputed logits (the library's bf16 product sustains 1714 there, and
+// 1924 in a burst).  With few tokens it is W: 16 tokens x 65536 x 7168 forward
+// 150 us, 6.3 TB/s.
+//
 // dl is rounded to bf16 because the tensor cores multiply it with bf16 W and H:
 // a relative error of at most 2^-8 per entry, as the outputs' own rounding,
 // and unbiased; the common factor `scale` is applied to the fp32 results, so
@@ -52,8 +59,8 @@ constexpr int kAlone = 224;                // most columns of a single CTA's til
 constexpr int kStep = 64;                  // summed elements per step (one 128-byte swizzle row)
 constexpr int kBlockBytes = 64 * 64 * 2;   // 64 rows of 64 bf16: one column block of an MN-major operand
 constexpr int kAtom = 2 * kBlockBytes;     // 128 rows of one step
-constexpr int kThreads = 256;
-constexpr int kRing = 3;                   // tiles handed out ahead
+constexpr int kThreads = 384;
+constexpr int kRing = 4;                   // tiles handed out ahead (even: a place serves one epilogue group)
 constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sleep up to kSuspendNs
 constexpr uint32_t kSuspendNs = 1000;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -76,8 +83,8 @@ struct Cfg {
     static constexpr int kA = kKps * kAtom, kB = kKps * kAtomB;
     static constexpr int kOffA = 0;
     static constexpr int kOffB = kStages * kA;
-    static constexpr int kOffOut = kOffB + kStages * kB;  // 4 KB of results for each epilogue warp
-    static constexpr int kOut = PAIR ? 4 * 4096 : 0;
+    static constexpr int kOffOut = kOffB + kStages * kB;  // 4 KB for each epilogue warp
+    static constexpr int kOut = PAIR ? 8 * 4096 : 0;
     static constexpr int kOffBars = kOffOut + kOut;
     // full, empty; accumulators full x2, empty x2; ring full, empty; drain
     static constexpr int kNumBars = 2 * kStages + 4 + 2 * kRing + 1;
@@ -603,7 +610,9 @@ __device__ __forceinline__ void stats_chunk(float r[32], int n, float& m, float&
 
 // Warps 0 and 2 copy A and B (one thread each: a single thread issuing both is
 // 5 % slower), warp 1 of the leader issues the MMAs, warp 3 of the leader hands
-// out tiles, warps 4 to 7 run the epilogue.  Tiles differ in length by an order
+// out tiles, warps 4 to 7 and 8 to 11 run the epilogues of even and odd tiles
+// (each with its accumulator: where a tile has few steps, as dW of few tokens,
+// its epilogue is what takes the time).  Tiles differ in length by an order
 // of magnitude between products, so clusters take the next one from a counter
 // in global memory when they have room for it; which cluster computes a tile
 // changes nothing in its result.
@@ -643,11 +652,11 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), 1);             // the leader's commit
-            mbar_init(acce_bar(b), PAIR ? 8 : 4);  // the epilogue warps
+            mbar_init(acce_bar(b), PAIR ? 8 : 4);  // one group of epilogue warps
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(ringf_bar(i), 1);               // the leader's warp 3
-            mbar_init(ringe_bar(i), PAIR ? 13 : 7);   // two copiers and four epilogue warps a CTA, the MMA issuer
+            mbar_init(ringe_bar(i), PAIR ? 13 : 7);   // two copiers and a group of four epilogue warps a CTA, the issuer
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -680,7 +689,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
 
     if (warp == 3 && lane == 0 && peer == 0) {
         // ------------------------------------------------ hands out tiles (leader only)
-        for (int i = 0;; ++i) {
+        for (int i = 0, ends = 0; ends < 2; ++i) {  // an end for either epilogue group
             const int at = i % kRing;
             if (!mbar_wait_cluster(ringe_bar(at), ((i / kRing) & 1) ^ 1)) {
                 *abort_flag = 1;
@@ -692,7 +701,8 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 st_cluster(map_to_rank(slot, r), tile);
                 mbar_arrive_cluster(map_to_rank(ringf_bar(at), r));
             }
-            if (tile >= walk.total || *abort_flag) break;
+            ends += tile >= walk.total;
+            if (*abort_flag) break;
         }
     } else if ((warp == 0 || warp == 2) && lane == 0) {
         // ---------------------------------------------------- TMA copies (both CTAs)
@@ -785,9 +795,9 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         mbar_wait(drain_bar, 0);
     } else if (warp >= 4) {
         // ------------------------------------------------- epilogue (both CTAs)
-        const int q4 = warp - 4;
+        const int q4 = warp & 3;
         const float scale = p.scale ? *p.scale : 1.0f;
-        for (int tc = 0;; ++tc) {
+        for (int tc = (warp - 4) >> 2;; tc += 2) {
             const int tile = take(tc, false);  // every lane reads the tile, then one arrives
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(ringe_bar(tc % kRing), leader));
@@ -846,7 +856,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 } else {
                     d = make_dest(p.dh, p.ld_dh, count, q.n, p.dh_f32, false, p.index);
                 }
-                const Writer out(d, gbase + C::kOffOut + q4 * 4096, row - lane);
+                const Writer out(d, gbase + C::kOffOut + (warp - 4) * 4096, row - lane);
                 const bool empty = t.k_steps == 0;  // a sum of nothing: 0, whatever tensor memory holds
                 for (int c = 0; c < kTile; c += 32) {
                     tmem_ld32(acc + c, r);
