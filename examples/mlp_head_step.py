@@ -148,7 +148,7 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("tokens", 2048), ("hidden", 1024), ("ffn", 2816), ("vocab", 16384), ("steps", 20)):
         ap.add_argument("--" + name, type=int, default=value)
-    ap.add_argument("--rate", type=float, default=2.0)
+    ap.add_argument("--rate", type=float, default=0.05)
     a = ap.parse_args()
     model = Model(a.tokens, a.hidden, a.ffn, a.vocab)
     x, targets = data(a.tokens, a.hidden, a.vocab)

@@ -541,7 +541,9 @@ ufp4_status ufp4_head_loss(const void* h, int64_t ldh, const void* w, int64_t ld
  *              added to with accumulate_dw = 1 (fp32 only), or NULL; not both
  *              dh and dw NULL
  *   workspace  at least ufp4_head_loss_backward_workspace_size bytes,
- *              256-byte aligned */
+ *              256-byte aligned: dl of two pieces of the vocabulary (of 256 MB
+ *              or 256 columns each, or of one that is all of it), a copy of
+ *              the rows of h that have a target, and fp32 sums of dh */
 ufp4_status ufp4_head_loss_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, size_t* bytes);
 ufp4_status ufp4_head_loss_backward(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* targets,
                                     int64_t tokens, int64_t vocab, int64_t hidden, float z_loss, const float* lse,
