@@ -128,20 +128,25 @@ def _check(status: int, what: str):
         raise Ufp4Error(status, what)
 
 
-_raw_stream = None  # (device index) -> cudaStream_t of torch's current stream
+def _find_current_stream():
+    """The cudaStream_t of torch's current stream, asked for by its handle: a Stream object costs as much host
+    time as a launch.  The first call replaces itself by what the later ones need."""
+    global _current_stream
+    import torch
+    torch.cuda.current_device()  # initializes CUDA
+    raw, device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
+_current_stream = _find_current_stream
 
 
 def _stream(stream):
-    """The cudaStream_t of `stream`, by default torch's current one (asked for by its handle: a Stream object
-    costs as much host time as a launch)."""
-    global _raw_stream
-    if stream is not None:
-        return int(stream)
-    import torch
-    if _raw_stream is None:
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _raw_stream(torch.cuda.current_device())
+    return _current_stream() if stream is None else int(stream)
 
 
 def make_desc(grid="e1m2", block=(1, 16), n=16, sign_seed=0, rounding=ROUND_RTNE, sr_seed=0,
@@ -345,18 +350,20 @@ def _dtype(t, what: str) -> int:
     return code
 
 
-def _matrix(t, what: str, rows: int, cols: int, dtype=None):
-    """(pointer, leading dimension) of a 2-D tensor with unit column stride; (None, 0) of None."""
+def _matrix(t, what: str, shape, dtype=None):
+    """(pointer, leading dimension) of a 2-D tensor of that shape with unit column stride; (None, 0) of None."""
     if t is None:
         return None, 0
-    if t.shape != (rows, cols):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}: ({rows}, {cols}) is wanted")
+    if t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}: {tuple(shape)} is wanted")
     ld, step = t.stride()
-    if step != 1 and cols > 1:
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{what}'s rows are not contiguous")
     if dtype is not None and _code(t) != dtype:
         raise TypeError(f"{what} is {t.dtype}")
-    return t.data_ptr(), ld if rows > 1 or ld > cols else cols
+    if shape[0] < 2 and ld < shape[1]:  # the stride of a single row says nothing
+        ld = shape[1]
+    return t.data_ptr(), ld
 
 
 def _vector(t, what: str, n: int, code: int):
@@ -370,29 +377,25 @@ def _vector(t, what: str, n: int, code: int):
     return t.data_ptr()
 
 
-def _ref(q: QTensor | None):
-    return ctypes.byref(q) if q is not None else None
-
-
 def _act(act) -> int:
     return ACTS[act] if isinstance(act, str) else int(act)
 
 
 def ufp4_glu(gate, up, y, act="silu", ckpt_gate: QTensor | None = None, ckpt_up: QTensor | None = None, stream=None):
     """y = act(gate) * up; the 8-bit checkpoints of gate and up are written if both are given."""
-    rows, cols = gate.shape
+    shape = rows, cols = gate.shape
     dt = _dtype(gate, "gate")
-    _check(load().ufp4_glu(*_matrix(gate, "gate", rows, cols), *_matrix(up, "up", rows, cols, dt), dt, rows, cols,
-                           _act(act), *_matrix(y, "y", rows, cols, BF16), _ref(ckpt_gate), _ref(ckpt_up),
+    _check(load().ufp4_glu(*_matrix(gate, "gate", shape), *_matrix(up, "up", shape, dt), dt, rows, cols,
+                           _act(act), *_matrix(y, "y", shape, BF16), ckpt_gate, ckpt_up,
                            _stream(stream)), "ufp4_glu")
 
 
 def ufp4_glu_backward(dy, ckpt_gate: QTensor, ckpt_up: QTensor, dgate, dup, act="silu", y=None, stream=None):
     """dgate and dup of ufp4_glu at the checkpointed values, and act(gate) * up again into y if given."""
-    rows, cols = dy.shape
-    _check(load().ufp4_glu_backward(*_matrix(dy, "dy", rows, cols), _dtype(dy, "dy"), _ref(ckpt_gate), _ref(ckpt_up),
-                                    rows, cols, _act(act), *_matrix(dgate, "dgate", rows, cols, BF16),
-                                    *_matrix(dup, "dup", rows, cols, BF16), *_matrix(y, "y", rows, cols, BF16),
+    shape = rows, cols = dy.shape
+    _check(load().ufp4_glu_backward(*_matrix(dy, "dy", shape), _dtype(dy, "dy"), ckpt_gate, ckpt_up,
+                                    rows, cols, _act(act), *_matrix(dgate, "dgate", shape, BF16),
+                                    *_matrix(dup, "dup", shape, BF16), *_matrix(y, "y", shape, BF16),
                                     _stream(stream)), "ufp4_glu_backward")
 
 
@@ -400,13 +403,13 @@ def ufp4_rms_norm(x, gamma, y, rstd=None, residual=None, total=None, ckpt: QTens
                   stream=None):
     """y = RMS norm of x + residual times gamma; total (the bf16 sum), rstd and the 8-bit checkpoint of the sum are
     written if given."""
-    rows, cols = x.shape
+    shape = rows, cols = x.shape
     dt = _dtype(gamma, "gamma")
-    _check(load().ufp4_rms_norm(*_matrix(x, "x", rows, cols), _dtype(x, "x"),
-                                *_matrix(residual, "residual", rows, cols, BF16),
+    _check(load().ufp4_rms_norm(*_matrix(x, "x", shape), _dtype(x, "x"),
+                                *_matrix(residual, "residual", shape, BF16),
                                 _vector(gamma, "gamma", cols, dt), dt, rows, cols,
-                                eps, *_matrix(y, "y", rows, cols, BF16), *_matrix(total, "total", rows, cols, BF16),
-                                _vector(rstd, "rstd", rows, F32), _ref(ckpt), _stream(stream)), "ufp4_rms_norm")
+                                eps, *_matrix(y, "y", shape, BF16), *_matrix(total, "total", shape, BF16),
+                                _vector(rstd, "rstd", rows, F32), ckpt, _stream(stream)), "ufp4_rms_norm")
 
 
 def ufp4_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -419,14 +422,14 @@ def ufp4_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
 def ufp4_rms_norm_backward(dy, ckpt: QTensor, rstd, gamma, dx, dgamma, workspace, dtotal=None, y=None, stream=None):
     """dx and dgamma of ufp4_rms_norm at the checkpointed rows, dtotal added to dx if given, and the normalised rows
     again into y if given."""
-    rows, cols = dy.shape
+    shape = rows, cols = dy.shape
     dt = _dtype(gamma, "gamma")
-    _check(load().ufp4_rms_norm_backward(*_matrix(dy, "dy", rows, cols), _dtype(dy, "dy"), _ref(ckpt),
+    _check(load().ufp4_rms_norm_backward(*_matrix(dy, "dy", shape), _dtype(dy, "dy"), ckpt,
                                          _vector(rstd, "rstd", rows, F32),
                                          _vector(gamma, "gamma", cols, dt), dt,
-                                         *_matrix(dtotal, "dtotal", rows, cols, BF16), rows, cols,
-                                         *_matrix(dx, "dx", rows, cols, BF16), _vector(dgamma, "dgamma", cols, F32),
-                                         *_matrix(y, "y", rows, cols, BF16), workspace.data_ptr(),
+                                         *_matrix(dtotal, "dtotal", shape, BF16), rows, cols,
+                                         *_matrix(dx, "dx", shape, BF16), _vector(dgamma, "dgamma", cols, F32),
+                                         *_matrix(y, "y", shape, BF16), workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(), _stream(stream)),
            "ufp4_rms_norm_backward")
 
@@ -450,7 +453,7 @@ def ufp4_head_loss(h, w, targets, loss, lse, workspace, z_loss=0.0, stream=None)
     targets: int64; a target outside [0, vocab) gives loss and lse 0."""
     tokens, hidden = h.shape
     vocab = w.shape[0]
-    _check(load().ufp4_head_loss(*_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
+    _check(load().ufp4_head_loss(*_matrix(h, "h", (tokens, hidden), BF16), *_matrix(w, "w", (vocab, hidden), BF16),
                                  _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss,
                                  _vector(loss, "loss", tokens, F32), _vector(lse, "lse", tokens, F32),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -463,11 +466,11 @@ def ufp4_head_loss_backward(h, w, targets, lse, dh, dw, workspace, token_weight=
     tokens, hidden = h.shape
     vocab = w.shape[0]
     _check(load().ufp4_head_loss_backward(
-        *_matrix(h, "h", tokens, hidden, BF16), *_matrix(w, "w", vocab, hidden, BF16),
+        *_matrix(h, "h", (tokens, hidden), BF16), *_matrix(w, "w", (vocab, hidden), BF16),
         _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss,
         _vector(lse, "lse", tokens, F32), _vector(token_weight, "token_weight", tokens, F32),
-        _vector(scale, "scale", 1, F32), *_matrix(dh, "dh", tokens, hidden),
-        BF16 if dh is None else _dtype(dh, "dh"), *_matrix(dw, "dw", vocab, hidden),
+        _vector(scale, "scale", 1, F32), *_matrix(dh, "dh", (tokens, hidden)),
+        BF16 if dh is None else _dtype(dh, "dh"), *_matrix(dw, "dw", (vocab, hidden)),
         BF16 if dw is None else _dtype(dw, "dw"), int(accumulate_dw), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream)), "ufp4_head_loss_backward")
 
