@@ -22,17 +22,24 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "internal.h"
 #include "train.h"
+#include "ufp4_device.cuh"
 
 namespace ufp4 {
 
 constexpr int kCkptBlock = 32;  // elements per scale
 constexpr int kVec = 8;         // elements a thread carries; four threads share a block
 
-// Bit pattern of |v|: ordered like the magnitudes, infinities and NaNs on top.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
-// E8M0 byte of a block whose largest magnitude has bit pattern m.  For a
+// E8M0 byte of a block whose largest magnitude has bit pattern m (an
+// infinity's or a NaN's is 0x7F800000 or more).  For a
 // normal M = f * 2^k (1 <= f < 2), 448 = 1.75 * 2^8 gives e = k - 8, plus one
 // when f > 1.75; the carry of the mantissa plus 0x1FFFFF into the exponent is
 // that plus one.
@@ -46,14 +53,17 @@ __device__ __forceinline__ uint32_t ckpt_scale_byte(uint32_t m) {
 __device__ __forceinline__ float ckpt_inv_unit(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 __device__ __forceinline__ float ckpt_unit(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
 
-// Four E4M3 bytes (round to nearest even) of v * inv; zeros as +0.
-__device__ __forceinline__ uint32_t ckpt_pack4(const float* v, float inv) {
+// Four E4M3 bytes (round to nearest even) of two fp32 pairs; zeros as +0.
+__device__ __forceinline__ uint32_t ckpt_pack4(uint64_t a, uint64_t b) {
+    float v0, v1, v2, v3;
+    up2(a, v0, v1);
+    up2(b, v2, v3);
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1] * inv), "f"(v[0] * inv));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3] * inv), "f"(v[2] * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v1), "f"(v0));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v3), "f"(v2));
     const uint32_t c = (uint32_t)lo | ((uint32_t)hi << 16);
-    const uint32_t mag = c & 0x7F7F7F7Fu;
-    return mag | (c & (mag + 0x7F7F7F7Fu) & 0x80808080u);  // the sign only where a magnitude bit is set
+    const uint32_t mag = (c & 0x7F7F7F7Fu) + 0x7F7F7F7Fu;  // a byte's top bit: it has a magnitude bit
+    return c & (mag | 0x7F7F7F7Fu);                        // the sign only there
 }
 
 // The values of four codes, without their block's unit.
@@ -123,18 +133,19 @@ __device__ __forceinline__ void store8_bf16(__nv_bfloat16* p, int n, const float
 // block of 32 and call this together (n = 0 past the end of the row).
 template <bool VEC>
 __device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int c, int n, const float v[kVec]) {
-    uint32_t m = 0;
+    float m = max_abs3(v[0], v[1], v[2]);
+    m = max_abs3(m, v[3], v[4]);
+    m = max_abs3(m, v[5], v[6]);
+    m = max_abs3(m, v[7], __shfl_xor_sync(0xFFFFFFFFu, max_abs3(m, v[7], v[7]), 1));
+    m = max_abs3(m, m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const uint32_t byte = ckpt_scale_byte(__float_as_uint(m));
+    const float inv = ckpt_inv_unit(byte);  // unused where the block is not finite
+    const uint64_t inv2 = pk2(inv, inv);
+    uint64_t t[4];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) m = max(m, abs_bits(v[i]));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t byte = ckpt_scale_byte(m);
-    uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if (byte != 255u) {
-        const float inv = ckpt_inv_unit(byte);
-        q.x = ckpt_pack4(v, inv);
-        q.y = ckpt_pack4(v + 4, inv);
-    }
+    for (int i = 0; i < 4; ++i) t[i] = mul2(pk2(v[2 * i], v[2 * i + 1]), inv2);
+    uint2 q = make_uint2(ckpt_pack4(t[0], t[1]), ckpt_pack4(t[2], t[3]));
+    if (byte == 255u) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     if (n <= 0) return;
     uint8_t* dst = k.codes + row * k.codes_ld + c;
     if (VEC) {
@@ -168,8 +179,9 @@ __device__ __forceinline__ void ckpt_load8(const Ckpt& k, int64_t row, int c, in
     const float unit = ckpt_unit(byte);
     ckpt_unpack4(q.x, v);
     ckpt_unpack4(q.y, v + 4);
+    const uint64_t unit2 = pk2(unit, unit);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] *= unit;
+    for (int i = 0; i < 4; ++i) up2(mul2(pk2(v[2 * i], v[2 * i + 1]), unit2), v[2 * i], v[2 * i + 1]);
     if (!VEC && byte == 255u) {  // the zeros past the end of a row stay zeros beside a NaN block
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
