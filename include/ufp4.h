@@ -521,7 +521,8 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
  *            not looked at, and it costs nothing in the products.
  *   loss, lse  device float, tokens elements, written
  *   workspace  at least ufp4_head_loss_workspace_size bytes, 256-byte aligned
- * Extents up to 2^30 (UFP4_ERR_UNSUPPORTED beyond). */
+ * Extents up to 2^30, and products of at most about 2^29 tiles of 256 x 256
+ * (UFP4_ERR_UNSUPPORTED beyond). */
 ufp4_status ufp4_head_loss_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, size_t* bytes);
 ufp4_status ufp4_head_loss(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* targets,
                            int64_t tokens, int64_t vocab, int64_t hidden, float z_loss, float* loss, float* lse,

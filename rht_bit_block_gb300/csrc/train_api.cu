@@ -192,10 +192,17 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
     return to_status(launch_rms_norm_backward(a, sms, stream));
 }
 
+// Whether the loss's extents and the tiles of its products (dH's up to 32 times, in shares) are 32-bit numbers.
+static bool head_fits(int64_t tokens, int64_t vocab, int64_t hidden) {
+    if (tokens > kMaxExtent || vocab > kMaxExtent || hidden > kMaxExtent) return false;
+    const int64_t t = tokens / 256 + 1, v = vocab / 256 + 1, k = hidden / 256 + 1;
+    return t * v + v * k + 32 * t * k < (1ll << 29);
+}
+
 static ufp4_status check_head(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* targets,
                               int64_t tokens, int64_t vocab, int64_t hidden, float z_loss) {
     if (tokens < 0 || vocab < 1 || hidden < 1 || !std::isfinite(z_loss)) return UFP4_ERR_INVALID_ARG;
-    if (tokens > kMaxExtent || vocab > kMaxExtent || hidden > kMaxExtent) return UFP4_ERR_UNSUPPORTED;
+    if (!head_fits(tokens, vocab, hidden)) return UFP4_ERR_UNSUPPORTED;
     if (!w || ldw < hidden || (tokens && (!h || !targets || ldh < hidden))) return UFP4_ERR_INVALID_ARG;
     if ((uintptr_t)w % 16 || ldw % 8) return UFP4_ERR_ALIGNMENT;
     if (tokens && ((uintptr_t)h % 16 || ldh % 8 || (uintptr_t)targets % 8)) return UFP4_ERR_ALIGNMENT;
@@ -210,7 +217,7 @@ static ufp4_status check_workspace(const void* workspace, size_t bytes, size_t n
 static ufp4_status head_bytes(int64_t tokens, int64_t vocab, int64_t hidden,
                               size_t (*f)(int64_t, int64_t, int64_t, int), size_t* bytes) {
     if (tokens < 0 || vocab < 1 || hidden < 1 || !bytes) return UFP4_ERR_INVALID_ARG;
-    if (tokens > kMaxExtent || vocab > kMaxExtent || hidden > kMaxExtent) return UFP4_ERR_UNSUPPORTED;
+    if (!head_fits(tokens, vocab, hidden)) return UFP4_ERR_UNSUPPORTED;
     *bytes = f(tokens, vocab, hidden, current_num_sms());
     return UFP4_OK;
 }

@@ -108,7 +108,7 @@ def test_head_loss_refusals(lib):
     for bad in (dict(h=0x1008), dict(w=0x90002), dict(ldh=130), dict(ldw=132), dict(t=0x8004), dict(loss=0xA002),
                 dict(lse=0xB001), dict(ws=0x100080)):
         assert fwd(**bad) == 3, bad
-    assert fwd(V=(1 << 30) + 1) == 2
+    assert fwd(V=(1 << 30) + 1) == 2 and fwd(T=1 << 24, V=1 << 24) == 2   # extents, and tiles of the product
 
     def bwd(lse=0xB000, weight=None, scale=None, dh=0x20000, ldd=128, ht=0, dw=0x30000, ldw=128, wt=0, acc=0,
             ws=0x100000, n=1 << 40, T=64):
