@@ -414,7 +414,7 @@ struct HeadParams {
     int tokens;
     const int64_t* targets; // with tokens in place
     int vocab;
-    int* next;              // tiles handed out beyond one per cluster; null: a fixed share each
+    int* next;              // tiles handed out beyond one per cluster (pairs)
     const int* index;
     const RowInfo* info;
     float2* part;           // kStats: [row][vocabulary tile]
@@ -615,7 +615,8 @@ __device__ __forceinline__ void stats_chunk(float r[32], int n, float& m, float&
 // its epilogue is what takes the time).  Tiles differ in length by an order
 // of magnitude between products, so clusters take the next one from a counter
 // in global memory when they have room for it; which cluster computes a tile
-// changes nothing in its result.
+// changes nothing in its result.  Single CTAs, whose tiles are all alike, take
+// a fixed share.
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ HeadParams p) {
@@ -656,7 +657,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(ringf_bar(i), 1);               // the leader's warp 3
-            mbar_init(ringe_bar(i), PAIR ? 13 : 7);   // two copiers and a group of four epilogue warps a CTA, the issuer
+            mbar_init(ringe_bar(i), 13);              // two copiers and a group of four epilogue warps a CTA, the issuer
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -677,6 +678,10 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
     // The tile number i of this cluster, or -1 when there is none (or a wait gave up).  `arrive`: this
     // thread speaks for its reader (a copier, the issuer, an epilogue warp).
     auto take = [&](int i, bool arrive) {
+        if (!PAIR) {  // a fixed share
+            const int tile = cluster_id + i * num_clusters;
+            return tile < walk.total && !*abort_flag ? tile : -1;
+        }
         const int at = i % kRing;
         if (!mbar_wait_cluster(ringf_bar(at), (i / kRing) & 1)) {
             *abort_flag = 1;
@@ -687,7 +692,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         return tile < walk.total ? tile : -1;
     };
 
-    if (warp == 3 && lane == 0 && peer == 0) {
+    if (PAIR && warp == 3 && lane == 0 && peer == 0) {
         // ------------------------------------------------ hands out tiles (leader only)
         for (int i = 0, ends = 0; ends < 2; ++i) {  // an end for either epilogue group
             const int at = i % kRing;
@@ -695,9 +700,9 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 *abort_flag = 1;
                 break;
             }
-            const int tile = i == 0 || !p.next ? cluster_id + i * num_clusters : num_clusters + atomicAdd(p.next, 1);
+            const int tile = i == 0 ? cluster_id : num_clusters + atomicAdd(p.next, 1);
             const uint32_t slot = smem_u32(const_cast<int*>(ring + at));
-            for (uint32_t r = leader; r <= leader + (PAIR ? 1 : 0); ++r) {
+            for (uint32_t r = leader; r <= leader + 1; ++r) {
                 st_cluster(map_to_rank(slot, r), tile);
                 mbar_arrive_cluster(map_to_rank(ringf_bar(at), r));
             }
@@ -800,7 +805,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         for (int tc = (warp - 4) >> 2;; tc += 2) {
             const int tile = take(tc, false);  // every lane reads the tile, then one arrives
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(ringe_bar(tc % kRing), leader));
+            if (PAIR && lane == 0) mbar_arrive_cluster(map_to_rank(ringe_bar(tc % kRing), leader));
             const int buf = tc & 1;
             if (__any_sync(0xFFFFFFFFu, tile < 0)) break;
             const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(accf_bar(buf), (tc >> 1) & 1));
