@@ -24,7 +24,7 @@
 // TFLOP/s, and 4096 x 65536 x 7168 with the gradients 9.0 ms, 1710 TFLOP/s with
 // the recomputed logits (the library's bf16 product sustains 1714 there, and
 // 1924 in a burst).  With few tokens it is W: 16 tokens x 65536 x 7168 forward
-// 150 us, 6.3 TB/s.
+// 148 us, 6.35 TB/s.
 //
 // dl is rounded to bf16 because the tensor cores multiply it with bf16 W and H:
 // a relative error of at most 2^-8 per entry, as the outputs' own rounding,
@@ -71,8 +71,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // which halves the hand-offs between the copies and the tensor core (one-step
 // stages: 4096 x 16384 x 2048 logits 193 us, two-step stages 174 us).  A
 // single CTA's tile is for reading W once: 224 columns leave room for a fifth
-// stage (16 tokens, 131072 x 2048: 256 columns and four stages 124 us, 224 and
-// five 111 us, 96 and eight 173 us).
+// stage (16 tokens, 131072 x 2048, when first built: 256 columns and four
+// stages 124 us, 224 and five 111 us, 96 and eight 173 us; now 91 us, 5.9 TB/s).
 template <bool PAIR>
 struct Cfg {
     static constexpr int kRows = PAIR ? kTile : kHalf;   // rows of a tile
@@ -390,6 +390,7 @@ struct Job {
     int a, b;               // operands (Operand)
     int a_mn, b_mn;         // the operand's contiguous index is not the summed one
     int group;              // tile rows that advance before the column does
+    int a_rows;             // rows of A that a CTA copies: kHalf, or the tokens there are (a multiple of 8)
     int width;              // columns of a tile: kTile, or less for single CTAs (a multiple of 16, up to kAlone)
     int m, n, k;            // extents; kernel-side: m (or k for kDW) comes from the token count
     int v0;                 // first vocabulary row of the piece
@@ -724,7 +725,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             // W's rows are the whole vocabulary, a piece starts at v0; dl's columns are the piece's own
             const int r0 = is_a ? t.m * C::kRows + peer * kHalf
                                 : t.n * q.width + peer * C::kBRows + (q.b_mn ? 0 : q.v0);
-            const int tx = PAIR ? 4 * kAtom : kAtom + q.width * 128;  // bytes of one step, of both CTAs
+            const int tx = PAIR ? 4 * kAtom : (q.a_rows + q.width) * 128;  // bytes of one step, of both CTAs
             // first summed element; of W, counted from its first row
             const int kb = t.k0 * kStep + (!is_a && q.kind == kDH ? q.v0 : 0);
             for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
@@ -1118,7 +1119,9 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
 
 cudaError_t make_maps(const HeadArgs& a, const Plan& pl, bool back, HeadMaps& maps) {
     uint8_t* ws = (uint8_t*)a.workspace;
-    bool ok = (pl.direct ? bf16_maps(maps.m[kOpH], a.h, a.K, a.T, a.ldh)
+    // tokens in place: boxes of the rows there are.  The accumulator rows past them hold whatever shared memory
+    // did, and are not looked at; rows that the copy fills with zeros cost time (one token, 32000 x 2048: 37 us with 128 rows, 31 with 8).
+    bool ok = (pl.direct ? bf16_maps(maps.m[kOpH], a.h, a.K, a.T, a.ldh, (int)up(a.T, 8))
                          : bf16_maps(maps.m[kOpH], ws + pl.packed, a.K, pl.Tp, pl.Kp)) &&
               bf16_maps(maps.m[kOpW], a.w, a.K, a.V, a.ldw, pl.direct ? (int)pl.width / 2 : kHalf);
     for (int i = 0; i < 2; ++i) {
@@ -1153,6 +1156,7 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
     p.Tp = pl.Tp;
     p.shares = pl.slices > 1 ? (int)(pl.slices * pl.pieces) : 1;
     for (Job& q : p.job) {
+        q.a_rows = kHalf;
         q.width = kTile;
         q.slices = 1;
     }
@@ -1162,6 +1166,7 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
         p.targets = a.targets;
         p.vocab = (int)a.V;
         p.next = nullptr;
+        p.job[0].a_rows = (int)up(a.T, 8);
         p.job[0].width = (int)pl.width;
     }
     return p;
