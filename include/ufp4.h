@@ -517,8 +517,9 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
  *   w        device bf16 [vocab x hidden], leading dimension ldw; both 16-byte
  *            aligned with leading dimensions that are multiples of 8
  *   targets  device int64, tokens elements.  A token whose target is outside
- *            [0, vocab) is ignored: its loss and lse are 0, its row of h is
- *            not looked at, and it costs nothing in the products.
+ *            [0, vocab) is ignored: its loss and lse are 0, nothing
+ *            else depends on its row of h, and it costs nothing in the
+ *            products (with up to 128 tokens, forward: as much as another).
  *   loss, lse  device float, tokens elements, written
  *   workspace  at least ufp4_head_loss_workspace_size bytes, 256-byte aligned
  * Extents up to 2^30, and products of at most about 2^29 tiles of 256 x 256

@@ -12,8 +12,9 @@
 // kernel of either pass packs the rows of H that have one, so work goes with
 // the number of valid tokens, and whatever an ignored row holds stays out of
 // dW.  (Up to 128 tokens, forward, are read where they lie: W is what that call
-// reads, and a logit's row meets no other.)  Forward, each 256 x 256 tile of logits leaves its rows' running maximum
-// and sum of exponentials, joined in the tiles' order by a last kernel.
+// reads, and a logit's row meets no other.)  Forward, each tile of logits
+// leaves its rows' running maximum and sum of exponentials, joined in the
+// tiles' order by a last kernel.
 // Backward, the vocabulary is walked in pieces: a piece's logits are computed
 // again, become dl (bf16) in a workspace of two pieces, and are multiplied
 // into dH (fp32 until the last piece) and dW.  Recomputing costs 2 of the 8
@@ -609,6 +610,17 @@ __device__ __forceinline__ void stats_chunk(float r[32], int n, float& m, float&
     m = top;
 }
 
+// 32 logits of a row, from vocabulary entry `v` on (n of them exist), become dl.
+__device__ __forceinline__ void grad_chunk(float r[32], const RowInfo& info, int v, int n) {
+    const int at = info.target - v;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        float x = info.a * ex2(fmaf(r[i], kLog2e, -info.lse2));
+        if (at == i) x -= info.weight;
+        r[i] = i < n ? x : 0.0f;
+    }
+}
+
 // Warps 0 and 2 copy A and B (one thread each: a single thread issuing both is
 // 5 % slower), warp 1 of the leader issues the MMAs, warp 3 of the leader hands
 // out tiles, warps 4 to 7 and 8 to 11 run the epilogues of even and odd tiles
@@ -843,7 +855,26 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                     p.part[row * p.ld_part + t.n] = make_float2(m, sum);
                     if (target >= n0 && target < n0 + q.width) p.target_logit[row] = hit;
                 }
-            } else if (PAIR) {  // single CTAs only take logits
+            } else if (!PAIR) {
+                // dl of few tokens: whole rows of the tile (zeros as below), in the last one up to a whole step
+                RowInfo info = {0.0f, 0.0f, 0.0f, -1};
+                if (row < count) info = p.info[row];
+                const int end = (q.n + kStep - 1) / kStep * kStep - n0;
+                const int cols = min(q.width, end);
+                uint4* dst = reinterpret_cast<uint4*>(q.dl + row * q.ld_dl + n0);
+                for (int c = 0; c < cols; c += 32) {
+                    tmem_ld32(acc + c, r);
+                    grad_chunk(r, info, n0 + c, row < count ? q.n - (n0 + c) : 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + 8 * i < cols)
+                            dst[c / 8 + i] =
+                                make_uint4(pack_bf16(r[8 * i], r[8 * i + 1]), pack_bf16(r[8 * i + 2], r[8 * i + 3]),
+                                           pack_bf16(r[8 * i + 4], r[8 * i + 5]), pack_bf16(r[8 * i + 6], r[8 * i + 7]));
+                }
+                if (n0 + q.width >= q.n)
+                    for (int c = cols; c < end; c += 8) dst[c / 8] = make_uint4(0, 0, 0, 0);
+            } else {
                 // a piece's dl whole (zeros beside the valid rows and columns: dH and dW sum over them);
                 // dH of the valid rows; rows of dW
                 RowInfo info = {0.0f, 0.0f, 0.0f, -1};
@@ -867,14 +898,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 for (int c = 0; c < kTile; c += 32) {
                     tmem_ld32(acc + c, r);
                     if (q.kind == kGrad) {
-                        const int at = info.target - q.v0 - (n0 + c);
-                        const int n = row < count ? q.n - (n0 + c) : 0;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            float v = info.a * ex2(fmaf(r[i], kLog2e, -info.lse2));
-                            if (at == i) v -= info.weight;
-                            r[i] = i < n ? v : 0.0f;
-                        }
+                        grad_chunk(r, info, q.v0 + n0 + c, row < count ? q.n - (n0 + c) : 0);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] = empty ? 0.0f : r[i] * factor;
@@ -963,9 +987,28 @@ struct Plan {
     int64_t launches;        // of the product kernel
     int64_t slices;          // backward: shares of a piece's dH
     bool direct;             // forward: tokens in place, none packed
-    int64_t width, tiles;    // forward: columns of a tile, tiles of the vocabulary
+    int64_t width, tiles;    // columns of a tile of logits; forward: tiles of the vocabulary
     size_t count, next, index, info, packed, part, target, dl[2], acc, total;
 };
+
+// Few tokens' logits are computed by single CTAs: a pair's tile costs the same
+// for 16 tokens as for 256, and what should bound the call is the reading of W.
+// Forward up to half a tile of tokens, which are then read where they lie (16 x
+// 32000 x 2048: 45 us in pairs, 31 so).  The tiles' widths decide where its sums
+// are joined; with more tokens all widths are the same, so that a row's bits do not
+// depend on how many ignored tokens stand among the others.  Backward (dl, with
+// the same bits from either) up to kAloneBack: 128 x 32000 x 2048 138 us in
+// pairs, 128 so; 300: 178 and 167; 384 x 5000 x 2048: 84 and 76; 256 x 131072 x
+// 4096: 741 and 762, 384: 1070 and 1040, 512: 1150 and 1195.
+constexpr int64_t kDirect = kHalf;
+constexpr int64_t kAloneBack = 384;
+
+// Columns of such a tile: all CTAs have as many of them.
+int64_t alone_width(int64_t T, int64_t V, int num_sms) {
+    const int64_t all = std::max<int64_t>(1, (T + kHalf - 1) / kHalf) * V;
+    const int64_t rounds = (all + (int64_t)kAlone * num_sms - 1) / ((int64_t)kAlone * num_sms);
+    return std::max<int64_t>(32, up((all + rounds * num_sms - 1) / (rounds * num_sms), 16));
+}
 
 // A piece's dl takes about kPieceBytes.  Wider pieces mean fewer launches,
 // longer sums and fewer passes over the fp32 dH; narrower ones a smaller
@@ -1011,16 +1054,15 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back, int num_sms) {
     p.info = take((int64_t)sizeof(RowInfo) * p.Tp);
     p.packed = take(2 * p.Tp * p.Kp);
     if (back) {
+        p.width = T <= kAloneBack && p.pieces == 1 ? alone_width(T, V, num_sms) : kTile;
         p.dl[0] = take(2 * p.Tp * p.piece);
         p.dl[1] = p.pieces > 1 ? take(2 * p.Tp * p.piece) : p.dl[0];
         p.slices = dh_slices(T, K, p.piece, p.pieces, num_sms);
         const int64_t shares = p.slices > 1 ? p.slices * p.pieces : (p.pieces > 1 ? 1 : 0);
         p.acc = shares ? take(4 * p.Tp * p.Kp * shares) : 0;
     } else {
-        // up to kHalf tokens: one tile a CTA and round, all CTAs busy
-        p.direct = T <= kHalf;
-        const int64_t rounds = (V + (int64_t)kAlone * num_sms - 1) / ((int64_t)kAlone * num_sms);
-        p.width = p.direct ? std::max<int64_t>(32, up((V + rounds * num_sms - 1) / (rounds * num_sms), 16)) : kTile;
+        p.direct = T <= kDirect;
+        p.width = p.direct ? alone_width(T, V, num_sms) : kTile;
         p.tiles = (V + p.width - 1) / p.width;
         p.part = take((int64_t)sizeof(float2) * p.Tp * p.tiles);
         p.target = take(4 * p.Tp);
@@ -1123,7 +1165,7 @@ cudaError_t make_maps(const HeadArgs& a, const Plan& pl, bool back, HeadMaps& ma
     // did, and are not looked at; rows that the copy fills with zeros cost time (one token, 32000 x 2048: 37 us with 128 rows, 31 with 8).
     bool ok = (pl.direct ? bf16_maps(maps.m[kOpH], a.h, a.K, a.T, a.ldh, (int)up(a.T, 8))
                          : bf16_maps(maps.m[kOpH], ws + pl.packed, a.K, pl.Tp, pl.Kp)) &&
-              bf16_maps(maps.m[kOpW], a.w, a.K, a.V, a.ldw, pl.direct ? (int)pl.width / 2 : kHalf);
+              bf16_maps(maps.m[kOpW], a.w, a.K, a.V, a.ldw, (int)pl.width / 2);
     for (int i = 0; i < 2; ++i) {
         if (back)
             ok = ok && bf16_maps(maps.m[kOpDl + i], ws + pl.dl[i], pl.piece, pl.Tp, pl.piece);
@@ -1193,8 +1235,6 @@ cudaError_t launch_head_loss(const HeadArgs& a, int num_sms, cudaStream_t st) {
     p.job[0].b = kOpW;
     p.job[0].n = (int)a.V;
     p.job[0].k = (int)a.K;
-    // A pair's tile costs the same for 16 tokens as for 256, and with up to 128 the reading of W is what
-    // should bound the call: a single CTA's tile leaves twice the tensor time to spare.
     e = pl.direct ? run_gemm<false>(maps, p, a.T, st) : run_gemm<true>(maps, p, a.T, st);
     if (e != cudaSuccess) return e;
     return launch_pdl(head_join_kernel, dim3((unsigned)((a.T + 7) / 8)), dim3(256), 0, st, p, (int)pl.tiles, a.z, a.loss,
@@ -1250,7 +1290,9 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
         std::sort(p.job, p.job + p.jobs, [&](const Job& x, const Job& y) {
             return (x.kind == kDW ? a.T : x.k / x.slices) > (y.kind == kDW ? a.T : y.k / y.slices);
         });
-        if (p.jobs) e = run_gemm<true>(maps, p, a.T, st);
+        const bool alone = i < 0 && pl.width < kTile;
+        if (alone) p.job[0].width = (int)pl.width;
+        if (p.jobs) e = alone ? run_gemm<false>(maps, p, a.T, st) : run_gemm<true>(maps, p, a.T, st);
     }
     if (e == cudaSuccess && a.dh && (pl.pieces > 1 || pl.slices > 1))
         e = launch_pdl(head_dh_kernel, dim3((unsigned)a.T, (unsigned)std::min<int64_t>((a.K + 255) / 256, 65535)), dim3(256),

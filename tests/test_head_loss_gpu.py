@@ -279,3 +279,14 @@ def test_few_tokens(tokens, vocab):
     h, w, t = _inputs(tokens, vocab, 192, seed=tokens, ignored=0.3)
     loss, lse = _forward(h, w, t)
     _check_forward(h, w, t, loss, lse)
+
+
+@pytest.mark.parametrize("tokens", [1, 100, 128, 129, 200, 256, 300, 384, 385])
+@pytest.mark.parametrize("vocab,hidden", [(33, 64), (4000, 200), (40001, 136)])
+def test_up_to_a_few_hundred_tokens(tokens, vocab, hidden):
+    """Both sides of the steps from single CTAs' tiles to pairs', forward (128 tokens) and backward (384)."""
+    h, w, t = _inputs(tokens, vocab, hidden, seed=tokens, ignored=0.3)
+    loss, lse = _forward(h, w, t)
+    _check_forward(h, w, t, loss, lse)
+    dh, dw = _backward(h, w, t, lse)
+    _check_backward(h, w, t, dh, dw)
