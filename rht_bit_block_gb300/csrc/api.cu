@@ -73,8 +73,9 @@ bool is_pow2(int64_t v) { return v >= 1 && (v & (v - 1)) == 0; }
 
 float inv_sqrt_n(int n) { return (float)(1.0 / std::sqrt((double)n)); }
 
-// Loads every kernel of the library on the current device, once, before the
-// library's first launch there (see the preload functions).
+// Loads every kernel of the library on the current device, and sets the norm's
+// shared-memory limits, once, before the library's first launch there (see the
+// preload functions).
 void ensure_loaded() {
     static std::mutex mu;
     static bool done[64];

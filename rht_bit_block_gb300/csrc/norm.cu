@@ -465,34 +465,51 @@ int ctas_per_sm(const Shape& s, int threads, size_t smem) {
     return std::max(1, std::min<int>(std::min(32, threads / s.threads()), (int)(kSmSmem / (smem + kReserved))));
 }
 
+// Dynamic shared memory of a CTA of so many warps.  Forward: its copies.
+template <bool F32, bool VEC, int ITER>
+constexpr int forward_smem(int warps) {
+    return VEC ? warps * Stage<F32, ITER, false>::kWarp : 0;
+}
+// Backward: its copies; at least the sums of dgamma, which the groups but the
+// last leave there (four bytes for each of `cols`).
+template <bool F32, bool VEC, int ITER>
+constexpr int backward_smem(int warps, int cols) {
+    return VEC ? warps * Stage<F32, ITER, true>::kWarp : cols * 4;
+}
+
 template <bool F32, bool VEC, int ITER, int THREADS>
 struct Fwd {
     static cudaError_t run(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
-        const size_t smem = VEC ? (size_t)s.warps * s.groups * Stage<F32, ITER, false>::kWarp : 0;
-        auto k = norm_kernel<F32, VEC, ITER, THREADS>;
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
+        const size_t smem = forward_smem<F32, VEC, ITER>(s.warps * s.groups);
         const int64_t grid = std::min<int64_t>(p.rows, (int64_t)num_sms * ctas_per_sm(s, kForwardThreads, smem));
-        return launch_pdl(k, dim3((unsigned)grid), dim3(s.threads()), smem, st, p);
+        return launch_pdl(norm_kernel<F32, VEC, ITER, THREADS>, dim3((unsigned)grid), dim3(s.threads()), smem, st, p);
     }
 };
 template <bool F32, bool VEC, int ITER, int THREADS>
 struct Bwd {
     static cudaError_t run(const NormParams& p, const Shape& s, int parts, cudaStream_t st) {
-        // the copies; at least the sums of dgamma, which the groups but the last leave there
-        const int smem = VEC ? s.warps * s.groups * Stage<F32, ITER, true>::kWarp : p.cols * 4;
-        auto k = norm_backward_kernel<F32, VEC, ITER, THREADS>;
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        return launch_pdl(k, dim3((unsigned)parts), dim3(s.threads()), (size_t)smem, st, p);
+        const size_t smem = backward_smem<F32, VEC, ITER>(s.warps * s.groups, p.cols);
+        return launch_pdl(norm_backward_kernel<F32, VEC, ITER, THREADS>, dim3((unsigned)parts), dim3(s.threads()), smem, st,
+                          p);
     }
 };
+// Loads both kernels, and lets them have as much shared memory as the widest
+// row they serve takes: the limit belongs to the kernel, which calls of other
+// widths use at the same time, so no call may set it to its own need.
 template <bool F32, bool VEC, int ITER, int THREADS>
 struct Preload {
     static cudaError_t run() {
+        constexpr int warps = THREADS / 32, cols = warps * ITER * kStepCols;
+        constexpr int fwd = forward_smem<F32, VEC, ITER>(warps), bwd = backward_smem<F32, VEC, ITER>(warps, cols);
+        static_assert(fwd <= 232448 - 128 && bwd <= 232448 - 128, "shared memory overflow");
         cudaFuncAttributes at;
         cudaFuncGetAttributes(&at, norm_kernel<F32, VEC, ITER, THREADS>);
-        return cudaFuncGetAttributes(&at, norm_backward_kernel<F32, VEC, ITER, THREADS>);
+        cudaFuncGetAttributes(&at, norm_backward_kernel<F32, VEC, ITER, THREADS>);
+        const cudaError_t e =
+            cudaFuncSetAttribute(norm_kernel<F32, VEC, ITER, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, fwd);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(norm_backward_kernel<F32, VEC, ITER, THREADS>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bwd);
     }
 };
 
