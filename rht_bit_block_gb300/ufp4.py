@@ -54,6 +54,7 @@ class QTensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("codes_ld", ctypes.c_int64), ("scales_ld", ctypes.c_int64),
                 ("tensor_amax", ctypes.c_void_p)]
+    device = None  # CUDA device index of the tensors it describes (-1: host memory), where known
 
 
 class Ufp4Error(RuntimeError):
@@ -159,8 +160,12 @@ def qtensor(codes, scales, rows: int, cols: int, tensor_amax=None) -> QTensor:
     """Describe a quantized matrix held in torch tensors codes [rows, cols/2]
     (uint8; [rows, cols] for MXFP8) and scales [rows/br, cols/bc] (float32 or uint8); tensor_amax: a
     1-element float32 tensor for the two-level scale format."""
-    return QTensor(codes.data_ptr(), scales.data_ptr(), rows, cols, codes.stride(0) * codes.element_size(),
-                   scales.stride(0), tensor_amax.data_ptr() if tensor_amax is not None else None)
+    q = QTensor(codes.data_ptr(), scales.data_ptr(), rows, cols, codes.stride(0) * codes.element_size(),
+                scales.stride(0), tensor_amax.data_ptr() if tensor_amax is not None else None)
+    q.device = codes.get_device()
+    if scales.get_device() != q.device:
+        raise ValueError(f"codes are on {codes.device}, their scales on {scales.device}")
+    return q
 
 
 # ------------------------------------------------------------- C entry points
@@ -377,6 +382,45 @@ def _vector(t, what: str, n: int, code: int):
     return t.data_ptr()
 
 
+def _find_current_device():
+    global _current_device
+    import torch
+    torch.cuda.current_device()  # initializes CUDA
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
+_current_device = _find_current_device
+
+
+def _check_devices(what: str, tensors, *ckpts):
+    """The kernels take addresses: every operand (None: left out) lies in the current CUDA device's memory.
+    tensors[0] is not None."""
+    here = tensors[0].get_device()
+    good = here >= 0 and here == _current_device()
+    if good:
+        for t in tensors:
+            if t is not None and t.get_device() != here:
+                good = False
+        for q in ckpts:
+            if q is not None and q.device is not None and q.device != here:  # None: a QTensor of addresses
+                good = False
+    if not good:
+        devices = {t.get_device() for t in tensors if t is not None}
+        devices |= {q.device for q in ckpts if q is not None and q.device is not None}
+        if min(devices) < 0:
+            raise ValueError(f"{what}: an operand is in host memory")
+        raise ValueError(f"{what}: operands on {', '.join(f'cuda:{d}' for d in sorted(devices))}, "
+                         f"the current device is cuda:{_current_device()}")
+
+
+def _workspace(t):
+    """(pointer, bytes) of a workspace."""
+    if not t.is_contiguous():
+        raise ValueError("workspace is not contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _act(act) -> int:
     return ACTS[act] if isinstance(act, str) else int(act)
 
@@ -385,18 +429,19 @@ def ufp4_glu(gate, up, y, act="silu", ckpt_gate: QTensor | None = None, ckpt_up:
     """y = act(gate) * up; the 8-bit checkpoints of gate and up are written if both are given."""
     shape = rows, cols = gate.shape
     dt = _dtype(gate, "gate")
-    _check(load().ufp4_glu(*_matrix(gate, "gate", shape), *_matrix(up, "up", shape, dt), dt, rows, cols,
-                           _act(act), *_matrix(y, "y", shape, BF16), ckpt_gate, ckpt_up,
-                           _stream(stream)), "ufp4_glu")
+    args = (*_matrix(gate, "gate", shape), *_matrix(up, "up", shape, dt), dt, rows, cols, _act(act),
+            *_matrix(y, "y", shape, BF16), ckpt_gate, ckpt_up)
+    _check_devices("ufp4_glu", (gate, up, y), ckpt_gate, ckpt_up)
+    _check(load().ufp4_glu(*args, _stream(stream)), "ufp4_glu")
 
 
 def ufp4_glu_backward(dy, ckpt_gate: QTensor, ckpt_up: QTensor, dgate, dup, act="silu", y=None, stream=None):
     """dgate and dup of ufp4_glu at the checkpointed values, and act(gate) * up again into y if given."""
     shape = rows, cols = dy.shape
-    _check(load().ufp4_glu_backward(*_matrix(dy, "dy", shape), _dtype(dy, "dy"), ckpt_gate, ckpt_up,
-                                    rows, cols, _act(act), *_matrix(dgate, "dgate", shape, BF16),
-                                    *_matrix(dup, "dup", shape, BF16), *_matrix(y, "y", shape, BF16),
-                                    _stream(stream)), "ufp4_glu_backward")
+    args = (*_matrix(dy, "dy", shape), _dtype(dy, "dy"), ckpt_gate, ckpt_up, rows, cols, _act(act),
+            *_matrix(dgate, "dgate", shape, BF16), *_matrix(dup, "dup", shape, BF16), *_matrix(y, "y", shape, BF16))
+    _check_devices("ufp4_glu_backward", (dy, dgate, dup, y), ckpt_gate, ckpt_up)
+    _check(load().ufp4_glu_backward(*args, _stream(stream)), "ufp4_glu_backward")
 
 
 def ufp4_rms_norm(x, gamma, y, rstd=None, residual=None, total=None, ckpt: QTensor | None = None, eps=1e-6,
@@ -405,11 +450,11 @@ def ufp4_rms_norm(x, gamma, y, rstd=None, residual=None, total=None, ckpt: QTens
     written if given."""
     shape = rows, cols = x.shape
     dt = _dtype(gamma, "gamma")
-    _check(load().ufp4_rms_norm(*_matrix(x, "x", shape), _dtype(x, "x"),
-                                *_matrix(residual, "residual", shape, BF16),
-                                _vector(gamma, "gamma", cols, dt), dt, rows, cols,
-                                eps, *_matrix(y, "y", shape, BF16), *_matrix(total, "total", shape, BF16),
-                                _vector(rstd, "rstd", rows, F32), ckpt, _stream(stream)), "ufp4_rms_norm")
+    args = (*_matrix(x, "x", shape), _dtype(x, "x"), *_matrix(residual, "residual", shape, BF16),
+            _vector(gamma, "gamma", cols, dt), dt, rows, cols, eps, *_matrix(y, "y", shape, BF16),
+            *_matrix(total, "total", shape, BF16), _vector(rstd, "rstd", rows, F32), ckpt)
+    _check_devices("ufp4_rms_norm", (x, gamma, y, rstd, residual, total), ckpt)
+    _check(load().ufp4_rms_norm(*args, _stream(stream)), "ufp4_rms_norm")
 
 
 def ufp4_rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -424,14 +469,12 @@ def ufp4_rms_norm_backward(dy, ckpt: QTensor, rstd, gamma, dx, dgamma, workspace
     again into y if given."""
     shape = rows, cols = dy.shape
     dt = _dtype(gamma, "gamma")
-    _check(load().ufp4_rms_norm_backward(*_matrix(dy, "dy", shape), _dtype(dy, "dy"), ckpt,
-                                         _vector(rstd, "rstd", rows, F32),
-                                         _vector(gamma, "gamma", cols, dt), dt,
-                                         *_matrix(dtotal, "dtotal", shape, BF16), rows, cols,
-                                         *_matrix(dx, "dx", shape, BF16), _vector(dgamma, "dgamma", cols, F32),
-                                         *_matrix(y, "y", shape, BF16), workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)),
-           "ufp4_rms_norm_backward")
+    args = (*_matrix(dy, "dy", shape), _dtype(dy, "dy"), ckpt, _vector(rstd, "rstd", rows, F32),
+            _vector(gamma, "gamma", cols, dt), dt, *_matrix(dtotal, "dtotal", shape, BF16), rows, cols,
+            *_matrix(dx, "dx", shape, BF16), _vector(dgamma, "dgamma", cols, F32), *_matrix(y, "y", shape, BF16),
+            *_workspace(workspace))
+    _check_devices("ufp4_rms_norm_backward", (dy, rstd, gamma, dx, dgamma, workspace, dtotal, y), ckpt)
+    _check(load().ufp4_rms_norm_backward(*args, _stream(stream)), "ufp4_rms_norm_backward")
 
 
 def ufp4_head_loss_workspace_size(tokens: int, vocab: int, hidden: int) -> int:
@@ -453,11 +496,11 @@ def ufp4_head_loss(h, w, targets, loss, lse, workspace, z_loss=0.0, stream=None)
     targets: int64; a target outside [0, vocab) gives loss and lse 0."""
     tokens, hidden = h.shape
     vocab = w.shape[0]
-    _check(load().ufp4_head_loss(*_matrix(h, "h", (tokens, hidden), BF16), *_matrix(w, "w", (vocab, hidden), BF16),
-                                 _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss,
-                                 _vector(loss, "loss", tokens, F32), _vector(lse, "lse", tokens, F32),
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
-           "ufp4_head_loss")
+    args = (*_matrix(h, "h", (tokens, hidden), BF16), *_matrix(w, "w", (vocab, hidden), BF16),
+            _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss, _vector(loss, "loss", tokens, F32),
+            _vector(lse, "lse", tokens, F32), *_workspace(workspace))
+    _check_devices("ufp4_head_loss", (h, w, targets, loss, lse, workspace))
+    _check(load().ufp4_head_loss(*args, _stream(stream)), "ufp4_head_loss")
 
 
 def ufp4_head_loss_backward(h, w, targets, lse, dh, dw, workspace, token_weight=None, scale=None, z_loss=0.0,
@@ -465,14 +508,14 @@ def ufp4_head_loss_backward(h, w, targets, lse, dh, dw, workspace, token_weight=
     """dh and dw of scale * sum(token_weight * loss); either may be None.  dw is added to with accumulate_dw (float32)."""
     tokens, hidden = h.shape
     vocab = w.shape[0]
-    _check(load().ufp4_head_loss_backward(
-        *_matrix(h, "h", (tokens, hidden), BF16), *_matrix(w, "w", (vocab, hidden), BF16),
-        _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss,
-        _vector(lse, "lse", tokens, F32), _vector(token_weight, "token_weight", tokens, F32),
-        _vector(scale, "scale", 1, F32), *_matrix(dh, "dh", (tokens, hidden)),
-        BF16 if dh is None else _dtype(dh, "dh"), *_matrix(dw, "dw", (vocab, hidden)),
-        BF16 if dw is None else _dtype(dw, "dw"), int(accumulate_dw), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "ufp4_head_loss_backward")
+    args = (*_matrix(h, "h", (tokens, hidden), BF16), *_matrix(w, "w", (vocab, hidden), BF16),
+            _vector(targets, "targets", tokens, -1), tokens, vocab, hidden, z_loss, _vector(lse, "lse", tokens, F32),
+            _vector(token_weight, "token_weight", tokens, F32), _vector(scale, "scale", 1, F32),
+            *_matrix(dh, "dh", (tokens, hidden)), BF16 if dh is None else _dtype(dh, "dh"),
+            *_matrix(dw, "dw", (vocab, hidden)), BF16 if dw is None else _dtype(dw, "dw"), int(accumulate_dw),
+            *_workspace(workspace))
+    _check_devices("ufp4_head_loss_backward", (h, w, targets, lse, dh, dw, workspace, token_weight, scale))
+    _check(load().ufp4_head_loss_backward(*args, _stream(stream)), "ufp4_head_loss_backward")
 
 
 # ------------------------------------------------------------- conveniences
