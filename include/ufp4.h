@@ -564,15 +564,16 @@ ufp4_status ufp4_head_loss_backward(const void* h, int64_t ldh, const void* w, i
 ufp4_status ufp4_device_error(int32_t* code);
 
 /* ufp4_set_quantize_wait_limit -- failure-detection hook (no counterpart in
- * the pages).  Sets how many times the quantizer kernels poll for a tile's
- * arrival before they give up, on the current device, for later launches;
- * polls < 0 restores the default (2^24 polls, seconds).  With polls = 0 the
- * first wait of every quantizer CTA gives up at once: the kernel records the
- * timeout, waits (with the default limit) for the copies it has started and
- * returns, so tests can exercise the timeout path without hanging or faulting
- * the GPU; ufp4_device_error then returns UFP4_ERR_TIMEOUT.  Synchronizes the
- * device; do not call it while quantizer work is in flight on another
- * thread. */
+ * the pages).  Sets how many times the quantizer kernels, and the products of
+ * the vocabulary loss, poll for a tile's arrival before they give up, on the
+ * current device, for later launches; polls < 0 restores the default (2^24
+ * polls, 2^22 of the products: seconds).  With polls = 0 the first wait of
+ * every such CTA (of the products: cluster) gives up at once: the kernel
+ * records the timeout, waits (with a limit of its own) for the copies it has
+ * started and returns, so tests can exercise the timeout path without hanging
+ * or faulting the GPU; ufp4_device_error then returns UFP4_ERR_TIMEOUT.
+ * Synchronizes the device; do not call it while such work is in flight on
+ * another thread. */
 ufp4_status ufp4_set_quantize_wait_limit(int64_t polls);
 
 /* ufp4_status_string -- static, human-readable name of a status code. */

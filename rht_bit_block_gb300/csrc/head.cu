@@ -41,6 +41,7 @@
 // not the contiguous one (W in dH; dl and H in dW) the tiles are staged
 // MN-major and the instruction descriptor says so; nothing is transposed.
 #include <algorithm>
+#include <atomic>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -64,6 +65,8 @@ constexpr int kThreads = 384;
 constexpr int kRing = 4;                   // tiles handed out ahead (even: a place serves one epilogue group)
 constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sleep up to kSuspendNs
 constexpr uint32_t kSuspendNs = 1000;
+constexpr uint32_t kLook = 1024;  // polls between looks at the abort flag
+constexpr uint32_t kDrainLimit = 1u << 16;  // polls for copies in flight, after a wait has given up
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A CTA pair's 256 x 256 tile, or a single CTA's 128 x (up to 224) tile.  A
@@ -89,8 +92,10 @@ struct Cfg {
     static constexpr int kOffBars = kOffOut + kOut;
     // full, empty; accumulators full x2, empty x2; ring full, empty; drain
     static constexpr int kNumBars = 2 * kStages + 4 + 2 * kRing + 1;
-    static constexpr int kOffWords = kOffBars + 8 * kNumBars;  // tensor memory address, abort flag, ring of tiles
-    static constexpr int kSmem = kOffWords + 4 * (2 + kRing) + 1024;
+    // tensor memory address, abort flag, ring of tiles; stages that the CTA's copiers filled (x2), and that were used
+    static constexpr int kOffWords = kOffBars + 8 * kNumBars;
+    static constexpr int kOffStages = kOffWords + 4 * (2 + kRing);
+    static constexpr int kSmem = kOffStages + 4 * 3 + 1024;
     static_assert(kSmem <= 232448, "shared memory overflow");
 };
 
@@ -103,31 +108,34 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Bounded wait on an mbarrier phase; false (and the error word set) at the limit.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(kSuspendNs)
-            : "memory");
-        if (ok) return true;
-    }
-    atomicExch(&g_head_error, 1);
-    return false;
-}
-// The same for what a thread of either CTA of the pair wrote before it arrived.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;"
-            " selp.u32 %0, 1, 0, p; }"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(kSuspendNs)
-            : "memory");
-        if (ok) return true;
+// Bounded wait on an mbarrier phase; false at the limit (with the error word
+// set), or once `abort` (where given) is set, which is looked at every kLook
+// polls.  CLUSTER: for what a thread of either CTA of the pair wrote before it
+// arrived.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int* abort,
+                                          uint32_t limit = kWaitLimit) {
+    for (uint32_t left = limit; left;) {
+        const uint32_t n = min(left, kLook);
+        for (uint32_t i = 0; i < n; ++i) {
+            uint32_t ok;
+            if (CLUSTER)
+                asm volatile(
+                    "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;"
+                    " selp.u32 %0, 1, 0, p; }"
+                    : "=r"(ok)
+                    : "r"(bar), "r"(parity), "r"(kSuspendNs)
+                    : "memory");
+            else
+                asm volatile(
+                    "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                    : "=r"(ok)
+                    : "r"(bar), "r"(parity), "r"(kSuspendNs)
+                    : "memory");
+            if (ok) return true;
+        }
+        left -= n;
+        if (abort && *abort) return false;
     }
     atomicExch(&g_head_error, 1);
     return false;
@@ -150,6 +158,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
 }
 __device__ __forceinline__ void st_cluster(uint32_t caddr, int v) {
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_cluster(uint32_t caddr) {
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
+    return v;
 }
 // TMA box into this CTA's shared memory, counted on a barrier of either CTA of the pair.
 template <bool PAIR>
@@ -412,6 +425,7 @@ struct HeadMaps {
 struct HeadParams {
     Job job[kMaxJobs];
     int jobs;
+    uint32_t wait_limit;    // polls of a stage's arrival; all other waits keep kWaitLimit
     const int* count;       // null: all `tokens`, in place
     int tokens;
     const int64_t* targets; // with tokens in place
@@ -650,6 +664,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffWords);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffWords + 4);
     volatile int* ring = reinterpret_cast<volatile int*>(gbase + C::kOffWords + 8);
+    volatile int* stages_of = reinterpret_cast<volatile int*>(gbase + C::kOffStages);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -688,6 +703,12 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
     const int count = p.count ? *p.count : p.tokens;
     const Walk<C::kRows> walk(p, count);
 
+    // Sets the abort flag of every CTA of the cluster.
+    auto give_up = [&] {
+        *abort_flag = 1;
+        if (PAIR) st_cluster(map_to_rank(base + C::kOffWords + 4, rank ^ 1u), 1);
+    };
+
     // The tile number i of this cluster, or -1 when there is none (or a wait gave up).  `arrive`: this
     // thread speaks for its reader (a copier, the issuer, an epilogue warp).
     auto take = [&](int i, bool arrive) {
@@ -696,8 +717,8 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             return tile < walk.total && !*abort_flag ? tile : -1;
         }
         const int at = i % kRing;
-        if (!mbar_wait_cluster(ringf_bar(at), (i / kRing) & 1)) {
-            *abort_flag = 1;
+        if (!mbar_wait<true>(ringf_bar(at), (i / kRing) & 1, abort_flag)) {
+            give_up();
             return -1;
         }
         const int tile = ring[at];
@@ -709,8 +730,8 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
         // ------------------------------------------------ hands out tiles (leader only)
         for (int i = 0, ends = 0; ends < 2; ++i) {  // an end for either epilogue group
             const int at = i % kRing;
-            if (!mbar_wait_cluster(ringe_bar(at), ((i / kRing) & 1) ^ 1)) {
-                *abort_flag = 1;
+            if (!mbar_wait<true>(ringe_bar(at), ((i / kRing) & 1) ^ 1, abort_flag)) {
+                give_up();
                 break;
             }
             const int tile = i == 0 ? cluster_id : num_clusters + atomicAdd(p.next, 1);
@@ -725,7 +746,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
     } else if ((warp == 0 || warp == 2) && lane == 0) {
         // ---------------------------------------------------- TMA copies (both CTAs)
         const bool is_a = warp == 0;
-        int s = 0;
+        int s = 0, stages = 0;
         uint32_t ph = 0;
         for (int i = 0;; ++i) {
             const int tile = take(i, true);
@@ -741,10 +762,11 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             // first summed element; of W, counted from its first row
             const int kb = t.k0 * kStep + (!is_a && q.kind == kDH ? q.v0 : 0);
             for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
-                if (!mbar_wait(empty_bar(s), ph ^ 1u)) {
-                    *abort_flag = 1;
+                if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) {
+                    give_up();
                     break;
                 }
+                ++stages;
                 const int nk = min(C::kKps, t.k_steps - ks);
                 const uint32_t fb = PAIR ? map_to_rank(full_bar(s), leader) : full_bar(s);
                 if (is_a && peer == 0) mbar_expect_tx(full_bar(s), nk * tx);
@@ -766,9 +788,10 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 }
             }
         }
+        stages_of[is_a ? 0 : 1] = stages;
     } else if (warp == 1 && lane == 0 && peer == 0) {
         // ------------------------------------------------ MMA issuer (leader only)
-        int s = 0;
+        int s = 0, stages = 0;
         uint32_t ph = 0;
         bool ok = true;
         for (int tc = 0; ok; ++tc) {
@@ -777,7 +800,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             const TileAt t = walk.at(p, tile);
             const Job& q = p.job[t.job];
             const int buf = tc & 1;
-            if (!mbar_wait(acce_bar(buf), ((tc >> 1) & 1) ^ 1)) {
+            if (!mbar_wait(acce_bar(buf), ((tc >> 1) & 1) ^ 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -787,10 +810,11 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             // 16 summed elements: 32 bytes along a swizzle row, or 16 rows of 128 bytes
             const int astep = q.a_mn ? 2048 >> 4 : 32 >> 4, bstep = q.b_mn ? 2048 >> 4 : 32 >> 4;
             for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
-                if (!mbar_wait(full_bar(s), ph)) {
+                if (!mbar_wait(full_bar(s), ph, nullptr, p.wait_limit)) {
                     ok = false;
                     break;
                 }
+                ++stages;
                 tc_fence_after();
                 const int nk = min(C::kKps, t.k_steps - ks);
                 for (int j = 0; j < nk; ++j) {
@@ -808,9 +832,10 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             }
             if (ok) tc_commit<PAIR>(accf_bar(buf));
         }
-        if (!ok) *abort_flag = 1;
+        if (!ok) give_up();
+        stages_of[2] = stages;
         tc_commit_local<PAIR>(drain_bar);
-        mbar_wait(drain_bar, 0);
+        mbar_wait(drain_bar, 0, nullptr);
     } else if (warp >= 4) {
         // ------------------------------------------------- epilogue (both CTAs)
         const int q4 = warp & 3;
@@ -821,7 +846,8 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             if (PAIR && lane == 0) mbar_arrive_cluster(map_to_rank(ringe_bar(tc % kRing), leader));
             const int buf = tc & 1;
             if (__any_sync(0xFFFFFFFFu, tile < 0)) break;
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(accf_bar(buf), (tc >> 1) & 1));
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(accf_bar(buf), (tc >> 1) & 1, abort_flag));
+            if (!ok) give_up();
             if (!ok || *abort_flag) break;
             tc_fence_after();
             const TileAt t = walk.at(p, tile);
@@ -914,6 +940,19 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync_all();  // neither CTA leaves while the other may still use its memory or barriers
+    if (__builtin_expect(*abort_flag, 0)) {
+        // A wait gave up (both CTAs of a pair know): stages that were filled but not used may still be on their way into
+        // either CTA.  They are waited for before any CTA leaves, with a limit, since a stage that only some of the
+        // copiers filled never completes.
+        if (threadIdx.x == 0 && peer == 0) {
+            int most = max(stages_of[0], stages_of[1]);
+            if (PAIR)
+                for (int i = 0; i < 2; ++i) most = max(most, ld_cluster(map_to_rank(base + C::kOffStages + 4 * i, leader + 1)));
+            for (int i = stages_of[2]; i < most; ++i) mbar_wait(full_bar(i % S), (i / S) & 1, nullptr, kDrainLimit);
+        }
+        __syncthreads();
+        if (PAIR) cluster_sync_all();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_free<PAIR>(tmem);
@@ -1091,6 +1130,9 @@ int max_clusters(const cudaLaunchConfig_t& cfg) {
     return n;
 }
 
+// By how much the polls of a stage's arrival are lowered, per device.
+std::atomic<uint32_t> g_lowered[64];
+
 template <bool PAIR>
 cudaError_t run_gemm(const HeadMaps& maps, HeadParams& p, int64_t T, cudaStream_t st) {
     using C = Cfg<PAIR>;
@@ -1113,6 +1155,9 @@ cudaError_t run_gemm(const HeadMaps& maps, HeadParams& p, int64_t T, cudaStream_
     cfg.numAttrs = 1;
     const int most = max_clusters<PAIR>(cfg);
     if (most <= 0) return cudaErrorLaunchOutOfResources;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    p.wait_limit = kWaitLimit - g_lowered[dev].load(std::memory_order_relaxed);
     for (int j = 0; j < p.jobs; ++j) {
         Job& q = p.job[j];
         const int64_t m = q.kind == kDW ? q.m : T, k = q.kind == kDW ? T : q.k;
@@ -1305,6 +1350,14 @@ cudaError_t head_error_read_clear(int* value) {
     const int zero = 0;
     if (e == cudaSuccess && *value) e = cudaMemcpyToSymbol(g_head_error, &zero, sizeof(int));
     return e;
+}
+
+cudaError_t set_head_wait_limit(uint32_t polls) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    g_lowered[dev].store(kWaitLimit - std::min(polls, kWaitLimit), std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 cudaError_t preload_head_kernels() {

@@ -138,8 +138,9 @@ cudaError_t launch_quantize_rows(RowsParams& p, int grid, bool sr, int sf, int n
 cudaError_t launch_tensor_amax(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int n, float inv_sqrt_n,
                                const uint32_t sign_bits[8], float* amax, int num_sms, cudaStream_t st);
 cudaError_t quant_error_read_clear(int* value);
-// Polls of a tile barrier before the quantizer kernels give up (device-wide;
-// the default is restored by passing quant_wait_limit_default()).
+// Polls of a tile barrier before the quantizer kernels, and the vocabulary
+// loss's products up to their own default, give up (device-wide; the default
+// is restored by passing quant_wait_limit_default()).
 cudaError_t set_quant_wait_limit(uint32_t polls);
 uint32_t quant_wait_limit_default();
 // The row kernel's unit (quantize_rows.cu) keeps its own error word and wait

@@ -81,6 +81,7 @@ uint32_t quant_wait_limit_default() { return kWaitLimit; }
 cudaError_t set_quant_wait_limit(uint32_t polls) {
     cudaError_t e = general_set_wait_limit(polls);
     if (e == cudaSuccess) e = set_sr_wait_limit(polls);
+    if (e == cudaSuccess) e = set_head_wait_limit(polls);
     return e != cudaSuccess ? e : set_rows_wait_limit(polls);
 }
 

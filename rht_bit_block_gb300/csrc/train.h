@@ -96,6 +96,8 @@ size_t head_loss_backward_bytes(int64_t T, int64_t V, int64_t K, int num_sms);
 cudaError_t launch_head_loss(const HeadArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream_t st);
 cudaError_t head_error_read_clear(int* value);
+// Polls of a stage's arrival before the products give up, up to their default.
+cudaError_t set_head_wait_limit(uint32_t polls);
 cudaError_t preload_head_kernels();
 
 }  // namespace ufp4

@@ -327,7 +327,7 @@ def ufp4_device_error_status() -> int:
 
 def ufp4_set_quantize_wait_limit(polls: int):
     """Failure-detection hook: polls of a tile barrier before the quantizer
-    kernels give up (negative: the default)."""
+    kernels, or the vocabulary loss's products, give up (negative: the default)."""
     _check(load().ufp4_set_quantize_wait_limit(polls), "ufp4_set_quantize_wait_limit")
 
 
