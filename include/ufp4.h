@@ -35,9 +35,10 @@
  *    call stays memory-safe).
  *  - Host state: calls may be made from several threads on different
  *    streams.  The library keeps a little process-lifetime state per device,
- *    set up on first use and guarded by locks: a flag that its kernels have
- *    been loaded (done once, before its first launch on the device), the
- *    cached co-residency figures of the GEMM launch, the two internal streams
+ *    set up on first use and guarded by locks or atomic: a flag that its
+ *    kernels have been loaded (done once, before its first launch on the
+ *    device), the cached co-residency figures of the GEMM launches, the wait
+ *    limit of the vocabulary loss's products, the two internal streams
  *    of ufp4_gemm_grouped (created on its first call with two or more
  *    groups) and the device address of the ufp4_gemm_noalloc scratch.  After
  *    cudaDeviceReset that state is stale: do not call the library on that

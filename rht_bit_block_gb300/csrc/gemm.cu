@@ -30,6 +30,7 @@
 // Plain fp32 block scales cannot ride in a block-scaled MMA; they take the
 // two-scale kernel at the end of this file.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -38,6 +39,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/ufp4.h"
+#include "device_figure.h"
 #include "internal.h"
 #include "widen_e5m2.cuh"
 
@@ -1123,7 +1125,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
+    static std::atomic<EncodeTiledFn> kept;
+    EncodeTiledFn fn = kept.load(std::memory_order_relaxed);
     if (!fn) {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -1131,6 +1134,7 @@ EncodeTiledFn encode_fn() {
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             fn = (EncodeTiledFn)f;
+        if (fn) kept.store(fn, std::memory_order_relaxed);
     }
     return fn;
 }
@@ -1216,14 +1220,13 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int grid, int br, int bc, int sf
 // Co-resident two-CTA clusters of the pair kernel on this device (cached).
 template <int KIND, int STAGES, int KPS, int G>
 int pair_clusters(const cudaLaunchConfig_t& cfg) {
-    static int cached[64];
+    static DeviceFigure clusters;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (cached[dev] > 0) return cached[dev];
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<KIND, STAGES, KPS, G>, &cfg) != cudaSuccess) return 0;
-    cached[dev] = n;
-    return n;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    return clusters.get(dev, [&] {
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<KIND, STAGES, KPS, G>, &cfg) == cudaSuccess ? n : 0;
+    });
 }
 
 template <int KIND, int STAGES, int KPS, int G>

@@ -46,6 +46,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "device_figure.h"
 #include "internal.h"
 #include "train.h"
 
@@ -1119,15 +1120,12 @@ bool bf16_maps(CUtensorMap map[2], const void* ptr, int64_t inner, int64_t outer
 
 // Clusters that fit the device at once (per device, from the first launch on it).
 template <bool PAIR>
-int max_clusters(const cudaLaunchConfig_t& cfg) {
-    static int cached[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (cached[dev] > 0) return cached[dev];
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel<PAIR>, &cfg) != cudaSuccess) return 0;
-    cached[dev] = n;
-    return n;
+int max_clusters(int dev, const cudaLaunchConfig_t& cfg) {
+    static DeviceFigure clusters;
+    return clusters.get(dev, [&] {
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel<PAIR>, &cfg) == cudaSuccess ? n : 0;
+    });
 }
 
 // By how much the polls of a stage's arrival are lowered, per device.
@@ -1153,10 +1151,10 @@ cudaError_t run_gemm(const HeadMaps& maps, HeadParams& p, int64_t T, cudaStream_
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int most = max_clusters<PAIR>(cfg);
-    if (most <= 0) return cudaErrorLaunchOutOfResources;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const int most = max_clusters<PAIR>(dev, cfg);
+    if (most <= 0) return cudaErrorLaunchOutOfResources;
     p.wait_limit = kWaitLimit - g_lowered[dev].load(std::memory_order_relaxed);
     for (int j = 0; j < p.jobs; ++j) {
         Job& q = p.job[j];
