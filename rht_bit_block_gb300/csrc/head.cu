@@ -300,18 +300,22 @@ struct PackParams {
 };
 
 // CTA b packs the valid tokens among its rows: it counts those before them,
-// then each warp copies a row at a time.  Rows from the count up to the next
-// multiple of kStep are zeroed: dW sums over them.
-constexpr int kPackRows = 64;  // most rows a CTA takes
+// then, kPackRows rows at a time, each warp copies a row.  Rows from the count
+// up to the next multiple of kStep are zeroed: dW sums over them.  Every CTA
+// reads all targets, so there are no more of them than are resident at once,
+// whatever the tokens (with one for each 64 rows, a million tokens read 137 GB
+// of targets, and a pass over 1048576 x 256 x 256 took 8.6 ms; now 1.1).
+constexpr int kPackRows = 64;
+constexpr int kPackCtas = 5;  // an SM, at 48 registers a thread
 template <bool BACK>
-__global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
+__global__ void __launch_bounds__(256, kPackCtas) head_pack_kernel(const PackParams p) {
     __shared__ int before_s, all_s;
-    __shared__ int place[kPackRows];  // packed row of each of the CTA's rows, or -1
+    __shared__ int place[kPackRows];  // packed row of each of the rows in hand, or -1
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = (int64_t)blockIdx.x * p.rows_per_cta;
-    const int rows = (int)min((int64_t)p.rows_per_cta, p.T - r0);  // none in CTAs past the tokens
+    const int64_t end = min(r0 + p.rows_per_cta, p.T);  // no rows in CTAs past the tokens
     auto valid = [&](int64_t r) {
         const int64_t t = p.targets[r];
         return t >= 0 && t < p.V;
@@ -333,61 +337,65 @@ __global__ void __launch_bounds__(256) head_pack_kernel(const PackParams p) {
     }
     __syncthreads();
     const int count = all_s;
-    if (warp == 0) {
-        int at = before_s;
-        for (int i = 0; i < rows; i += 32) {
-            const bool v = i + lane < rows && valid(r0 + i + lane);
-            const uint32_t which = __ballot_sync(0xFFFFFFFFu, v);
-            if (i + lane < rows) place[i + lane] = v ? at + __popc(which & ((1u << lane) - 1)) : -1;
-            at += __popc(which);
-        }
-    }
+    int next = before_s;  // warp 0's: packed row of the next valid token
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0) *p.count = count;
         for (int i = threadIdx.x; i < p.launches; i += blockDim.x) p.next[i] = 0;
     }
-    __syncthreads();
     auto clear_row = [&](char* row, int64_t bytes) {  // a warp's; 2-byte multiples, 2-byte aligned at least
         const int64_t wide = (uintptr_t)row % 16 == 0 ? bytes / 16 : 0;
         for (int64_t i = lane; i < wide; i += 32) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
         for (int64_t i = wide * 8 + lane; i < bytes / 2; i += 32) reinterpret_cast<uint16_t*>(row)[i] = 0;
     };
-    for (int i = warp; i < rows; i += 8) {
-        const int64_t r = r0 + i;
-        const int at = place[i];
-        if (at < 0) {
-            if (BACK) {
-                const int es = p.dh_f32 ? 4 : 2;
-                if (p.dh) clear_row((char*)p.dh + r * p.ld_dh * es, p.K * es);
-            } else if (lane == 0) {
-                p.loss[r] = 0.0f;
-                p.lse_out[r] = 0.0f;
+    for (int64_t first = r0; first < end; first += kPackRows) {
+        const int rows = (int)min((int64_t)kPackRows, end - first);
+        if (first > r0) __syncthreads();  // the places of the rows before are read
+        if (warp == 0) {
+            for (int i = 0; i < rows; i += 32) {
+                const bool v = i + lane < rows && valid(first + i + lane);
+                const uint32_t which = __ballot_sync(0xFFFFFFFFu, v);
+                if (i + lane < rows) place[i + lane] = v ? next + __popc(which & ((1u << lane) - 1)) : -1;
+                next += __popc(which);
             }
-            continue;
         }
-        const uint4* src = reinterpret_cast<const uint4*>(p.h + r * p.ldh);
-        uint4* dst = reinterpret_cast<uint4*>(p.packed + (int64_t)at * p.Kp);
+        __syncthreads();
+        for (int i = warp; i < rows; i += 8) {
+            const int64_t r = first + i;
+            const int at = place[i];
+            if (at < 0) {
+                if (BACK) {
+                    const int es = p.dh_f32 ? 4 : 2;
+                    if (p.dh) clear_row((char*)p.dh + r * p.ld_dh * es, p.K * es);
+                } else if (lane == 0) {
+                    p.loss[r] = 0.0f;
+                    p.lse_out[r] = 0.0f;
+                }
+                continue;
+            }
+            const uint4* src = reinterpret_cast<const uint4*>(p.h + r * p.ldh);
+            uint4* dst = reinterpret_cast<uint4*>(p.packed + (int64_t)at * p.Kp);
 #pragma unroll 8
-        for (int64_t j = lane; j < p.K / 8; j += 32) dst[j] = src[j];
-        if (lane < p.K % 8) {  // nothing past a row's K elements is read
-            const int64_t j = p.K / 8 * 8 + lane;
-            p.packed[(int64_t)at * p.Kp + j] = p.h[r * p.ldh + j];
-        }
-        if (lane == 0) {
-            p.index[at] = (int)r;
-            RowInfo info = {0.0f, 0.0f, 0.0f, (int)p.targets[r]};
-            if (BACK) {
-                const float l = p.lse[r], w = p.weight ? p.weight[r] : 1.0f;
-                info.lse2 = l * kLog2e;
-                info.weight = w;
-                info.a = w * fmaf(2.0f * p.z, l, 1.0f);
+            for (int64_t j = lane; j < p.K / 8; j += 32) dst[j] = src[j];
+            if (lane < p.K % 8) {  // nothing past a row's K elements is read
+                const int64_t j = p.K / 8 * 8 + lane;
+                p.packed[(int64_t)at * p.Kp + j] = p.h[r * p.ldh + j];
             }
-            p.info[at] = info;
+            if (lane == 0) {
+                p.index[at] = (int)r;
+                RowInfo info = {0.0f, 0.0f, 0.0f, (int)p.targets[r]};
+                if (BACK) {
+                    const float l = p.lse[r], w = p.weight ? p.weight[r] : 1.0f;
+                    info.lse2 = l * kLog2e;
+                    info.weight = w;
+                    info.a = w * fmaf(2.0f * p.z, l, 1.0f);
+                }
+                p.info[at] = info;
+            }
         }
     }
     if (BACK) {
-        const int end = (count + kStep - 1) / kStep * kStep;
-        for (int z = count + blockIdx.x * 8 + warp; z < end; z += gridDim.x * 8)
+        const int last = (count + kStep - 1) / kStep * kStep;
+        for (int z = count + blockIdx.x * 8 + warp; z < last; z += gridDim.x * 8)
             clear_row((char*)(p.packed + (int64_t)z * p.Kp), p.Kp * 2);
     }
 }
@@ -1196,7 +1204,8 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
     p.dh = a.dh;
     p.ld_dh = a.ld_dh;
     p.dh_f32 = a.dh_f32;
-    p.rows_per_cta = (int)std::min<int64_t>(kPackRows, std::max<int64_t>(2, (a.T + 2ll * num_sms - 1) / (2ll * num_sms)));
+    const auto share = [&](int64_t ctas) { return (a.T + ctas * num_sms - 1) / (ctas * num_sms); };
+    p.rows_per_cta = (int)std::max(std::min<int64_t>(kPackRows, std::max<int64_t>(2, share(2))), share(kPackCtas));
     const unsigned grid = (unsigned)std::max<int64_t>(8, (a.T + p.rows_per_cta - 1) / p.rows_per_cta);
     return back ? launch_pdl(head_pack_kernel<true>, dim3(grid), dim3(256), 0, st, p)
                 : launch_pdl(head_pack_kernel<false>, dim3(grid), dim3(256), 0, st, p);
