@@ -1044,12 +1044,23 @@ struct Plan {
 // Forward up to half a tile of tokens, which are then read where they lie (16 x
 // 32000 x 2048: 45 us in pairs, 31 so).  The tiles' widths decide where its sums
 // are joined; with more tokens all widths are the same, so that a row's bits do not
-// depend on how many ignored tokens stand among the others.  Backward (dl, with
-// the same bits from either) up to kAloneBack: 128 x 32000 x 2048 138 us in
-// pairs, 128 so; 300: 178 and 167; 384 x 5000 x 2048: 84 and 76; 256 x 131072 x
-// 4096: 741 and 762, 384: 1070 and 1040, 512: 1150 and 1195.
+// depend on how many ignored tokens stand among the others.
 constexpr int64_t kDirect = kHalf;
-constexpr int64_t kAloneBack = 384;
+
+// Backward (dl, with the same bits from either).  One or three tiles of 128
+// tokens leave half of a pair's last one empty: single CTAs are 3 to 10 %
+// faster (the whole pass, in pairs and so: 128 x 32000 x 2048 140 and 131 us,
+// 128 x 131072 x 4096 758 and 730, 320 x 32000 x 2048 182 and 170, 384 x 131072 x
+// 4096 1118 and 1069).  Two tiles fill a pair, and single CTAs copy W's rows
+// twice; what they gain is a fuller last round, which counts less the more
+// rounds there are: 256 x 5000 x 2048 62 and 58, x 32000 149 and 146, x 77824
+// 285 and 281, x 100000 333 and 333, x 116736 373 and 380, x 131072 411 and 416
+// (and 107 and 110 where pairs' tiles are just one round, x 19456).  Four: 512 x
+// 65536 x 7168 1056 and 1091.
+constexpr int64_t kAloneBack = 3 * kHalf, kAloneVocab = 100000;
+bool alone_backward(int64_t T, int64_t V) {
+    return T <= kAloneBack && (up(T, kHalf) != 2 * kHalf || V <= kAloneVocab);
+}
 
 // Columns of such a tile: all CTAs have as many of them.
 int64_t alone_width(int64_t T, int64_t V, int num_sms) {
@@ -1102,7 +1113,7 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back, int num_sms) {
     p.info = take((int64_t)sizeof(RowInfo) * p.Tp);
     p.packed = take(2 * p.Tp * p.Kp);
     if (back) {
-        p.width = T <= kAloneBack && p.pieces == 1 ? alone_width(T, V, num_sms) : kTile;
+        p.width = alone_backward(T, V) && p.pieces == 1 ? alone_width(T, V, num_sms) : kTile;
         p.dl[0] = take(2 * p.Tp * p.piece);
         p.dl[1] = p.pieces > 1 ? take(2 * p.Tp * p.piece) : p.dl[0];
         p.slices = dh_slices(T, K, p.piece, p.pieces, num_sms);
