@@ -1180,12 +1180,11 @@ cudaError_t run_gemm(const HeadMaps& maps, HeadParams& p, int64_t T, cudaStream_
         const int64_t m = q.kind == kDW ? q.m : T, k = q.kind == kDW ? T : q.k;
         q.group = 2 * m * k <= kResidentA ? 1 << 30 : kGroupM;
     }
-    int64_t tiles = 0;  // with every token valid
+    int64_t tiles = 0;  // with every token valid; the entry points refuse what would not fit 30 bits
     for (int j = 0; j < p.jobs; ++j) {
         const Job& q = p.job[j];
         tiles += up(q.kind == kDW ? q.m : T, C::kRows) / C::kRows * (up(q.n, q.width) / q.width) * q.slices;
     }
-    if (tiles > 0x3FFFFFFF) return cudaErrorNotSupported;
     cfg.gridDim = dim3(ctas * (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, most)));
     cfg.numAttrs = st ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, head_gemm_kernel<PAIR>, maps, p);
