@@ -557,8 +557,9 @@ ufp4_status ufp4_head_loss_backward(const void* h, int64_t ldh, const void* w, i
 /* ufp4_device_error -- reads and clears the library's device error words on
  * the current device (synchronizes the device first).  Every device-side wait
  * of the library is bounded: a kernel whose wait gives up records the event,
- * lets its copies in flight land, releases what it holds and returns, leaving
- * its outputs unspecified.  Returns UFP4_ERR_TIMEOUT, with *code = 1, when
+ * lets its copies in flight land (the GEMM kernels excepted, which do not wait
+ * for theirs), releases what it holds and returns, leaving its outputs
+ * unspecified.  Returns UFP4_ERR_TIMEOUT, with *code = 1, when
  * such a wait has given up since the last call, and UFP4_OK with *code = 0
  * otherwise (UFP4_ERR_CUDA if the device cannot be read).  The library does
  * not check the words on its other calls, which never synchronize. */
