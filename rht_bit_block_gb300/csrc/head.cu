@@ -68,6 +68,10 @@ constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sle
 constexpr uint32_t kSuspendNs = 1000;
 constexpr uint32_t kLook = 1024;  // polls between looks at the abort flag
 constexpr uint32_t kDrainLimit = 1u << 16;  // polls for copies in flight, after a wait has given up
+// The copiers' polls for a free stage, about 70 ms for what takes
+// microseconds: they do not look at the abort flag meanwhile (the look
+// takes 128 x 5000 x 2048 forward from 18.7 to 20.7 us).
+constexpr uint32_t kFreeLimit = 1u << 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A CTA pair's 256 x 256 tile, or a single CTA's 128 x (up to 224) tile.  A
@@ -771,7 +775,7 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
             // first summed element; of W, counted from its first row
             const int kb = t.k0 * kStep + (!is_a && q.kind == kDH ? q.v0 : 0);
             for (int ks = 0; ks < t.k_steps; ks += C::kKps) {
-                if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) {
+                if (!mbar_wait(empty_bar(s), ph ^ 1u, nullptr, kFreeLimit)) {
                     give_up();
                     break;
                 }
