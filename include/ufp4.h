@@ -513,7 +513,9 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
 
 /* ufp4_head_loss -- softmax cross entropy of the logits l = h w^T over the
  * vocabulary, which are never stored: lse[t] = log sum_v exp(l[t, v]) and
- * loss[t] = lse[t] - l[t, targets[t]] + z_loss lse[t]^2.
+ * loss[t] = lse[t] - l[t, targets[t]] + z_loss lse[t]^2.  Logits are the
+ * tensor cores' fp32 sums and exponentials are good to about an ulp: lse and
+ * loss are within a few 1e-7 of themselves on unit-scale logits.
  *   h        device bf16 [tokens x hidden], leading dimension ldh
  *   w        device bf16 [vocab x hidden], leading dimension ldw; both 16-byte
  *            aligned with leading dimensions that are multiples of 8
@@ -534,7 +536,11 @@ ufp4_status ufp4_head_loss(const void* h, int64_t ldh, const void* w, int64_t ld
  * loss[t]: dl[t, v] = token_weight[t] ((1 + 2 z_loss lse[t]) exp(l[t, v] -
  * lse[t]) - [v = targets[t]]), dh = scale dl w, dw = scale dl^T h.  The logits
  * are computed again, a piece of the vocabulary at a time; dl is held in bf16
- * (it is a tensor-core operand), dh and dw are summed in fp32.
+ * (it is a tensor-core operand: up to 2^-8 of an entry, which over many tokens
+ * makes 0.0017 of a gradient, as much as the rounding of a bf16 result), dh and
+ * dw are summed in fp32.  With up to 128 tokens and a vocabulary that is one
+ * piece, dl keeps 16 bits of each entry for dw and all of it at the target for
+ * dh.
  *   h, w, targets, z_loss  as in ufp4_head_loss, lse as it wrote it
  *   token_weight  device float, tokens elements, or NULL (ones)
  *   scale      device float, one element, or NULL (one)
@@ -545,8 +551,8 @@ ufp4_status ufp4_head_loss(const void* h, int64_t ldh, const void* w, int64_t ld
  *              dh and dw NULL
  *   workspace  at least ufp4_head_loss_backward_workspace_size bytes,
  *              256-byte aligned: dl of two pieces of the vocabulary (of 256 MB
- *              or 256 columns each, or of one that is all of it), a copy of
- *              the rows of h that have a target, and fp32 sums of dh */
+ *              or 256 columns each, or of one that is all of it), one or two
+ *              copies of the rows of h that have a target, and fp32 sums of dh */
 ufp4_status ufp4_head_loss_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, size_t* bytes);
 ufp4_status ufp4_head_loss_backward(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* targets,
                                     int64_t tokens, int64_t vocab, int64_t hidden, float z_loss, const float* lse,

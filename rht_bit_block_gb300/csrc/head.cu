@@ -30,7 +30,10 @@
 // dl is rounded to bf16 because the tensor cores multiply it with bf16 W and H:
 // a relative error of at most 2^-8 per entry, as the outputs' own rounding,
 // and unbiased; the common factor `scale` is applied to the fp32 results, so
-// that a uniform weight does not round every entry the same way.
+// that a uniform weight does not round every entry the same way.  Of many
+// tokens' gradients that leaves 0.0024 of the exact ones (2-norm, bf16 results;
+// their own rounding alone 0.0017); of few, where nothing averages it away, dl
+// is kept in two bf16 parts (fine_backward).
 //
 // All products run in one persistent kernel of CTA pairs (tcgen05.mma
 // .cta_group::2, 256 x 256 output tiles, fp32 accumulators in tensor memory,
@@ -63,6 +66,7 @@ constexpr int kStep = 64;                  // summed elements per step (one 128-
 constexpr int kBlockBytes = 64 * 64 * 2;   // 64 rows of 64 bf16: one column block of an MN-major operand
 constexpr int kAtom = 2 * kBlockBytes;     // 128 rows of one step
 constexpr int kThreads = 384;
+constexpr int kFine = kHalf;               // most tokens whose dl is kept in two parts (fine_backward)
 constexpr int kRing = 4;                   // tiles handed out ahead (even: a place serves one epilogue group)
 constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sleep up to kSuspendNs
 constexpr uint32_t kSuspendNs = 1000;
@@ -293,6 +297,7 @@ struct PackParams {
     int* count;
     int* next;                // tile counters of the launches that follow, zeroed
     int launches;
+    int fine;                 // backward: every packed row a second time, behind them all
     float* loss;              // forward: 0 for ignored tokens
     float* lse_out;
     const float* lse;         // backward
@@ -376,13 +381,16 @@ __global__ void __launch_bounds__(256, kPackCtas) head_pack_kernel(const PackPar
                 }
                 continue;
             }
-            const uint4* src = reinterpret_cast<const uint4*>(p.h + r * p.ldh);
-            uint4* dst = reinterpret_cast<uint4*>(p.packed + (int64_t)at * p.Kp);
+            for (int copy = 0; copy <= (BACK ? p.fine : 0); ++copy) {
+                const int64_t row = at + (copy ? count : 0);
+                const uint4* src = reinterpret_cast<const uint4*>(p.h + r * p.ldh);
+                uint4* dst = reinterpret_cast<uint4*>(p.packed + row * p.Kp);
 #pragma unroll 8
-            for (int64_t j = lane; j < p.K / 8; j += 32) dst[j] = src[j];
-            if (lane < p.K % 8) {  // nothing past a row's K elements is read
-                const int64_t j = p.K / 8 * 8 + lane;
-                p.packed[(int64_t)at * p.Kp + j] = p.h[r * p.ldh + j];
+                for (int64_t j = lane; j < p.K / 8; j += 32) dst[j] = src[j];
+                if (lane < p.K % 8) {  // nothing past a row's K elements is read
+                    const int64_t j = p.K / 8 * 8 + lane;
+                    p.packed[row * p.Kp + j] = p.h[r * p.ldh + j];
+                }
             }
             if (lane == 0) {
                 p.index[at] = (int)r;
@@ -398,8 +406,8 @@ __global__ void __launch_bounds__(256, kPackCtas) head_pack_kernel(const PackPar
         }
     }
     if (BACK) {
-        const int last = (count + kStep - 1) / kStep * kStep;
-        for (int z = count + blockIdx.x * 8 + warp; z < last; z += gridDim.x * 8)
+        const int used = count << p.fine, last = (used + kStep - 1) / kStep * kStep;
+        for (int z = used + blockIdx.x * 8 + warp; z < last; z += gridDim.x * 8)
             clear_row((char*)(p.packed + (int64_t)z * p.Kp), p.Kp * 2);
     }
 }
@@ -449,6 +457,10 @@ struct HeadParams {
     float2* part;           // kStats: [row][vocabulary tile]
     int64_t ld_part;
     float* target_logit;
+    int fine;               // backward: dl in two parts (fine_backward)
+    float* rest;            // with `fine`: what the first part leaves of each row's entry at its target
+    const __nv_bfloat16* w;
+    int64_t ldw;
     float* dh_acc;          // fp32 dH of the packed rows (x Kp), or each share of it; null: dH is written at once
     int64_t Kp, Tp;
     int shares;
@@ -482,7 +494,7 @@ struct Walk {
             m_tiles[j] = n_tiles[j] = k_steps[j] = 0;
             if (j >= p.jobs) continue;
             const Job& q = p.job[j];
-            const int m = q.kind == kDW ? q.m : count, k = q.kind == kDW ? count : q.k;
+            const int m = q.kind == kDW ? q.m : count, k = q.kind == kDW ? count << p.fine : q.k;
             m_tiles[j] = (m + ROWS - 1) / ROWS;
             n_tiles[j] = (q.n + q.width - 1) / q.width;
             k_steps[j] = (k + kStep - 1) / kStep;
@@ -900,19 +912,41 @@ head_gemm_kernel(const __grid_constant__ HeadMaps maps, const __grid_constant__ 
                 if (row < count) info = p.info[row];
                 const int end = (q.n + kStep - 1) / kStep * kStep - n0;
                 const int cols = min(q.width, end);
-                uint4* dst = reinterpret_cast<uint4*>(q.dl + row * q.ld_dl + n0);
+                // In two parts, the second ones' rows stand behind all of the first ones', and the zeros that dW's last
+                // step reads behind them both: the rows past the tokens (of the one tile) write those.
+                const bool live = row < count;
+                uint4* dst = reinterpret_cast<uint4*>(q.dl + (p.fine && !live ? row + count : row) * q.ld_dl + n0);
+                uint4* second = reinterpret_cast<uint4*>(q.dl + (live ? row + count : row + kHalf) * q.ld_dl + n0);
                 for (int c = 0; c < cols; c += 32) {
                     tmem_ld32(acc + c, r);
-                    grad_chunk(r, info, n0 + c, row < count ? q.n - (n0 + c) : 0);
+                    grad_chunk(r, info, n0 + c, live ? q.n - (n0 + c) : 0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (c + 8 * i < cols)
-                            dst[c / 8 + i] =
+                        if (c + 8 * i < cols) {
+                            const uint4 v =
                                 make_uint4(pack_bf16(r[8 * i], r[8 * i + 1]), pack_bf16(r[8 * i + 2], r[8 * i + 3]),
                                            pack_bf16(r[8 * i + 4], r[8 * i + 5]), pack_bf16(r[8 * i + 6], r[8 * i + 7]));
+                            dst[c / 8 + i] = v;
+                            if (!p.fine) continue;
+                            const uint32_t first[4] = {v.x, v.y, v.z, v.w};
+                            uint32_t lo[4];
+                            const int at = info.target - (n0 + c + 8 * i);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float a = r[8 * i + 2 * j] - __uint_as_float(first[j] << 16);
+                                const float b = r[8 * i + 2 * j + 1] - __uint_as_float(first[j] & 0xFFFF0000u);
+                                if (at == 2 * j) p.rest[row] = a;
+                                if (at == 2 * j + 1) p.rest[row] = b;
+                                lo[j] = pack_bf16(a, b);
+                            }
+                            second[c / 8 + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
                 }
                 if (n0 + q.width >= q.n)
-                    for (int c = cols; c < end; c += 8) dst[c / 8] = make_uint4(0, 0, 0, 0);
+                    for (int c = cols; c < end; c += 8) {
+                        dst[c / 8] = make_uint4(0, 0, 0, 0);
+                        if (p.fine) second[c / 8] = make_uint4(0, 0, 0, 0);
+                    }
             } else {
                 // a piece's dl whole (zeros beside the valid rows and columns: dH and dW sum over them);
                 // dH of the valid rows; rows of dW
@@ -1007,8 +1041,9 @@ __global__ void __launch_bounds__(256) head_join_kernel(const HeadParams p, int 
     loss[token] = valid ? fmaf(z * l, l, l - p.target_logit[row]) : 0.0f;
 }
 
-// dH from the fp32 sums of the packed rows, or their shares in order: a row's
-// columns 256 at a time over the grid's second dimension.
+// dH from the fp32 sums of the packed rows, or their shares in order, and with
+// dl in two parts what the first left at the target: a row's columns 256 at a
+// time over the grid's second dimension.
 __global__ void __launch_bounds__(256) head_dh_kernel(const HeadParams p, int cols) {
     griddep_wait();
     griddep_launch();
@@ -1016,11 +1051,14 @@ __global__ void __launch_bounds__(256) head_dh_kernel(const HeadParams p, int co
     if (row >= *p.count) return;
     const float scale = p.scale ? *p.scale : 1.0f;
     const int64_t out = (int64_t)p.index[row] * p.ld_dh, step = p.Tp * p.Kp;
+    const float rest = p.fine ? p.rest[row] : 0.0f;
+    const __nv_bfloat16* w = p.w + (int64_t)p.info[row].target * p.ldw;
     for (int64_t c = blockIdx.y * 256 + threadIdx.x; c < cols; c += gridDim.y * 256) {
         const float* part = p.dh_acc + row * p.Kp + c;
         float s = 0.0f;
 #pragma unroll 8
         for (int i = 0; i < p.shares; ++i) s += part[i * step];
+        if (p.fine) s += rest * __bfloat162float(w[c]);
         s *= scale;
         if (p.dh_f32)
             ((float*)p.dh)[out + c] = s;
@@ -1039,8 +1077,10 @@ struct Plan {
     int64_t launches;        // of the product kernel
     int64_t slices;          // backward: shares of a piece's dH
     bool direct;             // forward: tokens in place, none packed
+    bool fine;               // backward: dl in two parts
+    bool sums;               // backward: dH as fp32 sums first
     int64_t width, tiles;    // columns of a tile of logits; forward: tiles of the vocabulary
-    size_t count, next, index, info, packed, part, target, dl[2], acc, total;
+    size_t count, next, index, info, packed, part, target, dl[2], rest, acc, total;
 };
 
 // Few tokens' logits are computed by single CTAs: a pair's tile costs the same
@@ -1072,6 +1112,20 @@ int64_t alone_width(int64_t T, int64_t V, int num_sms) {
     const int64_t rounds = (all + (int64_t)kAlone * num_sms - 1) / ((int64_t)kAlone * num_sms);
     return std::max<int64_t>(32, up((all + rounds * num_sms - 1) / (rounds * num_sms), 16));
 }
+
+// The entry of dl at a token's target, weight (p - 1), dominates the token's
+// row, and its rounding to bf16 scales the token's whole gradient by up to
+// 2^-8.  Over many tokens these errors average to 0.0017 of the result; of few
+// they do not (10 x 12140 x 3200: dh and dw 0.0028 from the exact ones, 0.0017
+// of which are the bf16 results' own rounding).  Up to kFine tokens dl is
+// therefore kept in two bf16 parts, 16 bits of every entry: dW sums over both
+// (twice the summed index, which is still few steps), and dH gets what the
+// first part left at the target from head_dh_kernel.  One tile of 128 tokens,
+// so that the second parts are rows of the same 256.  It costs 2 % of the pass
+// for 16 tokens (16 x 32000 x 2048 124.6 -> 127.1 us), 5 to 10 % for 128 (x
+// 32000 x 2048 129.7 -> 136.1, x 131072 x 4096 729 -> 799); second parts for
+// tiles of dW with a target only: 130, 136 and 751 us.
+bool fine_backward(int64_t T, int64_t pieces) { return T <= kFine && pieces == 1; }
 
 // A piece's dl takes about kPieceBytes.  Wider pieces mean fewer launches,
 // longer sums and fewer passes over the fp32 dH; narrower ones a smaller
@@ -1121,8 +1175,10 @@ Plan make_plan(int64_t T, int64_t V, int64_t K, bool back, int num_sms) {
         p.dl[0] = take(2 * p.Tp * p.piece);
         p.dl[1] = p.pieces > 1 ? take(2 * p.Tp * p.piece) : p.dl[0];
         p.slices = dh_slices(T, K, p.piece, p.pieces, num_sms);
-        const int64_t shares = p.slices > 1 ? p.slices * p.pieces : (p.pieces > 1 ? 1 : 0);
-        p.acc = shares ? take(4 * p.Tp * p.Kp * shares) : 0;
+        p.fine = fine_backward(T, p.pieces);
+        p.rest = take(4 * p.Tp);
+        p.sums = p.pieces > 1 || p.slices > 1 || p.fine;
+        p.acc = p.sums ? take(4 * p.Tp * p.Kp * (p.slices > 1 ? p.slices * p.pieces : 1)) : 0;
     } else {
         p.direct = T <= kDirect;
         p.width = p.direct ? alone_width(T, V, num_sms) : kTile;
@@ -1210,6 +1266,7 @@ cudaError_t run_pack(const HeadArgs& a, const Plan& pl, bool back, int num_sms, 
     p.count = (int*)(ws + pl.count);
     p.next = (int*)(ws + pl.next);
     p.launches = (int)pl.launches;
+    p.fine = pl.fine;
     p.loss = a.loss;
     p.lse_out = a.lse;
     p.lse = a.lse;
@@ -1251,7 +1308,11 @@ HeadParams make_params(const HeadArgs& a, const Plan& pl) {
     p.part = (float2*)(ws + pl.part);
     p.target_logit = (float*)(ws + pl.target);
     p.ld_part = pl.tiles;
-    p.dh_acc = pl.pieces > 1 || pl.slices > 1 ? (float*)(ws + pl.acc) : nullptr;
+    p.fine = pl.fine;
+    p.rest = (float*)(ws + pl.rest);
+    p.w = (const __nv_bfloat16*)a.w;
+    p.ldw = a.ldw;
+    p.dh_acc = pl.sums ? (float*)(ws + pl.acc) : nullptr;
     p.Kp = pl.Kp;
     p.scale = a.scale;
     p.dh = a.dh;
@@ -1360,7 +1421,7 @@ cudaError_t launch_head_loss_backward(const HeadArgs& a, int num_sms, cudaStream
         if (alone) p.job[0].width = (int)pl.width;
         if (p.jobs) e = alone ? run_gemm<false>(maps, p, a.T, st) : run_gemm<true>(maps, p, a.T, st);
     }
-    if (e == cudaSuccess && a.dh && (pl.pieces > 1 || pl.slices > 1))
+    if (e == cudaSuccess && a.dh && pl.sums)
         e = launch_pdl(head_dh_kernel, dim3((unsigned)a.T, (unsigned)std::min<int64_t>((a.K + 255) / 256, 65535)), dim3(256),
                        0, st, make_params(a, pl), (int)a.K);
     return e;
