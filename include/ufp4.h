@@ -431,8 +431,9 @@ ufp4_status ufp4_round_levels(int32_t grid, int32_t rounding, int32_t scale_fmt,
  * The training step between the GEMMs: what a feed-forward block and the
  * vocabulary head of a model need around the quantized GEMMs of FPROP, DGRAD
  * and WGRAD [UFP4-method].  These calls take any row pitch and any alignment
- * of their elements (16-byte aligned rows run the vectorized kernels) and
- * any column count unless said otherwise; non-finite values are inside their
+ * of their elements and any column count unless said otherwise (16-byte aligned
+ * rows of a multiple of 8 columns run the vectorized kernels, others take two to
+ * five times as long); non-finite values are inside their
  * contract.  The rules above on ownership, asynchrony and errors hold, and
  * the kernels are launched as programmatic dependents on non-default streams.
  *
@@ -445,7 +446,8 @@ ufp4_status ufp4_round_levels(int32_t grid, int32_t rounding, int32_t scale_fmt,
  * aligned.  The scale is the truncation-free one [2D-block]: e the least
  * integer with M <= 448 * 2^e (M the block's amax), clamped to at least -127,
  * stored as e + 127; codes are v * 2^-e rounded to E4M3, nearest even, a zero
- * code as +0.  A block holding a NaN or an infinity gets scale byte 255 and
+ * code as +0: within 2^-4 of an element of at least 2^(e-6), within 2^(e-10) of
+ * a smaller one.  A block holding a NaN or an infinity gets scale byte 255 and
  * codes 0x7F and reads back as NaN; a finite value that rounds to 2^128
  * (above 248 * 2^120) reads back as an infinity.  tensor_amax is unused. */
 typedef enum { UFP4_BF16 = 0, UFP4_F32 = 1 } ufp4_dtype;

@@ -10,8 +10,9 @@
 // (448, 512) * 2^e would lose up to an eighth of its value, a bias on exactly
 // the outliers that a backward pass depends on most.  Eight bits are the
 // point of a checkpoint: it halves (bf16) or quarters (fp32) what a layer
-// keeps between its forward and its backward pass, at a relative error of at
-// most 2^-4 per element.
+// keeps between its forward and its backward pass.  Its error is at most 2^-4
+// of an element of at least 2^(e-6); smaller ones, below M 2^-14 or so, are
+// off by up to 2^(e-10), half of E4M3's smallest step, and can become 0.
 //
 // A block that holds a NaN or an infinity stores scale byte 255 and 0x7F
 // codes: it reads back as NaN, so an overflow is still seen in the gradients.

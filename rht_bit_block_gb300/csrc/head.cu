@@ -21,11 +21,11 @@
 // products-and-sums per logit; keeping the logits would cost 4 bytes each.
 //
 // The tensor cores bound it from about a thousand tokens on: 8192 tokens (a
-// tenth ignored) x 50001 x 2048 forward 0.88 ms when run without a pause, 1720
-// TFLOP/s, and 4096 x 65536 x 7168 with the gradients 9.0 ms, 1710 TFLOP/s with
-// the recomputed logits (the library's bf16 product sustains 1714 there, and
-// 1924 in a burst).  With few tokens it is W: 16 tokens x 65536 x 7168 forward
-// 148 us, 6.35 TB/s.
+// tenth ignored) x 50001 x 2048 forward 0.86 to 0.91 ms by box when run without
+// a pause, 1660 to 1750 TFLOP/s, and 4096 x 65536 x 7168 with the gradients 9.0 to
+// 9.3 ms, 1650 to 1710 TFLOP/s with the recomputed logits (the library's bf16
+// product sustains 1714, and 1924 in a burst).  With few tokens it is W: 16
+// tokens x 65536 x 7168 forward 149 us, 6.3 TB/s.
 //
 // dl is rounded to bf16 because the tensor cores multiply it with bf16 W and H:
 // a relative error of at most 2^-8 per entry, as the outputs' own rounding,
@@ -85,7 +85,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // stages: 4096 x 16384 x 2048 logits 193 us, two-step stages 174 us).  A
 // single CTA's tile is for reading W once: 224 columns leave room for a fifth
 // stage (16 tokens, 131072 x 2048, when first built: 256 columns and four
-// stages 124 us, 224 and five 111 us, 96 and eight 173 us; now 91 us, 5.9 TB/s).
+// stages 124 us, 224 and five 111 us, 96 and eight 173 us; now 93 us, 5.8 TB/s).
 template <bool PAIR>
 struct Cfg {
     static constexpr int kRows = PAIR ? kTile : kHalf;   // rows of a tile
@@ -1122,16 +1122,16 @@ int64_t alone_width(int64_t T, int64_t V, int num_sms) {
 // (twice the summed index, which is still few steps), and dH gets what the
 // first part left at the target from head_dh_kernel.  One tile of 128 tokens,
 // so that the second parts are rows of the same 256.  It costs 2 % of the pass
-// for 16 tokens (16 x 32000 x 2048 124.6 -> 127.1 us), 5 to 10 % for 128 (x
+// for 16 tokens (16 x 32000 x 2048 124.6 -> 127.1 us), 3 to 10 % for 128 (x
 // 32000 x 2048 129.7 -> 136.1, x 131072 x 4096 729 -> 799); second parts for
 // tiles of dW with a target only: 130, 136 and 751 us.
 bool fine_backward(int64_t T, int64_t pieces) { return T <= kFine && pieces == 1; }
 
 // A piece's dl takes about kPieceBytes.  Wider pieces mean fewer launches,
 // longer sums and fewer passes over the fp32 dH; narrower ones a smaller
-// workspace, and below 129 MB a dl that L2 holds, which measures no faster:
-// loss + gradients of 4096 x 65536 x 7168 take 8.9, 8.7 and 8.65 ms with 64,
-// 128 and 256 MB, of 2047 x 50001 x 2048 (a third ignored) 887, 815 and 780 us.
+// workspace, and below 129 MB a dl that L2 holds, which measures no faster: the
+// gradients of 4096 x 65536 x 7168 take 7.33, 7.00 and 6.90 ms with 64, 128 and
+// 256 MB, of 2047 x 50001 x 2048 (a third ignored) 671, 613 and 610 us.
 constexpr int64_t kPieceBytes = 256ll << 20;
 
 // dH has few tiles, each with a long sum, where there are few tokens (16

@@ -25,10 +25,19 @@
 // Measured on a GB300: forward 16384 x 7168 fp32 214 us, 6.05 TB/s (with both
 // 16-byte halves of a lane's 8 fp32 fetched apart, so that every sector came
 // twice: 248 us; without the copies ahead, one row a CTA: 278 us).  Backward
-// 8192 x 2048 32 us with the 4 us of the dgamma kernel, 16384 x 7168 164 us,
+// 8192 x 2048 31 us with the 5 us of the dgamma kernel, 16384 x 7168 164 us,
 // 5.0 TB/s: 512 threads an SM without a spill are its optimum (768 threads at
 // 80 registers, spilling 44 bytes: 45 and 210 us; the decoded row kept beside
-// dy gamma, spilling 140: 38 and 212 us; two rows ahead: 32 and 159 us).
+// dy gamma, spilling 140: 38 and 212 us; two rows ahead: 32 and 159 us).  That
+// is for up to 8192 columns.  Wider rows take CTAs of more than 256 threads,
+// built for up to 1024 with 64 registers a thread, of which the backward pass
+// spills about 570 bytes: 4096 x 8192 59 us (4.0 TB/s), x 12288 186 us (1.9), x
+// 16384 219 us (2.2), 2048 x 32768 216 us (2.2); forward 99 us (6.1) there.
+//
+// Rows off 16-byte alignment, and widths that are no multiple of 8, are read
+// and written element by element, with nothing copied ahead: 8192 x 2048 from
+// bf16 takes 25 us forward and 28 backward, with x or dy one element off 78 and
+// 76, 8192 x 2047 105 and 80, 8192 x 2049 93 and 126 (fp32 dy: 107).
 #include <algorithm>
 
 #include "ckpt8.cuh"
