@@ -38,7 +38,7 @@
  *    set up on first use and guarded by locks or atomic: a flag that its
  *    kernels have been loaded (done once, before its first launch on the
  *    device), the cached co-residency figures of the GEMM launches, the wait
- *    limit of the vocabulary loss's products, the two internal streams
+ *    limit of the vocabulary loss's and the 8-bit products, the two internal streams
  *    of ufp4_gemm_grouped (created on its first call with two or more
  *    groups) and the device address of the ufp4_gemm_noalloc scratch.  After
  *    cudaDeviceReset that state is stale: do not call the library on that
@@ -513,6 +513,82 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
                                    float* dgamma, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
                                    cudaStream_t stream);
 
+/* ufp4_layer_norm -- residual add and layer norm of each row: s = x + residual
+ * (fp32), m = mean(s), rstd = 1 / sqrt(mean((s - m)^2) + eps), y = (s - m) rstd
+ * gamma + beta.  Mean and variance are fp32, the variance in a second pass over
+ * the row; a row that holds a NaN or an infinity becomes NaN.
+ *   x, residual, total, y   as in ufp4_rms_norm
+ *   gamma, beta  device bf16 or fp32 (gamma_dtype, both), cols elements; beta
+ *             may be NULL (zeros)
+ *   eps       > 0
+ *   mean, rstd  device float, rows elements, written unless NULL
+ * 1 <= cols <= 32768 (UFP4_ERR_UNSUPPORTED beyond). */
+ufp4_status ufp4_layer_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* residual, int64_t ld_residual,
+                            const void* gamma, const void* beta, int32_t gamma_dtype, int64_t rows, int64_t cols, float eps,
+                            void* y, int64_t ldy, void* total, int64_t ld_total, float* mean, float* rstd,
+                            cudaStream_t stream);
+
+/* ufp4_layer_norm_backward -- the gradients of ufp4_layer_norm at the rows s
+ * with h = (s - m) rstd and q = dy gamma: dx = rstd (q - mean(q) - h mean(q h)) +
+ * dtotal, which is the gradient of x and of residual alike, dgamma = sum over
+ * the rows of dy h, dbeta = sum over the rows of dy (fp32, in an order that
+ * depends on the shape, the types, the alignment and the device only).
+ *   dy         device bf16 or fp32 (dy_dtype), leading dimension ld_dy
+ *   x          device bf16 or fp32 (x_dtype), leading dimension ldx: s, that is x
+ *              of the forward call, or its `total` where there was a residual.
+ *              There is no 8-bit checkpoint of a layer norm: its error is
+ *              relative to s, and the gradient depends on s - m.
+ *   mean, rstd what ufp4_layer_norm wrote
+ *   dtotal     device bf16, the gradient of `total`, or NULL
+ *   dx         device bf16, written
+ *   dgamma, dbeta  device float, cols elements, written (zeros when rows is 0)
+ *   workspace  at least ufp4_layer_norm_backward_workspace_size bytes,
+ *              256-byte aligned; contents on entry are ignored. */
+ufp4_status ufp4_layer_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+ufp4_status ufp4_layer_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dtype, const void* x, int64_t ldx,
+                                     int32_t x_dtype, const float* mean, const float* rstd, const void* gamma,
+                                     int32_t gamma_dtype, const void* dtotal, int64_t ld_dtotal, int64_t rows, int64_t cols,
+                                     void* dx, int64_t ld_dx, float* dgamma, float* dbeta, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream);
+
+/* 8-bit operands with a scale for each block of 128, for the linear layers that
+ * keep 8 bits [2D-block, section on mixed precision], with the fp32 scale of
+ * the codebooks [UFP4-data]: a qtensor of rows x cols with one E4M3 byte per
+ * element (codes 16-byte aligned, codes_ld a multiple of 16, at least cols) and
+ * fp32 scales, one for each block of 128 elements of a row (block_rows 1) or
+ * square block of 128 x 128 (block_rows 128): ceil(rows / block_rows) x
+ * ceil(cols / 128) of them, scales_ld >= ceil(cols / 128); blocks at the edges
+ * are short.  tensor_amax is unused.
+ *
+ * ufp4_fp8_quantize -- x to such operands: s = max(fp32(M / 448), 2^-126), M
+ * the block's amax, and codes fp32(x * fp32(1 / s)) rounded to E4M3, nearest
+ * even, a zero code as +0.  A block holding a NaN or an infinity gets M / 448 and
+ * codes 0x7F and reads back as NaN.
+ *   x        device bf16 or fp32 (x_dtype), rows x cols, leading dimension ld
+ *   block_rows  1 or 128
+ *   rowwise  written unless NULL: rows x cols, blocks along cols
+ *   colwise  written unless NULL: x^T, cols x rows, blocks along rows; not both
+ *            NULL.  Both come from one read of x.  Of square blocks the two have
+ *            the same codes and scales, transposed.
+ * Bytes between cols and codes_ld are left as they were.  Extents up to 2^30. */
+ufp4_status ufp4_fp8_quantize(const void* x, int64_t ld, int32_t x_dtype, int64_t rows, int64_t cols, int32_t block_rows,
+                              const ufp4_qtensor* rowwise, const ufp4_qtensor* colwise, cudaStream_t stream);
+
+/* ufp4_fp8_gemm -- D = A B^T of two such operands, both along the summed index
+ * K = A->cols = B->cols [UFP4-method, the quantized GEMM]: FPROP Y = X W^T takes
+ * X (blocks of rows) and W (square blocks), DGRAD dX = dY W takes dY and W's
+ * colwise operand, WGRAD dW = dY^T X the colwise operands of dY and X.  A block's
+ * products are summed in fp32 by the tensor cores and added, times both scales,
+ * in fp32.  A product of two scales outside the range of normal fp32 numbers
+ * loses the bits that fp32 does.
+ *   a_block_rows, b_block_rows  1 or 128
+ *   D         device bf16 or fp32 (d_dtype) [A->rows x B->rows], leading
+ *             dimension ldd; written, or added to with accumulate = 1 (fp32 only)
+ * Any extents up to 2^30 (K = 0 gives zeros) with at most about 2^27 tiles of
+ * 128 x 128 (UFP4_ERR_UNSUPPORTED beyond).  Results do not depend on timing. */
+ufp4_status ufp4_fp8_gemm(const ufp4_qtensor* A, int32_t a_block_rows, const ufp4_qtensor* B, int32_t b_block_rows, void* D,
+                          int64_t ldd, int32_t d_dtype, int32_t accumulate, cudaStream_t stream);
+
 /* ufp4_head_loss -- softmax cross entropy of the logits l = h w^T over the
  * vocabulary, which are never stored: lse[t] = log sum_v exp(l[t, v]) and
  * loss[t] = lse[t] - l[t, targets[t]] + z_loss lse[t]^2.  Logits are the
@@ -575,7 +651,7 @@ ufp4_status ufp4_device_error(int32_t* code);
 
 /* ufp4_set_quantize_wait_limit -- failure-detection hook (no counterpart in
  * the pages).  Sets how many times the quantizer kernels, and the products of
- * the vocabulary loss, poll for a tile's arrival before they give up, on the
+ * the vocabulary loss and of ufp4_fp8_gemm, poll for a tile's arrival before they give up, on the
  * current device, for later launches; polls < 0 restores the default (2^24
  * polls, 2^22 of the products: seconds).  With polls = 0 the first wait of
  * every such CTA (of the products: cluster) gives up at once: the kernel

@@ -73,8 +73,8 @@ bool is_pow2(int64_t v) { return v >= 1 && (v & (v - 1)) == 0; }
 
 float inv_sqrt_n(int n) { return (float)(1.0 / std::sqrt((double)n)); }
 
-// Loads every kernel of the library on the current device, and sets the norm's
-// shared-memory limits, once, before the library's first launch there (see the
+// Loads every kernel of the library on the current device, and sets the norms'
+// and the 8-bit product's shared-memory limits, once, before the library's first launch there (see the
 // preload functions).
 void ensure_loaded() {
     static std::mutex mu;
@@ -90,6 +90,9 @@ void ensure_loaded() {
     preload_round_levels_kernels();
     preload_glu_kernels();
     preload_norm_kernels();
+    preload_layer_norm_kernels();
+    preload_fp8_quantize_kernels();
+    preload_fp8_gemm_kernels();
     preload_head_kernels();
     cudaGetLastError();  // a failed query shows up again at the launch
     done[dev] = true;

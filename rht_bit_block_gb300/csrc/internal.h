@@ -139,7 +139,7 @@ cudaError_t launch_tensor_amax(const uint16_t* x, int64_t rows, int64_t cols, in
                                const uint32_t sign_bits[8], float* amax, int num_sms, cudaStream_t st);
 cudaError_t quant_error_read_clear(int* value);
 // Polls of a tile barrier before the quantizer kernels, and the vocabulary
-// loss's products up to their own default, give up (device-wide; the default
+// loss's and the 8-bit products up to their own default, give up (device-wide; the default
 // is restored by passing quant_wait_limit_default()).
 cudaError_t set_quant_wait_limit(uint32_t polls);
 uint32_t quant_wait_limit_default();

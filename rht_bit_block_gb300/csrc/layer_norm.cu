@@ -1,0 +1,578 @@
+// Residual add and layer norm, before the projections of a block (UFP4
+// summary, section 方法: the quantized GEMMs of FPROP, DGRAD and WGRAD take what
+// this writes), and its gradients.
+//
+//   forward:   s = x + residual, m = mean s, r = (mean (s - m)^2 + eps)^-1/2,
+//              y = (s - m) r gamma + beta, total = bf16(s)
+//   backward:  h = (s - m) r, q = dy gamma,
+//              dx = r (q - mean q - h mean(q h)) + dtotal,
+//              dgamma = sum over rows of dy h, dbeta = sum over rows of dy
+//
+// The variance is the mean of squared differences from the mean, in a second
+// pass over the row, which is in registers: the mean square minus the squared
+// mean loses all digits of a row that lies far from zero.
+//
+// Memory bounds both passes.  As in the RMS norm (norm.cu) a warp takes 256
+// neighbouring columns a step and each lane copies its elements of the group's
+// next row into shared memory while the current one is worked on.  The backward
+// pass keeps two rows there: it reads a row twice, once for its sums and once for
+// dx, so that registers hold nothing of it but the running dgamma and dbeta of the
+// lane's columns.  A CTA adds its groups' sums, and a second kernel the CTAs', in
+// their order: results do not depend on timing.
+#include <algorithm>
+
+#include "ckpt8.cuh"
+#include "internal.h"
+#include "norm_rows.cuh"
+#include "train.h"
+#include "ufp4_device.cuh"
+
+namespace ufp4 {
+namespace {
+
+constexpr int kForwardThreads = 1024;   // threads that an SM's registers should hold
+constexpr int kBackwardThreads = 512;
+constexpr size_t kMostSmem = 232448 - 1024;
+
+struct LnParams {
+    const void* x;             // forward: x; backward: the normalised rows
+    const void* dy;
+    const __nv_bfloat16* add;  // residual, or dtotal
+    const void* gamma;
+    const void* beta;
+    int64_t ldx, ld_dy, ld_add;
+    int x_f32, dy_f32, gamma_f32;  // x and dy: where they are read without copies
+    int vec;                       // the same: all rows are aligned to their vectors
+    int64_t rows;
+    int cols;
+    int group_warps, groups;       // warps a row, rows a CTA works on at once
+    float inv_cols, eps;
+    __nv_bfloat16* y;
+    __nv_bfloat16* out;            // total, or dx
+    int64_t ldy, ld_out;
+    float* mean;
+    float* rstd;
+    float* partials;               // backward, [part][2][cols]; null: no sums
+};
+
+__device__ __forceinline__ void load8_any(const void* p, int64_t at, int f32, int vec, int n, float v[kVec]) {
+    const char* src = (const char*)p + at * (f32 ? 4 : 2);
+    if (vec) {
+        if (f32) load8<true, true>(src, n, v);
+        else load8<false, true>(src, n, v);
+    } else {
+        if (f32) load8<true, false>(src, n, v);
+        else load8<false, false>(src, n, v);
+    }
+}
+// gamma or beta of eight columns; they stay in L1.
+__device__ __forceinline__ void load_weight8(const void* p, int f32, int vec, int c, int n, float v[kVec]) {
+    if (!vec) {
+        load8_any(p, c, f32, 0, n, v);
+    } else if (f32) {
+        const float4* q = (const float4*)((const float*)p + c);
+        widen8(__ldg(q), __ldg(q + 1), v);
+    } else {
+        widen8(__ldg((const uint4*)((const __nv_bfloat16*)p + c)), v);
+    }
+}
+__device__ __forceinline__ void store8_any(__nv_bfloat16* p, int vec, int n, const float v[kVec]) {
+    if (vec) store8_bf16<true>(p, n, v);
+    else store8_bf16<false>(p, n, v);
+}
+
+// A warp's share of a row in shared memory: one matrix, ITER steps of 256
+// columns.  Copied 16 consecutive bytes a lane, so that every 32-byte sector is
+// fetched once; read as a lane's 8 elements.
+template <bool F32, int ITER>
+struct Copy {
+    static constexpr int kStepBytes = F32 ? 1024 : 512;
+    static constexpr int kBytes = ITER * kStepBytes;
+    static __device__ __forceinline__ void fetch(uint32_t dst, const void* base, int64_t ld, int64_t row, int c0, int cols) {
+        const int lane = threadIdx.x & 31;
+        const char* src = (const char*)base + (row * ld + c0) * (F32 ? 4 : 2) + lane * 16;
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int left = cols - c0 - k * kStepCols;
+            if (left <= 0) break;
+            if (lane * (F32 ? 4 : 8) < left) copy16(dst + k * kStepBytes + lane * 16, src + k * kStepBytes);
+            if (F32 && 128 + lane * 4 < left) copy16(dst + k * kStepBytes + 512 + lane * 16, src + k * kStepBytes + 512);
+        }
+    }
+    static __device__ __forceinline__ void read(const uint8_t* src, int k, float v[kVec]) {
+        const uint8_t* p = src + k * kStepBytes + (threadIdx.x & 31) * (F32 ? 32 : 16);
+        if (F32) widen8(*(const float4*)p, *(const float4*)(p + 16), v);
+        else widen8(*(const uint4*)p, v);
+    }
+};
+
+// COPIED: rows are copied ahead (all of them aligned); otherwise they are read
+// where they are, by vectors or by elements.  THREADS: the most a CTA has.
+template <bool F32, bool COPIED, int ITER, int THREADS>
+__global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm_kernel(const LnParams p) {
+    using X = Copy<F32, ITER>;
+    using A = Copy<false, ITER>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float slots[32];
+    griddep_wait();
+    griddep_launch();
+    const Group<true> g(p.group_warps);
+    const int first = g.template first<ITER>();
+    const int c0 = first - g.lane * kVec;  // the warp's first column
+    const int vec = COPIED ? 1 : p.vec;
+    const uint8_t* mine = smem + (threadIdx.x >> 5) * (X::kBytes + A::kBytes);
+    const uint32_t saddr = (uint32_t)__cvta_generic_to_shared(mine);
+    auto fetch = [&](int64_t row) {
+        if (row >= p.rows) return;
+        X::fetch(saddr, p.x, p.ldx, row, c0, p.cols);
+        if (p.add) A::fetch(saddr + X::kBytes, p.add, p.ld_add, row, c0, p.cols);
+    };
+    if (COPIED) fetch(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        float s[ITER][kVec];
+        float sum = 0.0f;
+        if (COPIED) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+        }
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = first + k * kStepCols;
+            const int n = p.cols - c;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) s[k][i] = 0.0f;
+            if (n > 0) {
+                if (COPIED) X::read(mine, k, s[k]);
+                else load8_any(p.x, row * p.ldx + c, F32, vec, n, s[k]);
+                if (p.add) {
+                    float r[kVec];
+                    if (COPIED) A::read(mine + X::kBytes, k, r);
+                    else load8_any(p.add, row * p.ld_add + c, 0, vec, n, r);
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) s[k][i] += r[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) sum += s[k][i];
+        }
+        if (COPIED) {  // the warp's copies are in registers
+            __syncwarp();
+            fetch(row + gridDim.x);
+        }
+        const float mean = g.sum(sum, slots) * p.inv_cols;
+        float var = 0.0f;
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int n = p.cols - (first + k * kStepCols);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const float d = s[k][i] - mean;
+                if (i < n) var = fmaf(d, d, var);
+            }
+        }
+        const float r = rsqrtf(fmaf(g.sum(var, slots), p.inv_cols, p.eps));
+        if (g.warp == 0 && g.lane == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = r;
+        }
+        __nv_bfloat16* y = p.y + row * p.ldy + first;
+        __nv_bfloat16* out = p.out + row * p.ld_out + first;
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = first + k * kStepCols;
+            const int n = p.cols - c;
+            if (n <= 0) break;
+            if (p.out) store8_any(out + k * kStepCols, vec, n, s[k]);
+            float w[kVec], b[kVec];
+            load_weight8(p.gamma, p.gamma_f32, vec, c, n, w);
+            if (p.beta) {
+                load_weight8(p.beta, p.gamma_f32, vec, c, n, b);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) w[i] = fmaf((s[k][i] - mean) * r, w[i], b[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) w[i] = (s[k][i] - mean) * r * w[i];
+            }
+            store8_any(y + k * kStepCols, vec, n, w);
+        }
+    }
+}
+
+// The types of dy and x are given for copied rows (DY32, X32) and looked up
+// otherwise.  SUMS: dgamma and dbeta are summed.
+template <bool DY32, bool X32, bool COPIED, bool SUMS, int ITER, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > kBackwardThreads ? 1 : kBackwardThreads / THREADS)
+layer_norm_backward_kernel(const LnParams p) {
+    using D = Copy<DY32, ITER>;
+    using X = Copy<X32, ITER>;
+    using A = Copy<false, ITER>;
+    constexpr int kWarp = D::kBytes + X::kBytes + A::kBytes;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(8) float slots[64];
+    griddep_wait();
+    griddep_launch();
+    const Group<false> g(p.group_warps);
+    const int first = g.template first<ITER>();
+    const int c0 = first - g.lane * kVec;
+    const int vec = COPIED ? 1 : p.vec;
+    const int64_t stride = (int64_t)gridDim.x * p.groups;
+    const int other = (blockDim.x >> 5) * kWarp;  // from one of the two rows to the other
+    const uint8_t* mine = smem + (threadIdx.x >> 5) * kWarp;
+    const uint32_t saddr = (uint32_t)__cvta_generic_to_shared(mine);
+    auto fetch = [&](int64_t row, int at) {
+        if (row < p.rows) {
+            D::fetch(saddr + at, p.dy, p.ld_dy, row, c0, p.cols);
+            X::fetch(saddr + at + D::kBytes, p.x, p.ldx, row, c0, p.cols);
+            if (p.add) A::fetch(saddr + at + D::kBytes + X::kBytes, p.add, p.ld_add, row, c0, p.cols);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int64_t row = (int64_t)blockIdx.x * p.groups + g.index;
+    float mean_next = 0.0f, rstd_next = 0.0f;
+    auto stats = [&](int64_t r) {
+        if (r >= p.rows) return;
+        mean_next = p.mean[r];
+        rstd_next = p.rstd[r];
+    };
+    if (COPIED) fetch(row, 0);
+    stats(row);
+    uint64_t dgamma[SUMS ? ITER : 1][4], dbeta[SUMS ? ITER : 1][4];
+    if (SUMS) {
+#pragma unroll
+        for (int k = 0; k < ITER; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dgamma[k][i] = dbeta[k][i] = 0;
+    }
+    int at = 0;
+    for (; row < p.rows; row += stride) {
+        const float mean = mean_next, r = rstd_next;
+        const uint64_t minus = pk2(-mean, -mean), r2 = pk2(r, r);
+        if (COPIED) {
+            fetch(row + stride, at ^ other);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
+        }
+        stats(row + stride);
+        const uint8_t* src = mine + at;
+        // dy and the normalised row, step k
+        auto load = [&](int k, int c, int n, uint64_t dy[4], uint64_t h[4]) {
+            float v[kVec];
+            if (COPIED) D::read(src, k, v);
+            else load8_any(p.dy, row * p.ld_dy + c, p.dy_f32, vec, n, v);
+            pair8(v, dy);
+            if (COPIED) X::read(src + D::kBytes, k, v);
+            else load8_any(p.x, row * p.ldx + c, p.x_f32, vec, n, v);
+            pair8(v, h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = mul2(add2(h[i], minus), r2);
+        };
+        uint64_t sq = 0, sqh = 0;
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = first + k * kStepCols;
+            const int n = p.cols - c;
+            if (n <= 0) break;
+            uint64_t dy[4], h[4], w[4];
+            float v[kVec];
+            load(k, c, n, dy, h);  // past the row's end dy is 0
+            load_weight8(p.gamma, p.gamma_f32, vec, c, n, v);
+            pair8(v, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (SUMS) {
+                    dgamma[k][i] = fma2(dy[i], h[i], dgamma[k][i]);
+                    dbeta[k][i] = add2(dy[i], dbeta[k][i]);
+                }
+                const uint64_t q = mul2(dy[i], w[i]);
+                sq = add2(q, sq);
+                sqh = fma2(q, h[i], sqh);
+            }
+        }
+        float2 t, u;
+        up2(sq, t.x, t.y);
+        up2(sqh, u.x, u.y);
+        const float2 sums = g.sum2(make_float2(t.x + t.y, u.x + u.y), slots);
+        const float mq = -sums.x * p.inv_cols, mqh = -sums.y * p.inv_cols;
+        const uint64_t mq2 = pk2(mq, mq), mqh2 = pk2(mqh, mqh);
+        __nv_bfloat16* out = p.out + row * p.ld_out + first;
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = first + k * kStepCols;
+            const int n = p.cols - c;
+            if (n <= 0) break;
+            uint64_t dy[4], h[4], w[4], add[4] = {0, 0, 0, 0};
+            float v[kVec];
+            load(k, c, n, dy, h);
+            load_weight8(p.gamma, p.gamma_f32, vec, c, n, v);
+            pair8(v, w);
+            if (p.add) {
+                if (COPIED) A::read(src + D::kBytes + X::kBytes, k, v);
+                else load8_any(p.add, row * p.ld_add + c, 0, vec, n, v);
+                pair8(v, add);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                up2(fma2(r2, fma2(h[i], mqh2, fma2(dy[i], w[i], mq2)), add[i]), v[2 * i], v[2 * i + 1]);
+            store8_any(out + k * kStepCols, vec, n, v);
+        }
+        if (COPIED) {
+            __syncwarp();  // the warp is done with this row's copies
+            at ^= other;
+        }
+    }
+    if (!SUMS) return;
+    // the groups' sums, added in their order by the last one; no copy is in flight (those past the last row copy
+    // nothing), and their memory is free once every group is here
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);
+    for (int j = 0; j < p.groups; ++j) {
+        if (j) __syncthreads();
+        if (g.index != j) continue;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float* dst = (j == p.groups - 1 ? p.partials + (int64_t)blockIdx.x * 2 * p.cols : sums) + which * p.cols;
+            const float* before = sums + which * p.cols;
+#pragma unroll
+            for (int k = 0; k < ITER; ++k) {
+                const int c = first + k * kStepCols;
+                if (c >= p.cols) break;
+                float v[kVec];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) up2(which ? dbeta[k][i] : dgamma[k][i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    if (c + i < p.cols) dst[c + i] = j ? before[c + i] + v[i] : v[i];
+            }
+        }
+    }
+}
+
+// Rows too wide for a CTA's registers to hold their sums: partial sums of
+// dgamma and dbeta of 256 columns over a share of the rows.
+__global__ void __launch_bounds__(256) layer_norm_columns_kernel(const LnParams p) {
+    griddep_wait();
+    griddep_launch();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= p.cols) return;
+    float dgamma = 0.0f, dbeta = 0.0f;
+#pragma unroll 4
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
+        const int64_t i = row * p.ld_dy + c, j = row * p.ldx + c;
+        const float dy = p.dy_f32 ? ((const float*)p.dy)[i] : __bfloat162float(((const __nv_bfloat16*)p.dy)[i]);
+        const float x = p.x_f32 ? ((const float*)p.x)[j] : __bfloat162float(((const __nv_bfloat16*)p.x)[j]);
+        dgamma = fmaf(dy, (x - p.mean[row]) * p.rstd[row], dgamma);
+        dbeta += dy;
+    }
+    float* dst = p.partials + (int64_t)blockIdx.y * 2 * p.cols + c;
+    dst[0] = dgamma;
+    dst[p.cols] = dbeta;
+}
+
+// dgamma and dbeta: sums over the parts, in their order; a CTA takes 8 of the
+// 2 cols columns (one 32-byte sector a part), 128 slices of parts, then the slices.
+__global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* partials, int parts, int cols, float* dgamma,
+                                                               float* dbeta) {
+    __shared__ float slice[8][128 + 1];
+    griddep_wait();
+    griddep_launch();
+    const int i = threadIdx.x & 7, j = threadIdx.x >> 3;
+    const int c = blockIdx.x * 8 + i;
+    float s = 0.0f;
+    if (c < 2 * cols) {
+#pragma unroll 4
+        for (int q = j; q < parts; q += 128) s += partials[(int64_t)q * 2 * cols + c];
+    }
+    slice[i][j] = s;
+    __syncthreads();
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (w >= 8) return;
+    s = (slice[w][lane] + slice[w][lane + 32]) + (slice[w][lane + 64] + slice[w][lane + 96]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int at = blockIdx.x * 8 + w;
+    if (lane || at >= 2 * cols) return;
+    if (at < cols) dgamma[at] = s;
+    else dbeta[at - cols] = s;
+}
+
+// ------------------------------------------------------------------- shapes
+// Backward, a lane takes up to two steps (up to 8192 columns: 512 threads hold
+// their sums without a spill), then four (up to 16384); wider rows' sums are
+// the columns kernel's.
+constexpr int kMostSummed = 16384;
+Shape backward_shape(int64_t cols) {
+    Shape s;
+    s.iter = cols <= kStepCols ? 1 : (cols <= 32 * kStepCols ? 2 : 4);
+    s.warps = (int)((cols + s.iter * kStepCols - 1) / (s.iter * kStepCols));
+    s.groups = std::max(1, 8 / s.warps);
+    return s;
+}
+
+template <bool F32, bool COPIED, int ITER>
+constexpr int forward_smem(int warps) {
+    return COPIED ? warps * (Copy<F32, ITER>::kBytes + Copy<false, ITER>::kBytes) : 0;
+}
+// Two rows, and at least the sums that the groups but the last leave there.
+template <bool DY32, bool X32, bool COPIED, int ITER>
+constexpr int backward_smem(int warps, int groups, int cols) {
+    const int rows = COPIED ? 2 * warps * groups * (Copy<DY32, ITER>::kBytes + Copy<X32, ITER>::kBytes + Copy<false, ITER>::kBytes) : 0;
+    const int sums = groups > 1 ? 2 * cols * 4 : 0;
+    return rows > sums ? rows : sums;
+}
+int step_bytes(bool dy_f32, bool x_f32) { return kStepCols * ((dy_f32 ? 4 : 2) + (x_f32 ? 4 : 2) + 2); }
+bool copies_fit(const Shape& s, bool dy_f32, bool x_f32) {
+    return (size_t)2 * s.warps * s.groups * s.iter * step_bytes(dy_f32, x_f32) <= kMostSmem;
+}
+
+template <bool F32, bool COPIED, int ITER, int THREADS>
+struct Fwd {
+    static cudaError_t run(const LnParams& p, const Shape& s, int num_sms, cudaStream_t st) {
+        const size_t smem = forward_smem<F32, COPIED, ITER>(s.warps * s.groups);
+        const int64_t grid = std::min<int64_t>(p.rows, (int64_t)num_sms * ctas_per_sm(s, kForwardThreads, smem));
+        return launch_pdl(layer_norm_kernel<F32, COPIED, ITER, THREADS>, dim3((unsigned)grid), dim3(s.threads()), smem, st, p);
+    }
+    // Loads the kernel and lets it have what the widest row it serves takes: the limit belongs to the kernel, which
+    // calls of other widths use at the same time.
+    static cudaError_t load() {
+        constexpr int smem = forward_smem<F32, COPIED, ITER>(THREADS / 32);
+        static_assert(smem <= (int)kMostSmem, "shared memory overflow");
+        cudaFuncAttributes at;
+        cudaFuncGetAttributes(&at, layer_norm_kernel<F32, COPIED, ITER, THREADS>);
+        return cudaFuncSetAttribute(layer_norm_kernel<F32, COPIED, ITER, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    smem);
+    }
+};
+template <bool F32, bool COPIED, typename F>
+cudaError_t forward_by_shape(const Shape& s, F&& f) {
+    if (s.iter == 1) return f(Fwd<F32, COPIED, 1, 256>());
+    if (s.iter == 2) return f(Fwd<F32, COPIED, 2, 256>());
+    return s.threads() > 256 ? f(Fwd<F32, COPIED, 4, 1024>()) : f(Fwd<F32, COPIED, 4, 256>());
+}
+template <typename F>
+cudaError_t forward_kernel(bool f32, bool copied, const Shape& s, F&& f) {
+    if (f32) return copied ? forward_by_shape<true, true>(s, f) : forward_by_shape<true, false>(s, f);
+    return copied ? forward_by_shape<false, true>(s, f) : forward_by_shape<false, false>(s, f);
+}
+
+template <bool DY32, bool X32, bool COPIED, bool SUMS, int ITER, int THREADS>
+struct Bwd {
+    static cudaError_t run(const LnParams& p, const Shape& s, int parts, cudaStream_t st) {
+        const size_t smem = backward_smem<DY32, X32, COPIED, ITER>(s.warps, s.groups, p.cols);
+        return launch_pdl(layer_norm_backward_kernel<DY32, X32, COPIED, SUMS, ITER, THREADS>, dim3((unsigned)parts),
+                          dim3(s.threads()), smem, st, p);
+    }
+    static cudaError_t load() {
+        cudaFuncAttributes at;
+        cudaFuncGetAttributes(&at, layer_norm_backward_kernel<DY32, X32, COPIED, SUMS, ITER, THREADS>);
+        return cudaFuncSetAttribute(layer_norm_backward_kernel<DY32, X32, COPIED, SUMS, ITER, THREADS>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, COPIED ? (int)kMostSmem : 64 * 1024);
+    }
+};
+template <bool DY32, bool X32, bool COPIED, typename F>
+cudaError_t backward_by_shape(const Shape& s, F&& f) {
+    if (s.iter == 1) return f(Bwd<DY32, X32, COPIED, true, 1, 256>());
+    if (s.iter == 2)
+        return s.threads() > 256 ? f(Bwd<DY32, X32, COPIED, true, 2, 512>()) : f(Bwd<DY32, X32, COPIED, true, 2, 256>());
+    return f(Bwd<DY32, X32, COPIED, true, 4, 512>());
+}
+template <typename F>
+cudaError_t backward_kernel(bool dy_f32, bool x_f32, bool copied, const Shape& s, F&& f) {
+    if (s.threads() > kBackwardThreads) return f(Bwd<false, false, false, false, 4, 1024>());
+    if (!copied) return backward_by_shape<false, false, false>(s, f);
+    if (dy_f32) return x_f32 ? backward_by_shape<true, true, true>(s, f) : backward_by_shape<true, false, true>(s, f);
+    return x_f32 ? backward_by_shape<false, true, true>(s, f) : backward_by_shape<false, false, true>(s, f);
+}
+
+LnParams common(const LayerNormArgs& a) {
+    LnParams p = {};
+    p.x = a.x;
+    p.ldx = a.ldx;
+    p.x_f32 = a.x_f32;
+    p.gamma = a.gamma;
+    p.beta = a.beta;
+    p.gamma_f32 = a.gamma_f32;
+    p.rows = a.rows;
+    p.cols = (int)a.cols;
+    p.inv_cols = 1.0f / (float)a.cols;
+    p.eps = a.eps;
+    p.mean = a.mean;
+    p.rstd = a.rstd;
+    return p;
+}
+
+}  // namespace
+
+int layer_norm_parts(int64_t rows, int64_t cols, int num_sms) {
+    const Shape s = backward_shape(cols);
+    if (cols > kMostSummed) {  // shares of the rows, for about eight CTAs an SM
+        const int64_t chunks = (cols + 255) / 256;
+        return (int)std::max<int64_t>(1, std::min<int64_t>(rows, 8 * (int64_t)num_sms / chunks));
+    }
+    const size_t smem = (size_t)2 * s.warps * s.groups * s.iter * step_bytes(true, true);  // narrower types take as many
+    return (int)std::max<int64_t>(1, std::min<int64_t>((rows + s.groups - 1) / s.groups,
+                                                       (int64_t)num_sms * ctas_per_sm(s, kBackwardThreads, smem)));
+}
+
+cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t st) {
+    if (a.rows == 0) return cudaSuccess;
+    LnParams p = common(a);
+    p.add = (const __nv_bfloat16*)a.residual;
+    p.ld_add = a.ld_residual;
+    p.y = (__nv_bfloat16*)a.y;
+    p.ldy = a.ldy;
+    p.out = (__nv_bfloat16*)a.total;
+    p.ld_out = a.ld_total;
+    p.vec = a.cols % kVec == 0 && vec_ok(a.x, a.ldx, a.x_f32 ? 4 : 2, 16) && vec_ok(a.gamma, 0, 1, 16) &&
+            (!a.beta || vec_ok(a.beta, 0, 1, 16)) && vec_ok(a.y, a.ldy, 2, 16) &&
+            (!a.residual || vec_ok(a.residual, a.ld_residual, 2, 16)) && (!a.total || vec_ok(a.total, a.ld_total, 2, 16));
+    const Shape s = forward_shape(a.cols);
+    p.group_warps = s.warps;
+    p.groups = s.groups;
+    return forward_kernel(a.x_f32, p.vec != 0, s, [&](auto k) { return k.run(p, s, num_sms, st); });
+}
+
+cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cudaStream_t st) {
+    LnParams p = common(a);
+    p.dy = a.dy;
+    p.ld_dy = a.ld_dy;
+    p.dy_f32 = a.dy_f32;
+    p.add = (const __nv_bfloat16*)a.dtotal;
+    p.ld_add = a.ld_dtotal;
+    p.out = (__nv_bfloat16*)a.dx;
+    p.ld_out = a.ld_dx;
+    p.partials = a.partials;
+    p.vec = a.cols % kVec == 0 && vec_ok(a.dy, a.ld_dy, a.dy_f32 ? 4 : 2, 16) && vec_ok(a.x, a.ldx, a.x_f32 ? 4 : 2, 16) &&
+            vec_ok(a.gamma, 0, 1, 16) && vec_ok(a.dx, a.ld_dx, 2, 16) && (!a.dtotal || vec_ok(a.dtotal, a.ld_dtotal, 2, 16));
+    const Shape s = backward_shape(a.cols);
+    p.group_warps = s.warps;
+    p.groups = s.groups;
+    const int parts = layer_norm_parts(a.rows, a.cols, num_sms);  // with no rows: one part of zeros
+    cudaError_t e = cudaSuccess;
+    if (a.cols > kMostSummed) {
+        const int64_t grid = std::min<int64_t>(a.rows, num_sms);
+        if (grid)
+            e = backward_kernel(a.dy_f32, a.x_f32, false, s, [&](auto k) { return k.run(p, s, (int)grid, st); });
+        if (e == cudaSuccess)
+            e = launch_pdl(layer_norm_columns_kernel, dim3((unsigned)((a.cols + 255) / 256), (unsigned)parts), dim3(256), 0, st, p);
+    } else {
+        const bool copied = p.vec && copies_fit(s, a.dy_f32, a.x_f32);
+        e = backward_kernel(a.dy_f32, a.x_f32, copied, s, [&](auto k) { return k.run(p, s, parts, st); });
+    }
+    if (e != cudaSuccess) return e;
+    return launch_pdl(layer_norm_join_kernel, dim3((unsigned)((2 * a.cols + 7) / 8)), dim3(1024), 0, st,
+                      (const float*)a.partials, parts, (int)a.cols, a.dgamma, a.dbeta);
+}
+
+cudaError_t preload_layer_norm_kernels() {
+    const Shape fwd[] = {{1, 1, 1}, {2, 1, 1}, {4, 1, 1}, {4, 32, 1}};
+    const Shape bwd[] = {{1, 1, 8}, {2, 8, 1}, {2, 16, 1}, {4, 16, 1}, {4, 32, 1}};
+    for (const Shape& s : fwd)
+        for (int i = 0; i < 4; ++i) forward_kernel(i & 1, i & 2, s, [](auto k) { return k.load(); });
+    for (const Shape& s : bwd)
+        for (int i = 0; i < 8; ++i) backward_kernel(i & 1, i & 2, i & 4, s, [](auto k) { return k.load(); });
+    cudaFuncAttributes at;
+    cudaFuncGetAttributes(&at, layer_norm_columns_kernel);
+    return cudaFuncGetAttributes(&at, layer_norm_join_kernel);
+}
+
+}  // namespace ufp4

@@ -82,18 +82,20 @@ cudaError_t set_quant_wait_limit(uint32_t polls) {
     cudaError_t e = general_set_wait_limit(polls);
     if (e == cudaSuccess) e = set_sr_wait_limit(polls);
     if (e == cudaSuccess) e = set_head_wait_limit(polls);
+    if (e == cudaSuccess) e = set_fp8_wait_limit(polls);
     return e != cudaSuccess ? e : set_rows_wait_limit(polls);
 }
 
-// The first nonzero error word of the three quantizer units and the vocabulary
-// head's (each is cleared).
+// The first nonzero error word of the three quantizer units, the vocabulary
+// head's and the 8-bit product's (each is cleared).
 cudaError_t quant_error_read_clear(int* value) {
-    int v = 0, w = 0, r = 0, h = 0;
+    int v = 0, w = 0, r = 0, h = 0, f = 0;
     cudaError_t e = general_error_read_clear(&v);
     if (e == cudaSuccess) e = sr_error_read_clear(&w);
     if (e == cudaSuccess) e = rows_error_read_clear(&r);
     if (e == cudaSuccess) e = head_error_read_clear(&h);
-    *value = v ? v : (w ? w : (r ? r : h));
+    if (e == cudaSuccess) e = fp8_error_read_clear(&f);
+    *value = v ? v : (w ? w : (r ? r : (h ? h : f)));
     return e;
 }
 

@@ -1,6 +1,7 @@
 // Internal launch interface of the training-step operators between the GEMMs
-// (residual RMS norm and gated activation with 8-bit checkpoints, vocabulary
-// loss): between their C entry points (train_api.cu) and the kernels.
+// (residual RMS norm and gated activation with 8-bit checkpoints, layer norm,
+// vocabulary loss, 8-bit projections): between their C entry points
+// (train_api.cu, fp8_api.cu) and the kernels.
 #pragma once
 
 #include <cstddef>
@@ -70,6 +71,66 @@ int norm_parts(int64_t rows, int64_t cols, int num_sms);
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_rms_norm_backward(const NormArgs& a, int num_sms, cudaStream_t st);
 cudaError_t preload_norm_kernels();
+
+struct LayerNormArgs {
+    const void* x;         // forward: bf16 or fp32; backward: the normalised rows
+    const void* residual;  // bf16 or null
+    const void* dy;        // backward: bf16 or fp32
+    const void* dtotal;    // bf16 or null
+    int64_t ldx, ld_residual, ld_dy, ld_dtotal;
+    bool x_f32, dy_f32;
+    const void* gamma;
+    const void* beta;      // of gamma's type, or null
+    bool gamma_f32;
+    int64_t rows, cols;
+    float eps;
+    void* y;               // bf16
+    int64_t ldy;
+    void* total;           // bf16 or null
+    int64_t ld_total;
+    float* mean;           // forward: may be null
+    float* rstd;
+    void* dx;              // bf16
+    int64_t ld_dx;
+    float* dgamma;
+    float* dbeta;
+    float* partials;       // layer_norm_parts() x 2 cols
+};
+// Row groups whose dgamma and dbeta sums the backward pass writes apart.
+int layer_norm_parts(int64_t rows, int64_t cols, int num_sms);
+cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cudaStream_t st);
+cudaError_t preload_layer_norm_kernels();
+
+// E4M3 codes, and an fp32 scale for each block of 128 elements of a row or of
+// 128 x 128 (`square`).
+struct Fp8Operand {
+    uint8_t* codes;
+    float* scales;
+    int64_t codes_ld, scales_ld;
+};
+struct Fp8QuantArgs {
+    const void* x;  // bf16 or fp32
+    int64_t ld, rows, cols;
+    bool f32, square;
+    Fp8Operand row, col;  // codes null: not wanted
+};
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t st);
+cudaError_t preload_fp8_quantize_kernels();
+
+struct Fp8GemmArgs {
+    Fp8Operand a, b;  // M x K and N x K
+    bool a_square, b_square;
+    int64_t M, N, K;
+    void* d;          // bf16 or fp32
+    int64_t ldd;
+    bool d_f32, accumulate;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, int num_sms, cudaStream_t st);
+cudaError_t fp8_error_read_clear(int* value);
+// Polls of a stage's arrival before the product gives up, up to its default.
+cudaError_t set_fp8_wait_limit(uint32_t polls);
+cudaError_t preload_fp8_gemm_kernels();
 
 struct HeadArgs {
     const void* h;  // bf16 [T x K]

@@ -6,26 +6,12 @@
 #include <cuda_runtime.h>
 
 #include "../../include/ufp4.h"
+#include "api_checks.h"
 #include "train.h"
 
 using namespace ufp4;
 
 namespace {
-
-ufp4_status to_status(cudaError_t e) {
-    if (e == cudaSuccess) return UFP4_OK;
-    return e == cudaErrorNotSupported ? UFP4_ERR_UNSUPPORTED : UFP4_ERR_CUDA;
-}
-
-bool is_dtype(int32_t t) { return t == UFP4_BF16 || t == UFP4_F32; }
-int size_of(int32_t t) { return t == UFP4_F32 ? 4 : 2; }
-
-// A rows x cols matrix with leading dimension ld, elements of `bytes` bytes.
-ufp4_status check_matrix(const void* p, int64_t cols, int64_t ld, int bytes, bool optional) {
-    if (!p) return optional ? UFP4_OK : UFP4_ERR_INVALID_ARG;
-    if (ld < cols) return UFP4_ERR_INVALID_ARG;
-    return (uintptr_t)p % bytes ? UFP4_ERR_ALIGNMENT : UFP4_OK;
-}
 
 ufp4_status check_ckpt(const ufp4_qtensor* q, int64_t rows, int64_t cols, Ckpt* out) {
     if (!q->codes || !q->scales || q->rows != rows || q->cols != cols) return UFP4_ERR_INVALID_ARG;
@@ -34,15 +20,7 @@ ufp4_status check_ckpt(const ufp4_qtensor* q, int64_t rows, int64_t cols, Ckpt* 
     return UFP4_OK;
 }
 
-constexpr int64_t kMaxExtent = 1ll << 30;  // 32-bit column indices and tile counts
-
 }  // namespace
-
-#define UFP4_CHECK(expr)                          \
-    do {                                          \
-        const ufp4_status s_ = (expr);            \
-        if (s_ != UFP4_OK) return s_;             \
-    } while (0)
 
 extern "C" {
 
@@ -192,6 +170,98 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
     return to_status(launch_rms_norm_backward(a, sms, stream));
 }
 
+ufp4_status ufp4_layer_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* residual, int64_t ld_residual,
+                            const void* gamma, const void* beta, int32_t gamma_dtype, int64_t rows, int64_t cols, float eps,
+                            void* y, int64_t ldy, void* total, int64_t ld_total, float* mean, float* rstd,
+                            cudaStream_t stream) {
+    if (rows < 0 || cols < 1 || !is_dtype(x_dtype) || !is_dtype(gamma_dtype)) return UFP4_ERR_INVALID_ARG;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return UFP4_ERR_INVALID_ARG;
+    if (rows == 0) return UFP4_OK;
+    if (cols > kNormMaxCols) return UFP4_ERR_UNSUPPORTED;
+    UFP4_CHECK(check_matrix(x, cols, ldx, size_of(x_dtype), false));
+    UFP4_CHECK(check_matrix(residual, cols, ld_residual, 2, true));
+    UFP4_CHECK(check_matrix(gamma, cols, cols, size_of(gamma_dtype), false));
+    UFP4_CHECK(check_matrix(beta, cols, cols, size_of(gamma_dtype), true));
+    UFP4_CHECK(check_matrix(y, cols, ldy, 2, false));
+    UFP4_CHECK(check_matrix(total, cols, ld_total, 2, true));
+    UFP4_CHECK(check_matrix(mean, 1, 1, 4, true));
+    UFP4_CHECK(check_matrix(rstd, 1, 1, 4, true));
+    LayerNormArgs a = {};
+    a.x = x;
+    a.ldx = ldx;
+    a.x_f32 = x_dtype == UFP4_F32;
+    a.residual = residual;
+    a.ld_residual = ld_residual;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.gamma_f32 = gamma_dtype == UFP4_F32;
+    a.rows = rows;
+    a.cols = cols;
+    a.eps = eps;
+    a.y = y;
+    a.ldy = ldy;
+    a.total = total;
+    a.ld_total = ld_total;
+    a.mean = mean;
+    a.rstd = rstd;
+    return to_status(launch_layer_norm(a, current_num_sms(), stream));
+}
+
+static size_t layer_norm_bytes(int64_t rows, int64_t cols, int sms) {
+    return (size_t)layer_norm_parts(rows, cols, sms) * 2 * (size_t)cols * sizeof(float);
+}
+
+ufp4_status ufp4_layer_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+    if (rows < 0 || cols < 1 || !bytes) return UFP4_ERR_INVALID_ARG;
+    if (cols > kNormMaxCols) return UFP4_ERR_UNSUPPORTED;
+    *bytes = layer_norm_bytes(rows, cols, current_num_sms());
+    return UFP4_OK;
+}
+
+ufp4_status ufp4_layer_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dtype, const void* x, int64_t ldx,
+                                     int32_t x_dtype, const float* mean, const float* rstd, const void* gamma,
+                                     int32_t gamma_dtype, const void* dtotal, int64_t ld_dtotal, int64_t rows, int64_t cols,
+                                     void* dx, int64_t ld_dx, float* dgamma, float* dbeta, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
+    if (rows < 0 || cols < 1 || !is_dtype(dy_dtype) || !is_dtype(x_dtype) || !is_dtype(gamma_dtype))
+        return UFP4_ERR_INVALID_ARG;
+    if (cols > kNormMaxCols) return UFP4_ERR_UNSUPPORTED;
+    if (rows > 0) {
+        UFP4_CHECK(check_matrix(dy, cols, ld_dy, size_of(dy_dtype), false));
+        UFP4_CHECK(check_matrix(x, cols, ldx, size_of(x_dtype), false));
+        UFP4_CHECK(check_matrix(mean, 1, 1, 4, false));
+        UFP4_CHECK(check_matrix(rstd, 1, 1, 4, false));
+        UFP4_CHECK(check_matrix(gamma, cols, cols, size_of(gamma_dtype), false));
+        UFP4_CHECK(check_matrix(dtotal, cols, ld_dtotal, 2, true));
+        UFP4_CHECK(check_matrix(dx, cols, ld_dx, 2, false));
+    }
+    UFP4_CHECK(check_matrix(dgamma, cols, cols, 4, false));
+    UFP4_CHECK(check_matrix(dbeta, cols, cols, 4, false));
+    const int sms = current_num_sms();
+    UFP4_CHECK(check_workspace(workspace, workspace_bytes, layer_norm_bytes(rows, cols, sms)));
+    LayerNormArgs a = {};
+    a.dy = dy;
+    a.ld_dy = ld_dy;
+    a.dy_f32 = dy_dtype == UFP4_F32;
+    a.x = x;
+    a.ldx = ldx;
+    a.x_f32 = x_dtype == UFP4_F32;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.gamma = gamma;
+    a.gamma_f32 = gamma_dtype == UFP4_F32;
+    a.dtotal = dtotal;
+    a.ld_dtotal = ld_dtotal;
+    a.rows = rows;
+    a.cols = cols;
+    a.dx = dx;
+    a.ld_dx = ld_dx;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.partials = (float*)workspace;
+    return to_status(launch_layer_norm_backward(a, sms, stream));
+}
+
 // Whether the loss's extents and the tiles of its products (dH's up to 32 times, in shares) are 32-bit numbers.
 static bool head_fits(int64_t tokens, int64_t vocab, int64_t hidden) {
     if (tokens > kMaxExtent || vocab > kMaxExtent || hidden > kMaxExtent) return false;
@@ -207,11 +277,6 @@ static ufp4_status check_head(const void* h, int64_t ldh, const void* w, int64_t
     if ((uintptr_t)w % 16 || ldw % 8) return UFP4_ERR_ALIGNMENT;
     if (tokens && ((uintptr_t)h % 16 || ldh % 8 || (uintptr_t)targets % 8)) return UFP4_ERR_ALIGNMENT;
     return UFP4_OK;
-}
-
-static ufp4_status check_workspace(const void* workspace, size_t bytes, size_t need) {
-    if (!workspace || bytes < need) return UFP4_ERR_INVALID_ARG;
-    return (uintptr_t)workspace % 256 ? UFP4_ERR_ALIGNMENT : UFP4_OK;
 }
 
 static ufp4_status head_bytes(int64_t tokens, int64_t vocab, int64_t hidden,

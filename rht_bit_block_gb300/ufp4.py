@@ -28,6 +28,7 @@ BF16, F32 = 0, 1
 ACT_SILU, ACT_GELU = 0, 1
 ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 CKPT_BLOCK = 32  # elements of a row that share one checkpoint scale
+FP8_BLOCK = 128  # elements of a row (and rows, of a square block) that share one scale of an 8-bit operand
 
 # Every symbol include/ufp4.h declares (checked by the tests).
 EXPORTED = (
@@ -38,7 +39,8 @@ EXPORTED = (
     "ufp4_rht_quantize_batch", "ufp4_quant_error_stats", "ufp4_error_stats", "ufp4_set_quantize_wait_limit",
     "ufp4_rht_quantize_prepare", "ufp4_round_levels", "ufp4_glu", "ufp4_glu_backward", "ufp4_rms_norm",
     "ufp4_rms_norm_backward_workspace_size", "ufp4_rms_norm_backward", "ufp4_head_loss_workspace_size",
-    "ufp4_head_loss", "ufp4_head_loss_backward_workspace_size", "ufp4_head_loss_backward",
+    "ufp4_head_loss", "ufp4_head_loss_backward_workspace_size", "ufp4_head_loss_backward", "ufp4_layer_norm",
+    "ufp4_layer_norm_backward_workspace_size", "ufp4_layer_norm_backward", "ufp4_fp8_quantize", "ufp4_fp8_gemm",
 )
 MAX_BATCH = 4
 
@@ -112,7 +114,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ufp4_head_loss_backward_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(SZ)]
     L.ufp4_head_loss_backward.argtypes = [P, i64, P, i64, P, i64, i64, i64, f32, P, P, P, P, i64, i32, P, i64, i32, i32,
                                           P, SZ, P]
-    for name in ("ufp4_glu", "ufp4_glu_backward", "ufp4_rms_norm", "ufp4_rms_norm_backward_workspace_size",
+    L.ufp4_layer_norm.argtypes = [P, i64, i32, P, i64, P, P, i32, i64, i64, f32, P, i64, P, i64, P, P, P]
+    L.ufp4_layer_norm_backward_workspace_size.argtypes = [i64, i64, ctypes.POINTER(SZ)]
+    L.ufp4_layer_norm_backward.argtypes = [P, i64, i32, P, i64, i32, P, P, P, i32, P, i64, i64, i64, P, i64, P, P, P, SZ, P]
+    L.ufp4_fp8_quantize.argtypes = [P, i64, i32, i64, i64, i32, QT, QT, P]
+    L.ufp4_fp8_gemm.argtypes = [QT, i32, QT, i32, P, i64, i32, i32, P]
+    for name in ("ufp4_layer_norm", "ufp4_layer_norm_backward_workspace_size", "ufp4_layer_norm_backward",
+                 "ufp4_fp8_quantize", "ufp4_fp8_gemm", "ufp4_glu", "ufp4_glu_backward", "ufp4_rms_norm", "ufp4_rms_norm_backward_workspace_size",
                  "ufp4_rms_norm_backward", "ufp4_head_loss_workspace_size", "ufp4_head_loss",
                  "ufp4_head_loss_backward_workspace_size", "ufp4_head_loss_backward",
                  "ufp4_rht_quantize", "ufp4_rht_quantize_grouped", "ufp4_rht_transform", "ufp4_dequantize",
@@ -327,7 +335,7 @@ def ufp4_device_error_status() -> int:
 
 def ufp4_set_quantize_wait_limit(polls: int):
     """Failure-detection hook: polls of a tile barrier before the quantizer
-    kernels, or the vocabulary loss's products, give up (negative: the default)."""
+    kernels, the vocabulary loss's products, or ufp4_fp8_gemm, give up (negative: the default)."""
     _check(load().ufp4_set_quantize_wait_limit(polls), "ufp4_set_quantize_wait_limit")
 
 
@@ -518,7 +526,64 @@ def ufp4_head_loss_backward(h, w, targets, lse, dh, dw, workspace, token_weight=
     _check(load().ufp4_head_loss_backward(*args, _stream(stream)), "ufp4_head_loss_backward")
 
 
+def ufp4_layer_norm(x, gamma, y, mean=None, rstd=None, beta=None, residual=None, total=None, eps=1e-5, stream=None):
+    """y = layer norm of x + residual times gamma plus beta; mean, rstd and total (the bf16 sum) are written if given."""
+    shape = rows, cols = x.shape
+    dt = _dtype(gamma, "gamma")
+    args = (*_matrix(x, "x", shape), _dtype(x, "x"), *_matrix(residual, "residual", shape, BF16),
+            _vector(gamma, "gamma", cols, dt), _vector(beta, "beta", cols, dt), dt, rows, cols, eps,
+            *_matrix(y, "y", shape, BF16), *_matrix(total, "total", shape, BF16), _vector(mean, "mean", rows, F32),
+            _vector(rstd, "rstd", rows, F32))
+    _check_devices("ufp4_layer_norm", (x, gamma, y, mean, rstd, beta, residual, total))
+    _check(load().ufp4_layer_norm(*args, _stream(stream)), "ufp4_layer_norm")
+
+
+def ufp4_layer_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().ufp4_layer_norm_backward_workspace_size(rows, cols, ctypes.byref(out)),
+           "ufp4_layer_norm_backward_workspace_size")
+    return int(out.value)
+
+
+def ufp4_layer_norm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, workspace, dtotal=None, stream=None):
+    """dx, dgamma and dbeta of ufp4_layer_norm at the rows x (its x, or its total where there was a residual), dtotal
+    added to dx if given."""
+    shape = rows, cols = dy.shape
+    dt = _dtype(gamma, "gamma")
+    args = (*_matrix(dy, "dy", shape), _dtype(dy, "dy"), *_matrix(x, "x", shape), _dtype(x, "x"),
+            _vector(mean, "mean", rows, F32), _vector(rstd, "rstd", rows, F32), _vector(gamma, "gamma", cols, dt), dt,
+            *_matrix(dtotal, "dtotal", shape, BF16), rows, cols, *_matrix(dx, "dx", shape, BF16),
+            _vector(dgamma, "dgamma", cols, F32), _vector(dbeta, "dbeta", cols, F32), *_workspace(workspace))
+    _check_devices("ufp4_layer_norm_backward", (dy, x, mean, rstd, gamma, dx, dgamma, dbeta, workspace, dtotal))
+    _check(load().ufp4_layer_norm_backward(*args, _stream(stream)), "ufp4_layer_norm_backward")
+
+
+def ufp4_fp8_quantize(x, rowwise: QTensor | None, colwise: QTensor | None = None, block_rows=1, stream=None):
+    """E4M3 codes and fp32 scales of x (rowwise) and of its transpose (colwise), one scale for each 1 x 128 block
+    (block_rows 1) or 128 x 128 block (block_rows 128)."""
+    shape = rows, cols = x.shape
+    args = (*_matrix(x, "x", shape), _dtype(x, "x"), rows, cols, block_rows, rowwise, colwise)
+    _check_devices("ufp4_fp8_quantize", (x,), rowwise, colwise)
+    _check(load().ufp4_fp8_quantize(*args, _stream(stream)), "ufp4_fp8_quantize")
+
+
+def ufp4_fp8_gemm(A: QTensor, B: QTensor, D, a_block_rows=1, b_block_rows=128, accumulate=False, stream=None):
+    """D = A B^T of two operands of ufp4_fp8_quantize; added to D with accumulate (float32)."""
+    args = (A, a_block_rows, B, b_block_rows, *_matrix(D, "D", (A.rows, B.rows)), _dtype(D, "D"), int(accumulate))
+    _check_devices("ufp4_fp8_gemm", (D,), A, B)
+    _check(load().ufp4_fp8_gemm(*args, _stream(stream)), "ufp4_fp8_gemm")
+
+
 # ------------------------------------------------------------- conveniences
+def alloc_fp8(rows: int, cols: int, block_rows: int, device):
+    """torch buffers (codes, scales) of one 8-bit operand; describe them with qtensor(codes, scales, rows, cols)."""
+    import torch
+    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
+    scales = torch.empty(((rows + block_rows - 1) // block_rows, (cols + FP8_BLOCK - 1) // FP8_BLOCK), dtype=torch.float32,
+                         device=device)
+    return codes, scales
+
+
 def alloc_checkpoint(rows: int, cols: int, device):
     """torch buffers (codes, scales) of one 8-bit checkpoint; describe them with qtensor(codes, scales, rows, cols)."""
     import torch
