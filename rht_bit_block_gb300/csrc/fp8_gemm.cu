@@ -7,25 +7,30 @@
 // An fp32 scale cannot ride in a block-scaled MMA, whose scales are powers of
 // two (or E4M3).  So the tensor core sums one block of 128 at a time, in fp32,
 // into one of two buffers in tensor memory, and while it sums the next one into
-// the other, sixteen warps read the finished block and add it, scaled, to fp32
-// sums in registers.  That costs a multiply-add for each element and block, and
-// a second multiplication where both operands have a scale a row (WGRAD): on a
-// 256 x 256 tile of a CTA pair a block is 512 cycles of the tensor core and 256
-// of an SM's fp32 lanes (512 with both).
+// the other, other warps read the finished block and add it, scaled, to fp32 sums
+// in registers.
 //
-// Orientation.  The rows of B (a layer's outputs) lie along the lanes of tensor
-// memory, the rows of A (tokens) along its columns, so the tile is D^T: a warp
-// that writes a token's results writes 32 neighbouring ones, and what a token
-// count gives, from 1 to thousands, is the width of the tile.  A square block of
-// B has one scale for all 128 lanes of a tile's row block: it is multiplied into the
-// tokens' scales as they are laid out in shared memory, once a block and column.
+// One operand's rows (P) lie along the lanes of tensor memory, the other's (Q)
+// along its columns; three shapes:
 //
-// Two shapes.  Pairs: persistent CTA pairs, 256 x 256 tiles, tcgen05.mma
-// .cta_group::2; a pair holds 128 rows of B and half the tokens per CTA.  Shares:
-// a single CTA's tile is 128 rows of B by 16 to 128 tokens, and the summed index
-// is shared out over a cluster of up to eight CTAs, which add their sums through
-// distributed shared memory, in the order of their ranks: no workspace, no
-// atomics, and the same bits every time.
+// Pairs and singles (WIDE): P is A, Q is B.  Pairs are persistent CTA pairs with
+// 256 x 256 tiles, tcgen05.mma .cta_group::2, where a CTA holds 128 rows of either
+// operand; singles are 128 x 128 tiles of one CTA, for products with too few of
+// the large ones.  A block of a pair's tile is 512 cycles of the tensor core, and
+// 256 of an SM's fp32 lanes for one multiply-add an element.  What would not fit
+// is to bring every thread a scale for every column: 128 lanes x 256 columns from
+// shared memory are 1024 cycles.  So the sums are read in the layout that gives
+// a thread four rows and a quarter of the columns (16 x 256 bits), and where B has
+// square blocks one scale a row and 128 columns is all that it needs; with scales
+// for either's rows (WGRAD) a column pair's are read once for four rows.
+//
+// Few tokens (up to 64): P is B, Q is A, so that the tile is as wide as there
+// are tokens and the weights are read once.  A lane holds a row of B, and 32
+// neighbouring results of a token are one store of a warp.
+//
+// Singles and few tokens share the summed index out over a cluster of up to eight
+// CTAs, which add their sums through distributed shared memory, in the order of
+// their ranks: no workspace, no atomics, and the same bits every time.
 #include <algorithm>
 #include <atomic>
 #include <cuda.h>
@@ -43,36 +48,38 @@ __device__ int g_fp8_error;
 
 namespace {
 
-constexpr int kLanes = 128;                // rows of B that one CTA holds: the lanes of tensor memory
+constexpr int kLanes = 128;                // rows of P that one CTA holds: the lanes of tensor memory
 constexpr int kStep = 128;                 // summed elements (and bytes) of a block: one 128-byte swizzle row
 constexpr int kAtom = kLanes * kStep;
 constexpr int kSlab = 4;                   // blocks whose scales are laid out at a time
-constexpr int kSlabs = 3;
+constexpr int kSlabs = 2;
 constexpr int kPad = 8;                    // floats between a slab's blocks, off the same bank
 constexpr int kLoaders = 64;               // threads that lay out scales (warps 2 and 3)
 constexpr int kOthers = 128;               // threads of warps 0 to 3
 constexpr int kMaxShares = 8;
+constexpr int kGroup = 8;                  // tiles of P that advance before the tile of Q does
 constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sleep up to kSuspendNs
 constexpr uint32_t kSuspendNs = 1000;
 constexpr uint32_t kLook = 1024;           // polls between looks at the abort flag
 constexpr uint32_t kDrainLimit = 1u << 16; // polls for copies in flight, after a wait has given up
 
-// CW columns a warp, GROUPS warps of each lane quadrant: tiles of CW * GROUPS tokens.
-template <bool PAIR, int CW, int GROUPS>
+// CW columns a warp, GROUPS warps of each lane quadrant.
+template <bool WIDE, bool PAIR, int CW, int GROUPS>
 struct Cfg {
-    static constexpr int kCols = CW * GROUPS;
+    static constexpr int kCols = CW * GROUPS;                 // columns of a tile
+    static constexpr int kRows = PAIR ? 2 * kLanes : kLanes;  // rows of a tile
     static constexpr int kThreads = kOthers + 128 * GROUPS;
-    static constexpr int kRows = PAIR ? 2 * kLanes : kLanes;         // rows of B of a tile
-    static constexpr int kQRows = PAIR ? kCols / 2 : kCols;          // tokens that a CTA holds
+    static constexpr bool kSplit = CW == 128;                 // registers go from warps 0 to 3 to the others
+    static constexpr int kQRows = PAIR ? kCols / 2 : kCols;   // rows of Q that a CTA holds
     static constexpr int kQ = kQRows * kStep;
     static constexpr int kStage = kAtom + kQ;
-    static constexpr int kStages = PAIR ? 6 : (kCols <= 32 ? 5 : (kCols <= 64 ? 4 : 6));
+    static constexpr int kStages = WIDE ? 6 : (kCols <= 32 ? 5 : 4);
     static constexpr int kColPitch = kCols + kPad, kRowPitch = kLanes + kPad;
     static constexpr int kSlabFloats = kSlab * (kColPitch + kRowPitch);
     static constexpr int kOffScales = kStages * kStage;
     static constexpr int kOffBars = kOffScales + kSlabs * kSlabFloats * 4;
-    // full, empty; partial sums full x2, empty x2; slabs full, empty; drain
-    static constexpr int kNumBars = 2 * kStages + 4 + 2 * kSlabs + 1;
+    // full, done; partial sums read x2; slabs full, empty; drain
+    static constexpr int kNumBars = 2 * kStages + 2 + 2 * kSlabs + 1;
     static constexpr int kOffWords = kOffBars + 8 * kNumBars;  // tensor memory address, abort flag, stages filled and used
     static constexpr int kSmem = kOffWords + 16 + 1024;
     static constexpr int kTmem = 2 * kCols;
@@ -80,6 +87,7 @@ struct Cfg {
     static_assert(kSmem <= 232448, "shared memory overflow");
     static_assert(kCols * kLanes * 4 <= kStages * kStage, "a share's sums take the stages' place");
     static_assert(kQRows % 8 == 0 && kQ % 1024 == 0, "swizzle atoms");
+    static_assert(!WIDE || CW % 64 == 0, "a wide tile's columns are read 64 at a time");
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -94,18 +102,37 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+}
+__device__ __forceinline__ int ld_shared(uint32_t saddr) {
+    int v;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(saddr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_shared_f(uint32_t saddr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(saddr));
+    return v;
+}
+// Two pairs of floats, 16-byte aligned.
+__device__ __forceinline__ void ld_shared_pairs(uint32_t saddr, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(saddr));
+}
+__device__ __forceinline__ uint64_t ld_shared_pair(uint32_t saddr) {
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(saddr));
+    return v;
 }
 // Bounded wait on an mbarrier phase; false at the limit (with the error word
-// set), or once `abort` is set, which is looked at every kLook polls.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int* abort,
-                                          uint32_t limit = kWaitLimit) {
+// set), or once the word at `abort` (0: none) is set, which is looked at every
+// kLook polls.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit = kWaitLimit) {
     for (uint32_t left = limit; left;) {
         const uint32_t n = min(left, kLook);
         for (uint32_t i = 0; i < n; ++i) {
             uint32_t ok;
             asm volatile(
-                "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;"
+                "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;"
                 " selp.u32 %0, 1, 0, p; }"
                 : "=r"(ok)
                 : "r"(bar), "r"(parity), "r"(kSuspendNs)
@@ -113,7 +140,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const v
             if (ok) return true;
         }
         left -= n;
-        if (abort && *abort) return false;
+        if (abort && ld_shared(abort)) return false;
     }
     atomicExch(&g_fp8_error, 1);
     return false;
@@ -216,7 +243,7 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, int cols) {
     else
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
 }
-// 16 or 32 columns of a warp's 32 lanes.
+// 16 or 32 columns of a warp's 32 lanes, a lane a row ...
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[32]) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
     asm volatile(
@@ -228,7 +255,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[32]) {
           "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]),
           "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
         : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[16]) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
@@ -238,37 +264,63 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[16]) {
           "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]),
           "=r"(u[15])
         : "r"(taddr));
+}
+// ... or 64 columns of 16 lanes: r[4 j + e] is row lane / 4, r[4 j + 2 + e] row lane / 4 + 8, column 8 j + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&r)[32]) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]),
+          "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]),
+          "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]),
+          "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(taddr));
+}
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
+}
+// Waits for all of this warp's reads; `r` are what one of them brings (they are
+// not to be used before).
+template <int N>
+__device__ __forceinline__ void tmem_wait(float (&r)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
 }
 
 // ------------------------------------------------------------------- kernel
 struct Fp8Params {
-    int M, N;
-    int blocks;             // of the summed index
-    int m_tiles, n_tiles;   // of tokens, of rows of B
-    int group;              // tile order: rows of B that advance first
-    int shares, per;        // CTAs of a cluster and blocks of each (single CTAs)
-    int a_rows;             // tokens that a copy brings: up to a tile's
-    uint32_t wait_limit;    // polls of a stage's arrival; all other waits keep kWaitLimit
-    const float* sa;
-    const float* sb;
-    int64_t ld_sa, ld_sb;
-    int a_shift, b_shift;   // log2 of the rows that share a scale: 0 or 7
+    int p_rows, q_rows;        // extents of the operands
+    int blocks;                // of the summed index
+    int p_tiles, q_tiles;
+    int group;                 // tile order: tiles of P that advance first
+    int shares, per;           // CTAs of a cluster and blocks of each (one for pairs)
+    int q_box;                 // rows of Q that a copy brings: up to a CTA's
+    uint32_t wait_limit;       // polls of a stage's arrival; all other waits keep kWaitLimit
+    const float* sp;
+    const float* sq;
+    int64_t ld_sp, ld_sq;
+    int p_shift, q_shift;      // log2 of the rows that share a scale: 0 or 7
     void* d;
     int64_t ldd;
     int d_f32, accumulate;
+    int d_vec;                 // bytes that neighbouring results can be stored by: 16 or their own
 };
 
-__device__ __forceinline__ void tile_at(const Fp8Params& p, int tile, int& mt, int& nt) {
-    const int group = min(p.group, p.n_tiles);
-    const int span = group * p.m_tiles, g = tile / span, first = g * group;
-    const int rows = min(group, p.n_tiles - first), l = tile - g * span;
-    mt = l / rows;
-    nt = first + (l - mt * rows);
+__device__ __forceinline__ void tile_at(const Fp8Params& p, int tile, int& pt, int& qt) {
+    const int group = min(p.group, p.p_tiles);
+    const int span = group * p.q_tiles, g = tile / span, first = g * group;
+    const int rows = min(group, p.p_tiles - first), l = tile - g * span;
+    qt = l / rows;
+    pt = first + (l - qt * rows);
 }
 
-__device__ __forceinline__ void put(const Fp8Params& p, int m, int n, float v) {
-    const int64_t at = (int64_t)m * p.ldd + n;
+__device__ __forceinline__ void put(const Fp8Params& p, int64_t at, float v) {
     if (p.d_f32) {
         float* d = (float*)p.d + at;
         *d = p.accumulate ? *d + v : v;
@@ -276,21 +328,85 @@ __device__ __forceinline__ void put(const Fp8Params& p, int m, int n, float v) {
         ((__nv_bfloat16*)p.d)[at] = __float2bfloat16_rn(v);
     }
 }
-
 __device__ __forceinline__ float column(const uint64_t* acc, int c) {
     float x, y;
     up2(acc[c >> 1], x, y);
     return c & 1 ? y : x;
 }
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+    float x, y;
+    up2(v, x, y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A wide tile's sums of a warp (rows row0 + 8 i, i = 0..3, of the lane's quad; pairs of columns 8 j + 2 (lane % 4), j = 0 ..
+// CW / 8 - 1, acc[i * CW / 8 + j]) into D.  bf16: four lanes turn four groups of 8 columns around, so that each stores 16
+// bytes, 64 of a row in a piece; fp32 pairs fill whole sectors as they are.
+template <int CW>
+__device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&acc)[CW / 2], int row0, int col0) {
+    const int q = threadIdx.x & 3;
+    const bool whole = col0 + CW <= p.q_rows && p.d_vec == 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = row0 + 8 * i;
+        const bool live = row < p.p_rows;
+        const int64_t at = (int64_t)row * p.ldd + col0;
+        const uint64_t* a = acc + i * (CW / 8);
+        if (whole && !p.d_f32) {
+#pragma unroll
+            for (int j = 0; j < CW / 8; j += 4) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = pack_bf16(a[j + k]);
+                // lane q ends with what the quad's lanes hold of group j + q
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const uint32_t give = q & 1 ? v[k] : v[k + 1];
+                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+                    if (q & 1) v[k] = got;
+                    else v[k + 1] = got;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t give = q & 2 ? v[k] : v[k + 2];
+                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 2);
+                    if (q & 2) v[k] = got;
+                    else v[k + 2] = got;
+                }
+                if (live) *reinterpret_cast<uint4*>((__nv_bfloat16*)p.d + at + 8 * (j + q)) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        } else if (live) {
+#pragma unroll
+            for (int j = 0; j < CW / 8; ++j) {
+                const int c = 8 * j + 2 * q;
+                float x, y;
+                up2(a[j], x, y);
+                if (whole) {
+                    float2* d = reinterpret_cast<float2*>((float*)p.d + at + c);
+                    if (p.accumulate) {
+                        const float2 o = *d;
+                        x = o.x + x;
+                        y = o.y + y;
+                    }
+                    *d = make_float2(x, y);
+                } else {
+                    if (col0 + c < p.q_rows) put(p, at + c, x);
+                    if (col0 + c + 1 < p.q_rows) put(p, at + c + 1, y);
+                }
+            }
+        }
+    }
+}
 
 // Warp 0 copies the operands (one thread), warp 1 of the leader issues the
 // MMAs, warps 2 and 3 lay out the scales, the rest scale and add.  BOTH: the
-// rows of B have scales of their own; otherwise a tile's 128 share one.
-template <bool PAIR, bool BOTH, int CW, int GROUPS>
-__global__ void __launch_bounds__((Cfg<PAIR, CW, GROUPS>::kThreads), 1)
-fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+// rows of either operand have scales of their own; otherwise 128 rows of B share one.
+template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
+__global__ void __launch_bounds__((Cfg<WIDE, PAIR, CW, GROUPS>::kThreads), 1)
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                 const __grid_constant__ Fp8Params p) {
-    using C = Cfg<PAIR, CW, GROUPS>;
+    using C = Cfg<WIDE, PAIR, CW, GROUPS>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -298,17 +414,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     uint8_t* gbase = smem_raw + (base - raw);
     const uint32_t bars = base + C::kOffBars;
     auto full_bar = [&](int s) { return bars + 8u * s; };
-    auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
-    auto sumf_bar = [&](int b) { return bars + 8u * (2 * S + b); };
-    auto sume_bar = [&](int b) { return bars + 8u * (2 * S + 2 + b); };
-    auto slabf_bar = [&](int i) { return bars + 8u * (2 * S + 4 + i); };
-    auto slabe_bar = [&](int i) { return bars + 8u * (2 * S + 4 + kSlabs + i); };
-    const uint32_t drain_bar = bars + 8u * (2 * S + 4 + 2 * kSlabs);
+    auto done_bar = [&](int s) { return bars + 8u * (S + s); };
+    auto read_bar = [&](int b) { return bars + 8u * (2 * S + b); };
+    auto slabf_bar = [&](int i) { return bars + 8u * (2 * S + 2 + i); };
+    auto slabe_bar = [&](int i) { return bars + 8u * (2 * S + 2 + kSlabs + i); };
+    const uint32_t drain_bar = bars + 8u * (2 * S + 2 + 2 * kSlabs);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffWords);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffWords + 4);
+    const uint32_t abort_flag = base + C::kOffWords + 4;
     volatile int* stages_of = reinterpret_cast<volatile int*>(gbase + C::kOffWords + 8);  // filled, used
-    auto slab_cols = [&](int i) { return reinterpret_cast<float*>(gbase + C::kOffScales) + i * C::kSlabFloats; };
-    auto slab_rows = [&](int i) { return slab_cols(i) + kSlab * C::kColPitch; };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -316,26 +429,23 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     const int peer = PAIR ? (int)rank : 0;  // 0: the CTA that issues the MMAs
     const int cluster_id = PAIR ? blockIdx.x >> 1 : blockIdx.x / p.shares;
     const int num_clusters = PAIR ? gridDim.x >> 1 : gridDim.x / p.shares;
-    const int num_tiles = p.m_tiles * p.n_tiles;
+    const int num_tiles = p.p_tiles * p.q_tiles;
     // this CTA's share of the summed index
     const int k0 = PAIR ? 0 : (int)rank * p.per;
     const int k_blocks = PAIR ? p.blocks : max(0, min(p.per, p.blocks - k0));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1);   // the leader's expect_tx arrival (both CTAs' bytes)
-            mbar_init(empty_bar(s), 1);  // the leader's commit
+            mbar_init(full_bar(s), 1);  // the leader's expect_tx arrival (both CTAs' bytes)
+            mbar_init(done_bar(s), 1);  // the leader's commit: the stage may be filled, its sums be read
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(sumf_bar(b), 1);                              // the leader's commit
-            mbar_init(sume_bar(b), (PAIR ? 2 : 1) * 4 * GROUPS);    // every scaling warp
-        }
+        for (int b = 0; b < 2; ++b) mbar_init(read_bar(b), (PAIR ? 2 : 1) * 4 * GROUPS);  // every scaling warp
         for (int i = 0; i < kSlabs; ++i) {
             mbar_init(slabf_bar(i), kLoaders);
             mbar_init(slabe_bar(i), 4 * GROUPS);
         }
         mbar_init(drain_bar, 1);
-        *abort_flag = 0;
+        *reinterpret_cast<volatile int*>(gbase + C::kOffWords + 4) = 0;
         stages_of[0] = stages_of[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -350,191 +460,236 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 
     // Sets the abort flag of this CTA, and of its pair.
     auto give_up = [&] {
-        *abort_flag = 1;
-        if (PAIR) st_cluster(map_to_rank(base + C::kOffWords + 4, rank ^ 1u), 1);
+        *reinterpret_cast<volatile int*>(gbase + C::kOffWords + 4) = 1;
+        if (PAIR) st_cluster(map_to_rank(abort_flag, rank ^ 1u), 1);
     };
 
-    if (warp == 0 && lane == 0) {
-        // ---------------------------------------------------- TMA copies
-        int s = 0, stages = 0;
-        uint32_t ph = 0;
-        const uint32_t tx = PAIR ? 2 * C::kStage : kAtom + (uint32_t)p.a_rows * kStep;
-        for (int tile = cluster_id; tile < num_tiles && !*abort_flag; tile += num_clusters) {
-            int mt, nt;
-            tile_at(p, tile, mt, nt);
-            const int brow = nt * C::kRows + peer * kLanes, arow = mt * C::kCols + peer * C::kQRows;
-            for (int kb = 0; kb < k_blocks; ++kb) {
-                if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) {
-                    give_up();
-                    break;
-                }
-                ++stages;
-                const uint32_t fb = PAIR ? map_to_rank(full_bar(s), 0) : full_bar(s);
-                if (peer == 0) mbar_expect_tx(full_bar(s), tx);
-                const uint32_t dst = base + s * C::kStage;
-                tma_load<PAIR>(dst, &map_b, (k0 + kb) * kStep, brow, fb);
-                tma_load<PAIR>(dst + kAtom, &map_a, (k0 + kb) * kStep, arow, fb);
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-            }
-        }
-        stages_of[0] = stages;
-    } else if (warp == 1 && lane == 0 && peer == 0) {
-        // ------------------------------------------------ MMA issuer (leader only)
-        constexpr uint32_t idesc = make_idesc(C::kRows, C::kCols);
-        int s = 0, stages = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
-        bool ok = true;
-        for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
-            for (int kb = 0; kb < k_blocks; ++kb) {
-                if (!mbar_wait(full_bar(s), ph, nullptr, p.wait_limit) || !mbar_wait(sume_bar(buf), bph ^ 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                ++stages;
-                tc_fence_after();
-                const uint64_t db = sw128_desc(base + s * C::kStage), da = sw128_desc(base + s * C::kStage + kAtom);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)  // 32 bytes of the summed index each
-                    mma<PAIR>(tmem + buf * C::kCols, db + 2 * i, da + 2 * i, idesc, i > 0 ? 1u : 0u);
-                tc_commit<PAIR>(empty_bar(s));
-                tc_commit<PAIR>(sumf_bar(buf));
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-                if (++buf == 2) {
-                    buf = 0;
-                    bph ^= 1u;
-                }
-            }
-        }
-        if (!ok) give_up();
-        stages_of[1] = stages;
-        tc_commit_local<PAIR>(drain_bar);
-        mbar_wait(drain_bar, 0, nullptr);
-    } else if (warp == 2 || warp == 3) {
-        // ------------------------------------------------ scales
-        const int tid = threadIdx.x - 64;
-        const int kk = tid & (kSlab - 1);
-        int i = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
-            int mt, nt;
-            tile_at(p, tile, mt, nt);
-            const int m0 = mt * C::kCols, n0 = nt * C::kRows + peer * kLanes;
-            for (int kb = 0; kb < k_blocks; kb += kSlab) {
-                if (!mbar_wait(slabe_bar(i), ph ^ 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                // this thread's block of the slab, of every 16th column or row
-                const bool live = kb + kk < k_blocks;
-                const int64_t b = k0 + kb + kk;
-                const float* sa = p.sa + b;
-                float common = 1.0f;
-                if (!BOTH) common = live && n0 < p.N ? p.sb[(int64_t)(n0 >> p.b_shift) * p.ld_sb + b] : 0.0f;
-                float* cols = slab_cols(i) + kk * C::kColPitch;
-                constexpr int kEach = C::kCols * kSlab / kLoaders, kTurn = kEach < 8 ? kEach : 8;  // loads in flight
-#pragma unroll 1
-                for (int j0 = 0; j0 < kEach; j0 += kTurn) {
-                    float v[kTurn];
-                    const int q = (tid >> 2) + 16 * j0;
-#pragma unroll
-                    for (int j = 0; j < kTurn; ++j) {
-                        const int m = m0 + q + 16 * j;
-                        v[j] = live && m < p.M ? sa[(int64_t)(m >> p.a_shift) * p.ld_sa] : 0.0f;
+    // With kSplit, what the threads of warps 0 to 3 give up of the launch's 168 registers, twice as many others take:
+    // 128 x 72 + 256 x 216 = 384 x 168.
+    if (warp < 4) {
+        if (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // The copier and the issuer are whole warps, of which one lane acts: what a lane alone computes has to be moved to
+        // the uniform registers of its copies and MMAs each time (a step of the issuer took 1000 cycles).
+        if (warp == 0) {
+            // ---------------------------------------------------- TMA copies
+            const bool acts = elect_one();
+            int s = 0, stages = 0;
+            uint32_t ph = 0;
+            const uint32_t tx = PAIR ? 2 * C::kStage : kAtom + (uint32_t)p.q_box * kStep;
+            const uint32_t remote = PAIR ? map_to_rank(bars, 0) : bars;
+            bool ok = true;
+            for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
+                int pt, qt;
+                tile_at(p, tile, pt, qt);
+                const int prow = pt * C::kRows + peer * kLanes, qrow = qt * C::kCols + peer * C::kQRows;
+                for (int kb = 0; kb < k_blocks; ++kb) {
+                    ok = mbar_wait(done_bar(s), ph ^ 1u, abort_flag);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
                     }
-#pragma unroll
-                    for (int j = 0; j < kTurn; ++j) cols[q + 16 * j] = BOTH ? v[j] : v[j] * common;
-                }
-                if (BOTH) {
-                    float* rows = slab_rows(i) + kk * C::kRowPitch;
-                    float w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int n = n0 + (tid >> 2) + 16 * j;
-                        w[j] = live && n < p.N ? p.sb[(int64_t)(n >> p.b_shift) * p.ld_sb + b] : 0.0f;
+                    ++stages;
+                    if (acts) {
+                        if (peer == 0) mbar_expect_tx(full_bar(s), tx);
+                        const uint32_t dst = base + s * C::kStage;
+                        tma_load<PAIR>(dst, &map_p, (k0 + kb) * kStep, prow, remote + 8u * s);
+                        tma_load<PAIR>(dst + kAtom, &map_q, (k0 + kb) * kStep, qrow, remote + 8u * s);
                     }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) rows[(tid >> 2) + 16 * j] = w[j];
-                }
-                mbar_arrive(slabf_bar(i));
-                if (++i == kSlabs) {
-                    i = 0;
-                    ph ^= 1u;
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
+            if (!ok) give_up();
+            if (lane == 0) stages_of[0] = stages;
+        } else if (warp == 1 && peer == 0) {
+            // ------------------------------------------------ MMA issuer (leader only)
+            const bool acts = elect_one();
+            constexpr uint32_t idesc = make_idesc(C::kRows, C::kCols);
+            int s = 0, stages = 0;
+            uint32_t ph = 0, t = 0;  // t: blocks so far, buffer t & 1
+            bool ok = true;
+            for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
+                for (int kb = 0; kb < k_blocks; ++kb) {
+                    ok = mbar_wait(full_bar(s), ph, 0, p.wait_limit) && mbar_wait(read_bar(t & 1), (t >> 1 & 1) ^ 1u, abort_flag);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    ++stages;
+                    tc_fence_after();
+                    if (acts) {
+                        const uint64_t dp = sw128_desc(base + s * C::kStage), dq = sw128_desc(base + s * C::kStage + kAtom);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)  // 32 bytes of the summed index each
+                            mma<PAIR>(tmem + (t & 1) * C::kCols, dp + 2 * i, dq + 2 * i, idesc, i > 0 ? 1u : 0u);
+                        tc_commit<PAIR>(done_bar(s));
+                    }
+                    ++t;
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) give_up();
+            if (lane == 0) stages_of[1] = stages;
+            __syncwarp();
+            if (acts) tc_commit_local<PAIR>(drain_bar);
+            mbar_wait(drain_bar, 0, 0);
+        } else if (warp >= 2) {
+            // ------------------------------------------------ scales
+            // A slab is the scales of up to kSlab blocks: those of the tile's columns and of the CTA's rows, each block's apart.
+            // A thread takes one block, and every 16th column or row.  What lies past the operands is read at their edge
+            // instead; nothing looks at it.
+            const int tid = threadIdx.x - 64;
+            const int kk = tid & (kSlab - 1), each = tid >> 2;
+            constexpr bool kOfCols = !WIDE || BOTH;  // every column its scale; otherwise one for each 128
+            constexpr bool kOfRows = WIDE || BOTH;   // every row its scale; otherwise in the columns'
+            int i = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
+                int pt, qt;
+                tile_at(p, tile, pt, qt);
+                const int p0 = pt * C::kRows + peer * kLanes, q0 = qt * C::kCols;
+                for (int kb = 0; kb < k_blocks; kb += kSlab) {
+                    const int64_t b = min(k0 + kb + kk, p.blocks - 1);
+                    const float* sp = p.sp + b;
+                    const float* sq = p.sq + b;
+                    auto of_p = [&](int r) { return sp[(int64_t)(min(p0 + r, p.p_rows - 1) >> p.p_shift) * p.ld_sp]; };
+                    auto of_q = [&](int r) { return sq[(int64_t)(min(q0 + r, p.q_rows - 1) >> p.q_shift) * p.ld_sq]; };
+                    constexpr int kC = kOfCols ? C::kCols / 16 : 1, kR = kOfRows ? kLanes / 16 : 1;
+                    float v[kC], w[kR];
+#pragma unroll
+                    for (int j = 0; j < kC; ++j) v[j] = of_q(kOfCols ? each + 16 * j : min(each * 128, C::kCols - 1));
+#pragma unroll
+                    for (int j = 0; j < kR; ++j) w[j] = of_p(kOfRows ? each + 16 * j : 0);
+                    if (!mbar_wait(slabe_bar(i), ph ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    float* cols = reinterpret_cast<float*>(gbase + C::kOffScales) + i * C::kSlabFloats + kk * C::kColPitch;
+                    float* rows = reinterpret_cast<float*>(gbase + C::kOffScales) + i * C::kSlabFloats + kSlab * C::kColPitch +
+                                  kk * C::kRowPitch;
+#pragma unroll
+                    for (int j = 0; j < kC; ++j) cols[each + 16 * j] = kOfRows ? v[j] : v[j] * w[0];
+                    if (kOfRows) {
+#pragma unroll
+                        for (int j = 0; j < kR; ++j) rows[each + 16 * j] = w[j];
+                    }
+                    mbar_arrive(slabf_bar(i));
+                    i ^= 1;
+                    ph ^= i == 0;
+                }
+            }
+            if (!ok) give_up();
         }
-        if (!ok) give_up();
-    } else if (warp >= 4) {
+    } else {
         // ------------------------------------------------- scaling and adding
-        constexpr int kChunk = PAIR || CW < 32 ? 16 : 32;
+        if (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int quad = warp & 3, first = ((warp - 4) >> 2) * CW;
-        const int row = quad * 32 + lane;  // of the CTA's 128
-        int buf = 0, i = 0;
-        uint32_t bph = 0, ph = 0;
+        const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + first;
+        const uint32_t scales = base + C::kOffScales;
+        uint32_t t = 0, u = 0;  // blocks and slabs so far: buffer t & 1, slab u & 1
+        int s = 0;              // stage of block t
+        uint32_t ph = 0;
         bool ok = true;
-        uint64_t acc[CW / 2];
+        uint64_t acc[CW / 2];  // pairs of columns; WIDE: see store_wide
         for (int tile = cluster_id; tile < num_tiles; tile += num_clusters) {
 #pragma unroll
             for (int c = 0; c < CW / 2; ++c) acc[c] = 0;
             for (int kb = 0; kb < k_blocks; ++kb) {
                 const int kk = kb & (kSlab - 1);
-                if (kk == 0) ok = mbar_wait(slabf_bar(i), ph, abort_flag);
-                ok = ok && mbar_wait(sumf_bar(buf), bph, abort_flag);
+                if (kk == 0) ok = mbar_wait(slabf_bar(u & 1), (u >> 1) & 1, abort_flag);
+                const uint32_t cols = scales + ((u & 1) * C::kSlabFloats + kk * C::kColPitch) * 4;
+                const uint32_t rows = scales + ((u & 1) * C::kSlabFloats + kSlab * C::kColPitch + kk * C::kRowPitch) * 4;
+                uint64_t rs[WIDE ? 4 : 1];  // of the lane's rows, times the columns' where they share one
+                if constexpr (WIDE) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v = ld_shared_f(rows + (quad * 32 + 8 * i + (lane >> 2)) * 4);
+                        if (!BOTH) v *= ld_shared_f(cols + (first >> 7) * 4);
+                        rs[i] = pk2(v, v);
+                    }
+                } else {
+                    const float v = BOTH ? ld_shared_f(rows + (quad * 32 + lane) * 4) : 1.0f;
+                    rs[0] = pk2(v, v);
+                }
+                ok = ok && mbar_wait(done_bar(s), ph, abort_flag);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float* cols = slab_cols(i) + kk * C::kColPitch + first;
-                uint64_t rs2 = 0;
-                if (BOTH) {
-                    const float rs = slab_rows(i)[kk * C::kRowPitch + row];
-                    rs2 = pk2(rs, rs);
-                }
-                const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + buf * C::kCols + first;
+                const uint32_t at = from + (t & 1) * C::kCols;
+                auto release = [&] {  // the buffer has been read and may be filled again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(map_to_rank(read_bar(t & 1), 0));
+                        else mbar_arrive(read_bar(t & 1));
+                    }
+                };
+                if constexpr (WIDE) {
+                    // 64 columns of 16 rows at a time
+                    constexpr int kChunks = CW / 32;
+                    float r[2][32];
+                    tmem_ld_rows(at, r[0]);
 #pragma unroll
-                for (int c = 0; c < CW; c += kChunk) {
-                    float r[kChunk];
-                    tmem_ld(at + c, r);
-                    if (c + kChunk == CW) {  // read: the buffer may be filled again
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (PAIR) mbar_arrive_cluster(map_to_rank(sume_bar(buf), 0));
-                            else mbar_arrive(sume_bar(buf));
+                    for (int c = 0; c < kChunks; ++c) {
+                        const int half = c & 1, col = (c >> 1) * 64;
+                        tmem_wait(r[c & 1]);
+                        if (c + 1 < kChunks)  // on its way while this one is added
+                            tmem_ld_rows(at + ((c + 1) >> 1) * 64 + ((uint32_t)((c + 1) & 1) << 20), r[(c + 1) & 1]);
+                        else
+                            release();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float* v = r[c & 1] + 4 * j;
+                            uint64_t x = pk2(v[0], v[1]), y = pk2(v[2], v[3]);
+                            if (BOTH) {
+                                const uint64_t w = ld_shared_pair(cols + (first + col + 8 * j + 2 * (lane & 3)) * 4);
+                                x = mul2(x, w);
+                                y = mul2(y, w);
+                            }
+                            uint64_t& ax = acc[(2 * half) * (CW / 8) + col / 8 + j];
+                            uint64_t& ay = acc[(2 * half + 1) * (CW / 8) + col / 8 + j];
+                            ax = fma2(x, rs[2 * half], ax);
+                            ay = fma2(y, rs[2 * half + 1], ay);
                         }
                     }
+                } else {
+                    constexpr int kChunk = CW < 32 ? CW : 32, kChunks = CW / kChunk;
+                    float r[2][kChunk];
+                    tmem_ld(at, r[0]);
 #pragma unroll
-                    for (int j = 0; j < kChunk; j += 4) {
-                        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(cols + c + j);
-                        uint64_t x = pk2(r[j], r[j + 1]), y = pk2(r[j + 2], r[j + 3]);
-                        uint64_t &ax = acc[(c + j) / 2], &ay = acc[(c + j) / 2 + 1];
-                        if (BOTH) {
-                            ax = fma2(mul2(x, w.x), rs2, ax);
-                            ay = fma2(mul2(y, w.y), rs2, ay);
-                        } else {
-                            ax = fma2(x, w.x, ax);
-                            ay = fma2(y, w.y, ay);
+                    for (int c = 0; c < kChunks; ++c) {
+                        tmem_wait(r[c & 1]);
+                        if (c + 1 < kChunks) tmem_ld(at + (c + 1) * kChunk, r[(c + 1) & 1]);
+                        else release();
+#pragma unroll
+                        for (int j = 0; j < kChunk; j += 4) {
+                            uint64_t wx, wy;
+                            ld_shared_pairs(cols + (first + c * kChunk + j) * 4, wx, wy);
+                            const float* v = r[c & 1] + j;
+                            const uint64_t x = pk2(v[0], v[1]), y = pk2(v[2], v[3]);
+                            uint64_t &ax = acc[(c * kChunk + j) / 2], &ay = acc[(c * kChunk + j) / 2 + 1];
+                            ax = BOTH ? fma2(mul2(x, wx), rs[0], ax) : fma2(x, wx, ax);
+                            ay = BOTH ? fma2(mul2(y, wy), rs[0], ay) : fma2(y, wy, ay);
                         }
                     }
                 }
-                if (++buf == 2) {
-                    buf = 0;
-                    bph ^= 1u;
+                ++t;
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
                 }
                 if (kk == kSlab - 1 || kb + 1 == k_blocks) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(slabe_bar(i));
-                    if (++i == kSlabs) {
-                        i = 0;
-                        ph ^= 1u;
-                    }
+                    if (lane == 0) mbar_arrive(slabe_bar(u & 1));
+                    ++u;
                 }
             }
             if (!ok) {
@@ -542,36 +697,34 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
                 break;
             }
             if (!PAIR && p.shares > 1) {
-                // every copy and MMA of this CTA is done: the sums take the stages' place, [column][row]
+                // every copy and MMA of this CTA is done: the sums take the stages' place, neighbouring results side by side
                 float* sums = reinterpret_cast<float*>(gbase);
+                if constexpr (WIDE) {
 #pragma unroll
-                for (int c = 0; c < CW; c += 2) {
-                    float x, y;
-                    up2(acc[c / 2], x, y);
-                    sums[(first + c) * kLanes + row] = x;
-                    sums[(first + c + 1) * kLanes + row] = y;
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < CW / 8; ++j) {
+                            const int row = quad * 32 + 8 * i + (lane >> 2);
+                            *reinterpret_cast<uint64_t*>(sums + row * C::kCols + first + 8 * j + 2 * (lane & 3)) =
+                                acc[i * (CW / 8) + j];
+                        }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) sums[(first + c) * kLanes + quad * 32 + lane] = column(acc, c);
                 }
                 break;  // one tile a cluster
             }
-            int mt, nt;
-            tile_at(p, tile, mt, nt);
-            const int n = nt * C::kRows + peer * kLanes + row, m0 = mt * C::kCols + first;
-            const int live = n < p.N ? p.M - m0 : 0;
-            const int64_t at = (int64_t)m0 * p.ldd + n;
-            if (p.d_f32) {
-                float* d = (float*)p.d + at;
-#pragma unroll
-                for (int c = 0; c < CW; ++c) {
-                    if (c < live) *d = p.accumulate ? *d + column(acc, c) : column(acc, c);
-                    d += p.ldd;
-                }
+            int pt, qt;
+            tile_at(p, tile, pt, qt);
+            const int p0 = pt * C::kRows + peer * kLanes + quad * 32, q0 = qt * C::kCols + first;
+            if constexpr (WIDE) {
+                store_wide<CW>(p, acc, p0 + (lane >> 2), q0);
             } else {
-                __nv_bfloat16* d = (__nv_bfloat16*)p.d + at;
+                const int live = p0 + lane < p.p_rows ? p.q_rows - q0 : 0;
+                const int64_t at = (int64_t)q0 * p.ldd + p0 + lane;
 #pragma unroll
-                for (int c = 0; c < CW; ++c) {
-                    if (c < live) *d = __float2bfloat16_rn(column(acc, c));
-                    d += p.ldd;
-                }
+                for (int c = 0; c < CW; ++c)
+                    if (c < live) put(p, at + c * p.ldd, column(acc, c));
             }
         }
     }
@@ -580,14 +733,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
     if (PAIR) cluster_sync_all();  // neither CTA leaves while the other may still use its memory or barriers
     if (!PAIR && p.shares > 1) {
         cluster_sync_all();  // all shares' sums are there
-        int mt, nt;
-        tile_at(p, cluster_id, mt, nt);
-        // each CTA adds its share of the columns over the ranks, in their order
-        const int share = (C::kCols + p.shares - 1) / p.shares;
-        const int begin = (int)rank * share, end = min(C::kCols, begin + share);
-        const int live = min(end, p.M - mt * C::kCols);
-        for (int i = begin * kLanes + (int)threadIdx.x; i < live * kLanes; i += C::kThreads) {
-            const int n = nt * C::kRows + (i & (kLanes - 1));
+        int pt, qt;
+        tile_at(p, cluster_id, pt, qt);
+        // each CTA adds its share of D's rows over the ranks, in their order
+        constexpr int kDRows = WIDE ? kLanes : C::kCols, kDCols = WIDE ? C::kCols : kLanes;
+        const int m0 = WIDE ? pt * kLanes : qt * C::kCols, n0 = WIDE ? qt * C::kCols : pt * kLanes;
+        const int M = WIDE ? p.p_rows : p.q_rows, N = WIDE ? p.q_rows : p.p_rows;
+        const int rows = min(kDRows, M - m0), share = (rows + p.shares - 1) / p.shares;
+        const int begin = (int)rank * share, end = min(rows, begin + share);
+        for (int i = begin * kDCols + (int)threadIdx.x; i < end * kDCols; i += C::kThreads) {
             float v[kMaxShares];
 #pragma unroll
             for (int r = 0; r < kMaxShares; ++r)
@@ -596,18 +750,19 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant
 #pragma unroll
             for (int r = 1; r < kMaxShares; ++r)
                 if (r < p.shares) sum += v[r];
-            if (n < p.N) put(p, mt * C::kCols + (i >> 7), n, sum);
+            const int n = n0 + i % kDCols;
+            if (n < N) put(p, (int64_t)(m0 + i / kDCols) * p.ldd + n, sum);
         }
         cluster_sync_all();  // no CTA leaves while another reads its sums
     }
-    if (__builtin_expect(*abort_flag, 0)) {
+    if (__builtin_expect(ld_shared(abort_flag), 0)) {
         // A wait gave up (both CTAs of a pair know): stages that were filled but not used may still be on their way into
         // either CTA.  They are waited for before any CTA leaves, with a limit, since a stage that only one of the
         // copiers filled never completes.
         if (threadIdx.x == 0 && peer == 0) {
             int most = stages_of[0];
             if (PAIR) most = max(most, ld_cluster(map_to_rank(base + C::kOffWords + 8, 1)));
-            for (int i = stages_of[1]; i < most; ++i) mbar_wait(full_bar(i % S), (i / S) & 1, nullptr, kDrainLimit);
+            for (int i = stages_of[1]; i < most; ++i) mbar_wait(full_bar(i % S), (i / S) & 1, 0, kDrainLimit);
         }
         __syncthreads();
         if (PAIR) cluster_sync_all();
@@ -628,44 +783,46 @@ int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
     static DeviceFigure clusters;
     return clusters.get(dev, [&] {
         int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<true, BOTH, 64, 4>, &cfg) == cudaSuccess ? n : 0;
+        return cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<true, true, BOTH, 128, 2>, &cfg) == cudaSuccess ? n : 0;
     });
 }
 
-template <bool PAIR, bool BOTH, int CW, int GROUPS>
+template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
 cudaError_t run(const Fp8GemmArgs& a, int shares, cudaStream_t st) {
-    using C = Cfg<PAIR, CW, GROUPS>;
+    using C = Cfg<WIDE, PAIR, CW, GROUPS>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const Fp8Operand &op = WIDE ? a.a : a.b, &oq = WIDE ? a.b : a.a;
+    const int64_t p_rows = WIDE ? a.M : a.N, q_rows = WIDE ? a.N : a.M;
     Fp8Params p = {};
-    p.M = (int)a.M;
-    p.N = (int)a.N;
+    p.p_rows = (int)p_rows;
+    p.q_rows = (int)q_rows;
     p.blocks = (int)((a.K + kStep - 1) / kStep);
-    p.m_tiles = (int)((a.M + C::kCols - 1) / C::kCols);
-    p.n_tiles = (int)((a.N + C::kRows - 1) / C::kRows);
-    p.group = PAIR ? 8 : 1 << 30;
+    p.p_tiles = (int)((p_rows + C::kRows - 1) / C::kRows);
+    p.q_tiles = (int)((q_rows + C::kCols - 1) / C::kCols);
+    p.group = kGroup;
     p.shares = PAIR ? 1 : shares;
     p.per = (p.blocks + p.shares - 1) / p.shares;
-    p.a_rows = (int)std::min<int64_t>(C::kQRows, (a.M + 7) / 8 * 8);
-    if (PAIR) p.a_rows = C::kQRows;
+    p.q_box = WIDE ? C::kQRows : (int)std::min<int64_t>(C::kQRows, (q_rows + 7) / 8 * 8);
     p.wait_limit = kWaitLimit - g_lowered[dev].load(std::memory_order_relaxed);
-    p.sa = a.a.scales;
-    p.sb = a.b.scales;
-    p.ld_sa = a.a.scales_ld;
-    p.ld_sb = a.b.scales_ld;
-    p.a_shift = a.a_square ? 7 : 0;
-    p.b_shift = a.b_square ? 7 : 0;
+    p.sp = op.scales;
+    p.sq = oq.scales;
+    p.ld_sp = op.scales_ld;
+    p.ld_sq = oq.scales_ld;
+    p.p_shift = (WIDE ? a.a_square : a.b_square) ? 7 : 0;
+    p.q_shift = (WIDE ? a.b_square : a.a_square) ? 7 : 0;
     p.d = a.d;
     p.ldd = a.ldd;
     p.d_f32 = a.d_f32;
     p.accumulate = a.accumulate;
-    CUtensorMap ma, mb;
-    if (!encode_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a.codes, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.a.codes_ld,
-                       kStep, (uint32_t)p.a_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.b.codes, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.b.codes_ld,
-                       kStep, kLanes, CU_TENSOR_MAP_SWIZZLE_128B))
+    p.d_vec = (uintptr_t)a.d % 16 == 0 && a.ldd % (a.d_f32 ? 4 : 8) == 0 ? 16 : 1;
+    CUtensorMap mp, mq;
+    if (!encode_map_2d(&mp, CU_TENSOR_MAP_DATA_TYPE_UINT8, op.codes, (uint64_t)a.K, (uint64_t)p_rows, (uint64_t)op.codes_ld,
+                       kStep, kLanes, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_map_2d(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, oq.codes, (uint64_t)a.K, (uint64_t)q_rows, (uint64_t)oq.codes_ld,
+                       kStep, (uint32_t)p.q_box, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    auto k = fp8_gemm_kernel<PAIR, BOTH, CW, GROUPS>;
+    auto k = fp8_gemm_kernel<WIDE, PAIR, BOTH, CW, GROUPS>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(C::kThreads);
@@ -680,7 +837,7 @@ cudaError_t run(const Fp8GemmArgs& a, int shares, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
     if (PAIR) {
         const int most = max_pairs<BOTH>(dev, cfg);
         if (most <= 0) return cudaErrorLaunchOutOfResources;
@@ -689,18 +846,11 @@ cudaError_t run(const Fp8GemmArgs& a, int shares, cudaStream_t st) {
         cfg.gridDim = dim3((unsigned)(tiles * shares));
     }
     cfg.numAttrs = st ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k, ma, mb, p);
+    return cudaLaunchKernelEx(&cfg, k, mp, mq, p);
 }
 
-template <bool BOTH>
-cudaError_t launch(const Fp8GemmArgs& a, int num_sms, cudaStream_t st) {
-    const int64_t blocks = (a.K + kStep - 1) / kStep;
-    const int64_t pair_tiles = (a.M + 255) / 256 * ((a.N + 255) / 256);
-    if (a.M > 128 && pair_tiles >= num_sms / 4) return run<true, BOTH, 64, 4>(a, 1, st);
-    const int64_t width = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : (a.M <= 64 ? 64 : 128));
-    const int64_t tiles = (a.M + width - 1) / width * ((a.N + kLanes - 1) / kLanes);
-    const int64_t room = (width <= 64 ? 2 : 1) * (int64_t)num_sms;
-    // shares: the fewest blocks for the busiest SM
+// Shares of the summed index: the fewest blocks for the busiest SM, of which each holds `room` CTAs.
+int best_shares(int64_t tiles, int64_t blocks, int64_t room) {
     int shares = 1;
     int64_t best = 1ll << 60;
     for (int s = 1; s <= kMaxShares && s <= blocks; ++s) {
@@ -711,24 +861,35 @@ cudaError_t launch(const Fp8GemmArgs& a, int num_sms, cudaStream_t st) {
             shares = s;
         }
     }
-    if (width == 16) return run<false, BOTH, 16, 1>(a, shares, st);
-    if (width == 32) return run<false, BOTH, 32, 1>(a, shares, st);
-    if (width == 64) return run<false, BOTH, 64, 1>(a, shares, st);
-    return run<false, BOTH, 64, 2>(a, shares, st);
+    return shares;
 }
 
-template <bool PAIR, bool BOTH, int CW, int GROUPS>
+template <bool BOTH>
+cudaError_t launch(const Fp8GemmArgs& a, int num_sms, cudaStream_t st) {
+    const int64_t blocks = (a.K + kStep - 1) / kStep, lanes = (a.N + kLanes - 1) / kLanes;
+    if (a.M <= 64) {
+        const int shares = best_shares(lanes, blocks, 2 * (int64_t)num_sms);
+        if (a.M <= 16) return run<false, false, BOTH, 16, 1>(a, shares, st);
+        if (a.M <= 32) return run<false, false, BOTH, 32, 1>(a, shares, st);
+        return run<false, false, BOTH, 64, 1>(a, shares, st);
+    }
+    const int64_t pair_tiles = (a.M + 255) / 256 * ((a.N + 255) / 256);
+    if (pair_tiles >= num_sms / 4) return run<true, true, BOTH, 128, 2>(a, 1, st);
+    return run<true, false, BOTH, 64, 2>(a, best_shares((a.M + 127) / 128 * lanes, blocks, num_sms), st);
+}
+
+template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
 cudaError_t preload() {
-    return cudaFuncSetAttribute(fp8_gemm_kernel<PAIR, BOTH, CW, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Cfg<PAIR, CW, GROUPS>::kSmem);
+    return cudaFuncSetAttribute(fp8_gemm_kernel<WIDE, PAIR, BOTH, CW, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Cfg<WIDE, PAIR, CW, GROUPS>::kSmem);
 }
 template <bool BOTH>
 cudaError_t preload_all() {
-    cudaError_t e = preload<true, BOTH, 64, 4>();
-    if (e == cudaSuccess) e = preload<false, BOTH, 16, 1>();
-    if (e == cudaSuccess) e = preload<false, BOTH, 32, 1>();
-    if (e == cudaSuccess) e = preload<false, BOTH, 64, 1>();
-    return e == cudaSuccess ? preload<false, BOTH, 64, 2>() : e;
+    cudaError_t e = preload<true, true, BOTH, 128, 2>();
+    if (e == cudaSuccess) e = preload<true, false, BOTH, 64, 2>();
+    if (e == cudaSuccess) e = preload<false, false, BOTH, 16, 1>();
+    if (e == cudaSuccess) e = preload<false, false, BOTH, 32, 1>();
+    return e == cudaSuccess ? preload<false, false, BOTH, 64, 1>() : e;
 }
 
 }  // namespace
