@@ -16,13 +16,13 @@
 // Pairs and singles (WIDE): P is A, Q is B.  Pairs are persistent CTA pairs with
 // 256 x 256 tiles, tcgen05.mma .cta_group::2, where a CTA holds 128 rows of either
 // operand; singles are 128 x 128 tiles of one CTA, for products with too few of
-// the large ones.  A block of a pair's tile is 512 cycles of the tensor core, and
-// 256 of an SM's fp32 lanes for one multiply-add an element.  What would not fit
-// is to bring every thread a scale for every column: 128 lanes x 256 columns from
-// shared memory are 1024 cycles.  So the sums are read in the layout that gives
-// a thread four rows and a quarter of the columns (16 x 256 bits), and where B has
-// square blocks one scale a row and 128 columns is all that it needs; with scales
-// for either's rows (WGRAD) a column pair's are read once for four rows.
+// the large ones.  A block of a pair's tile is 512 cycles of the tensor core.
+// With square blocks of B a lane that holds a row needs one scale for 128 columns,
+// and the sums are read a row a lane, the layout that tensor memory reads fastest
+// (128 x 256 sums of an SM in about 155 cycles; 16 lanes x 256 bits: 512).  With
+// scales for the rows of either operand (WGRAD) every column has its own: brought
+// from shared memory to every lane that would be 1024 cycles, so the sums are read
+// 16 lanes x 256 bits, which gives a thread four rows and a quarter of the columns.
 //
 // Few tokens (up to 64): P is B, Q is A, so that the tile is as wide as there
 // are tokens and the weights are read once.  A lane holds a row of B, and 32
@@ -54,8 +54,8 @@ constexpr int kAtom = kLanes * kStep;
 constexpr int kSlab = 4;                   // blocks whose scales are laid out at a time
 constexpr int kSlabs = 2;
 constexpr int kPad = 8;                    // floats between a slab's blocks, off the same bank
+constexpr int kOthers = 4;                 // warps that do not scale
 constexpr int kLoaders = 64;               // threads that lay out scales (warps 2 and 3)
-constexpr int kOthers = 128;               // threads of warps 0 to 3
 constexpr int kMaxShares = 8;
 constexpr int kGroup = 8;                  // tiles of P that advance before the tile of Q does
 constexpr uint32_t kWaitLimit = 1u << 22;  // bounded polling; each poll may sleep up to kSuspendNs
@@ -68,16 +68,17 @@ template <bool WIDE, bool PAIR, int CW, int GROUPS>
 struct Cfg {
     static constexpr int kCols = CW * GROUPS;                 // columns of a tile
     static constexpr int kRows = PAIR ? 2 * kLanes : kLanes;  // rows of a tile
-    static constexpr int kThreads = kOthers + 128 * GROUPS;
-    static constexpr bool kSplit = CW == 128;                 // registers go from warps 0 to 3 to the others
+    static constexpr int kThreads = 32 * kOthers + 128 * GROUPS;
+    static constexpr bool kSplit = CW == 128;                 // registers go from the first four warps to the others
     static constexpr int kQRows = PAIR ? kCols / 2 : kCols;   // rows of Q that a CTA holds
     static constexpr int kQ = kQRows * kStep;
     static constexpr int kStage = kAtom + kQ;
-    static constexpr int kStages = WIDE ? 6 : (kCols <= 32 ? 5 : 4);
+    static constexpr int kStages = WIDE || kCols <= 32 ? 5 : 4;
     static constexpr int kColPitch = kCols + kPad, kRowPitch = kLanes + kPad;
     static constexpr int kSlabFloats = kSlab * (kColPitch + kRowPitch);
     static constexpr int kOffScales = kStages * kStage;
-    static constexpr int kOffBars = kOffScales + kSlabs * kSlabFloats * 4;
+    static constexpr int kOffOut = kOffScales + (kSlabs * kSlabFloats * 4 + 15) / 16 * 16;  // 4 KB for each scaling warp
+    static constexpr int kOffBars = kOffOut + (WIDE ? 4 * GROUPS * 4096 : 0);
     // full, done; partial sums read x2; slabs full, empty; drain
     static constexpr int kNumBars = 2 * kStages + 2 + 2 * kSlabs + 1;
     static constexpr int kOffWords = kOffBars + 8 * kNumBars;  // tensor memory address, abort flag, stages filled and used
@@ -114,33 +115,36 @@ __device__ __forceinline__ float ld_shared_f(uint32_t saddr) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(saddr));
     return v;
 }
-// Two pairs of floats, 16-byte aligned.
-__device__ __forceinline__ void ld_shared_pairs(uint32_t saddr, uint64_t& a, uint64_t& b) {
-    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(saddr));
-}
 __device__ __forceinline__ uint64_t ld_shared_pair(uint32_t saddr) {
     uint64_t v;
     asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(saddr));
     return v;
 }
-// Bounded wait on an mbarrier phase; false at the limit (with the error word
-// set), or once the word at `abort` (0: none) is set, which is looked at every
-// kLook polls.
+// Two pairs of floats, 16-byte aligned.
+__device__ __forceinline__ void ld_shared_pairs(uint32_t saddr, uint64_t& a, uint64_t& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(saddr));
+}
+// Bounded wait of a whole warp on an mbarrier phase, the same answer in every
+// lane: false at the limit (with the error word set), or once the word at
+// `abort` (0: none) is set, which is looked at every kLook polls.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit = kWaitLimit) {
-    for (uint32_t left = limit; left;) {
-        const uint32_t n = min(left, kLook);
-        for (uint32_t i = 0; i < n; ++i) {
-            uint32_t ok;
-            asm volatile(
-                "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;"
-                " selp.u32 %0, 1, 0, p; }"
-                : "=r"(ok)
-                : "r"(bar), "r"(parity), "r"(kSuspendNs)
-                : "memory");
-            if (ok) return true;
-        }
-        left -= n;
-        if (abort && ld_shared(abort)) return false;
+    uint32_t ok;
+    if (limit) {  // most waits find what they wait for: a test is answered in 15 cycles, a wait in 50
+        asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (__all_sync(0xFFFFFFFFu, ok)) return true;
+    }
+#pragma unroll 1
+    for (uint32_t i = 0; i < limit; ++i) {
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (__all_sync(0xFFFFFFFFu, ok)) return true;
+        if ((i + 1) % kLook == 0 && abort && __any_sync(0xFFFFFFFFu, ld_shared(abort))) return false;
     }
     atomicExch(&g_fp8_error, 1);
     return false;
@@ -244,8 +248,7 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, int cols) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
 }
 // 16 or 32 columns of a warp's 32 lanes, a lane a row ...
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[32]) {
-    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&u)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -256,8 +259,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[32]) {
           "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[16]) {
-    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&u)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
@@ -266,8 +268,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 // ... or 64 columns of 16 lanes: r[4 j + e] is row lane / 4, r[4 j + 2 + e] row lane / 4 + 8, column 8 j + 2 (lane % 4) + e.
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&r)[32]) {
-    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&u)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -287,10 +288,16 @@ __device__ __forceinline__ bool elect_one() {
 // Waits for all of this warp's reads; `r` are what one of them brings (they are
 // not to be used before).
 template <int N>
-__device__ __forceinline__ void tmem_wait(float (&r)[N]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
 }
 
 // ------------------------------------------------------------------- kernel
@@ -334,13 +341,13 @@ __device__ __forceinline__ float column(const uint64_t* acc, int c) {
     return c & 1 ? y : x;
 }
 __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
-    float x, y;
-    up2(v, x, y);
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    float lo, hi;
+    up2(v, lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A wide tile's sums of a warp (rows row0 + 8 i, i = 0..3, of the lane's quad; pairs of columns 8 j + 2 (lane % 4), j = 0 ..
+// A wide tile's sums of a warp that reads 16 lanes x 256 bits (rows row0 + 8 i, i = 0..3, of the lane's quad; pairs of columns 8 j + 2 (lane % 4), j = 0 ..
 // CW / 8 - 1, acc[i * CW / 8 + j]) into D.  bf16: four lanes turn four groups of 8 columns around, so that each stores 16
 // bytes, 64 of a row in a piece; fp32 pairs fill whole sectors as they are.
 template <int CW>
@@ -396,6 +403,65 @@ __device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&
                 }
             }
         }
+    }
+}
+
+// The same of a warp whose lanes hold a row each (row0 + lane; columns col0 on in order).  A lane's own stores would touch 32
+// rows at a time; instead 128 bytes of every row are turned around in `stage` (16-byte units, unit u of row i at u ^ (i & 7))
+// and stored four whole rows of them an instruction.
+template <int CW>
+__device__ __forceinline__ void store_rows(const Fp8Params& p, const uint64_t (&acc)[CW / 2], int row0, int col0,
+                                           uint8_t* stage) {
+    const int lane = threadIdx.x & 31;
+    if (col0 + CW <= p.q_rows && p.d_vec == 16) {
+        uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
+        auto flush = [&](int c, int bytes) {  // the stage holds columns col0 + c on
+            __syncwarp();
+            char* base = (char*)p.d + ((int64_t)(row0 + (lane >> 3)) * p.ldd + col0 + c) * bytes + (lane & 7) * 16;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = i * 4 + (lane >> 3);
+                uint4 v = reinterpret_cast<const uint4*>(stage + row * 128)[(lane & 7) ^ (row & 7)];
+                if (row0 + row < p.p_rows) {
+                    uint4* d = reinterpret_cast<uint4*>(base + (int64_t)i * 4 * p.ldd * bytes);
+                    if (p.accumulate) {
+                        const uint4 o = *d;
+                        v = make_uint4(__float_as_uint(__uint_as_float(o.x) + __uint_as_float(v.x)),
+                                       __float_as_uint(__uint_as_float(o.y) + __uint_as_float(v.y)),
+                                       __float_as_uint(__uint_as_float(o.z) + __uint_as_float(v.z)),
+                                       __float_as_uint(__uint_as_float(o.w) + __uint_as_float(v.w)));
+                    }
+                    *d = v;
+                }
+            }
+            __syncwarp();
+        };
+        if (p.d_f32) {
+#pragma unroll
+            for (int c = 0; c < CW; c += 32) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint64_t x = acc[c / 2 + 2 * u], y = acc[c / 2 + 2 * u + 1];
+                    mine[u ^ (lane & 7)] = make_uint4((uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32));
+                }
+                flush(c, 4);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < CW; c += 64) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint64_t* a = acc + c / 2 + 4 * u;
+                    mine[u ^ (lane & 7)] = make_uint4(pack_bf16(a[0]), pack_bf16(a[1]), pack_bf16(a[2]), pack_bf16(a[3]));
+                }
+                flush(c, 2);
+            }
+        }
+    } else if (row0 + lane < p.p_rows) {
+        const int64_t at = (int64_t)(row0 + lane) * p.ldd + col0;
+#pragma unroll
+        for (int c = 0; c < CW; ++c)
+            if (col0 + c < p.q_rows) put(p, at + c, column(acc, c));
     }
 }
 
@@ -464,19 +530,19 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         if (PAIR) st_cluster(map_to_rank(abort_flag, rank ^ 1u), 1);
     };
 
-    // With kSplit, what the threads of warps 0 to 3 give up of the launch's 168 registers, twice as many others take:
-    // 128 x 72 + 256 x 216 = 384 x 168.
-    if (warp < 4) {
+    // With kSplit, what the threads of the first four warps give up of the launch's 168 registers, twice as many others
+    // take: 128 x 72 + 256 x 216 = 384 x 168.
+    if (warp < kOthers) {
         if (C::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // The copier and the issuer are whole warps, of which one lane acts: what a lane alone computes has to be moved to
         // the uniform registers of its copies and MMAs each time (a step of the issuer took 1000 cycles).
         if (warp == 0) {
-            // ---------------------------------------------------- TMA copies
+            // ---------------------------------------------------- copies
             const bool acts = elect_one();
-            int s = 0, stages = 0;
-            uint32_t ph = 0;
             const uint32_t tx = PAIR ? 2 * C::kStage : kAtom + (uint32_t)p.q_box * kStep;
             const uint32_t remote = PAIR ? map_to_rank(bars, 0) : bars;
+            int s = 0, stages = 0;
+            uint32_t ph = 0;
             bool ok = true;
             for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
                 int pt, qt;
@@ -484,10 +550,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 const int prow = pt * C::kRows + peer * kLanes, qrow = qt * C::kCols + peer * C::kQRows;
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     ok = mbar_wait(done_bar(s), ph ^ 1u, abort_flag);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!ok) break;
                     ++stages;
                     if (acts) {
                         if (peer == 0) mbar_expect_tx(full_bar(s), tx);
@@ -495,6 +558,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         tma_load<PAIR>(dst, &map_p, (k0 + kb) * kStep, prow, remote + 8u * s);
                         tma_load<PAIR>(dst + kAtom, &map_q, (k0 + kb) * kStep, qrow, remote + 8u * s);
                     }
+                    __syncwarp();
                     if (++s == S) {
                         s = 0;
                         ph ^= 1u;
@@ -513,10 +577,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
                 for (int kb = 0; kb < k_blocks; ++kb) {
                     ok = mbar_wait(full_bar(s), ph, 0, p.wait_limit) && mbar_wait(read_bar(t & 1), (t >> 1 & 1) ^ 1u, abort_flag);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!ok) break;
                     ++stages;
                     tc_fence_after();
                     if (acts) {
@@ -539,49 +600,48 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             if (acts) tc_commit_local<PAIR>(drain_bar);
             mbar_wait(drain_bar, 0, 0);
         } else if (warp >= 2) {
-            // ------------------------------------------------ scales
+            // ---------------------------------------------------- scales
             // A slab is the scales of up to kSlab blocks: those of the tile's columns and of the CTA's rows, each block's apart.
-            // A thread takes one block, and every 16th column or row.  What lies past the operands is read at their edge
-            // instead; nothing looks at it.
+            // A thread takes one block, and every 16th column or row, and loads them before the slab is free.  What lies past
+            // the operands is read at their edge instead; nothing looks at it.
             const int tid = threadIdx.x - 64;
             const int kk = tid & (kSlab - 1), each = tid >> 2;
             constexpr bool kOfCols = !WIDE || BOTH;  // every column its scale; otherwise one for each 128
             constexpr bool kOfRows = WIDE || BOTH;   // every row its scale; otherwise in the columns'
-            int i = 0;
-            uint32_t ph = 0;
+            constexpr int kC = kOfCols ? C::kCols / 16 : 1, kR = kOfRows ? kLanes / 16 : 1;
+            uint32_t u = 0;
             bool ok = true;
             for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
                 int pt, qt;
                 tile_at(p, tile, pt, qt);
                 const int p0 = pt * C::kRows + peer * kLanes, q0 = qt * C::kCols;
-                for (int kb = 0; kb < k_blocks; kb += kSlab) {
+                for (int kb = 0; kb < k_blocks; kb += kSlab, ++u) {
                     const int64_t b = min(k0 + kb + kk, p.blocks - 1);
                     const float* sp = p.sp + b;
                     const float* sq = p.sq + b;
-                    auto of_p = [&](int r) { return sp[(int64_t)(min(p0 + r, p.p_rows - 1) >> p.p_shift) * p.ld_sp]; };
-                    auto of_q = [&](int r) { return sq[(int64_t)(min(q0 + r, p.q_rows - 1) >> p.q_shift) * p.ld_sq]; };
-                    constexpr int kC = kOfCols ? C::kCols / 16 : 1, kR = kOfRows ? kLanes / 16 : 1;
                     float v[kC], w[kR];
 #pragma unroll
-                    for (int j = 0; j < kC; ++j) v[j] = of_q(kOfCols ? each + 16 * j : min(each * 128, C::kCols - 1));
-#pragma unroll
-                    for (int j = 0; j < kR; ++j) w[j] = of_p(kOfRows ? each + 16 * j : 0);
-                    if (!mbar_wait(slabe_bar(i), ph ^ 1u, abort_flag)) {
-                        ok = false;
-                        break;
+                    for (int j = 0; j < kC; ++j) {
+                        const int r = kOfCols ? each + 16 * j : min(each * 128, C::kCols - 1);
+                        v[j] = sq[(int64_t)(min(q0 + r, p.q_rows - 1) >> p.q_shift) * p.ld_sq];
                     }
-                    float* cols = reinterpret_cast<float*>(gbase + C::kOffScales) + i * C::kSlabFloats + kk * C::kColPitch;
-                    float* rows = reinterpret_cast<float*>(gbase + C::kOffScales) + i * C::kSlabFloats + kSlab * C::kColPitch +
-                                  kk * C::kRowPitch;
 #pragma unroll
-                    for (int j = 0; j < kC; ++j) cols[each + 16 * j] = kOfRows ? v[j] : v[j] * w[0];
+                    for (int j = 0; j < kR; ++j) {
+                        const int r = kOfRows ? each + 16 * j : 0;
+                        w[j] = sp[(int64_t)(min(p0 + r, p.p_rows - 1) >> p.p_shift) * p.ld_sp];
+                    }
+                    ok = mbar_wait(slabe_bar(u % kSlabs), (u / kSlabs & 1) ^ 1u, abort_flag);
+                    if (!ok) break;
+                    float* cols = reinterpret_cast<float*>(gbase + C::kOffScales) + (u % kSlabs) * C::kSlabFloats +
+                                  kk * C::kColPitch + each;
+                    float* rows = cols + (kSlab - kk) * C::kColPitch + kk * C::kRowPitch;
+#pragma unroll
+                    for (int j = 0; j < kC; ++j) cols[16 * j] = kOfRows ? v[j] : v[j] * w[0];
                     if (kOfRows) {
 #pragma unroll
-                        for (int j = 0; j < kR; ++j) rows[each + 16 * j] = w[j];
+                        for (int j = 0; j < kR; ++j) rows[16 * j] = w[j];
                     }
-                    mbar_arrive(slabf_bar(i));
-                    i ^= 1;
-                    ph ^= i == 0;
+                    mbar_arrive(slabf_bar(u % kSlabs));
                 }
             }
             if (!ok) give_up();
@@ -589,95 +649,94 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     } else {
         // ------------------------------------------------- scaling and adding
         if (C::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int quad = warp & 3, first = ((warp - 4) >> 2) * CW;
+        const int quad = warp & 3, first = ((warp - kOthers) >> 2) * CW;  // a warp reads the quarter of the lanes that is its own
         const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + first;
-        const uint32_t scales = base + C::kOffScales;
-        uint32_t t = 0, u = 0;  // blocks and slabs so far: buffer t & 1, slab u & 1
+        const uint32_t slabs = base + C::kOffScales;
+        const uint32_t read = PAIR ? map_to_rank(read_bar(0), 0) : read_bar(0);  // the issuer's
+        const uint32_t own_row = (kSlab * C::kColPitch + quad * 32 + (WIDE && BOTH ? lane >> 2 : lane)) * 4;
+        uint32_t t = 0, u = 0;  // blocks and slabs so far: buffer t & 1, slab u % kSlabs
         int s = 0;              // stage of block t
         uint32_t ph = 0;
         bool ok = true;
-        uint64_t acc[CW / 2];  // pairs of columns; WIDE: see store_wide
+        uint64_t acc[CW / 2];     // pairs of columns; WIDE: see store_wide
         for (int tile = cluster_id; tile < num_tiles; tile += num_clusters) {
 #pragma unroll
             for (int c = 0; c < CW / 2; ++c) acc[c] = 0;
+#pragma unroll 1
             for (int kb = 0; kb < k_blocks; ++kb) {
                 const int kk = kb & (kSlab - 1);
-                if (kk == 0) ok = mbar_wait(slabf_bar(u & 1), (u >> 1) & 1, abort_flag);
-                const uint32_t cols = scales + ((u & 1) * C::kSlabFloats + kk * C::kColPitch) * 4;
-                const uint32_t rows = scales + ((u & 1) * C::kSlabFloats + kSlab * C::kColPitch + kk * C::kRowPitch) * 4;
-                uint64_t rs[WIDE ? 4 : 1];  // of the lane's rows, times the columns' where they share one
-                if constexpr (WIDE) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float v = ld_shared_f(rows + (quad * 32 + 8 * i + (lane >> 2)) * 4);
-                        if (!BOTH) v *= ld_shared_f(cols + (first >> 7) * 4);
-                        rs[i] = pk2(v, v);
-                    }
-                } else {
-                    const float v = BOTH ? ld_shared_f(rows + (quad * 32 + lane) * 4) : 1.0f;
-                    rs[0] = pk2(v, v);
-                }
+                if (kk == 0) ok = mbar_wait(slabf_bar(u % kSlabs), u / kSlabs & 1, abort_flag);
                 ok = ok && mbar_wait(done_bar(s), ph, abort_flag);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
+                if (!ok) break;
                 tc_fence_after();
+                const uint32_t slab = slabs + (u % kSlabs) * (C::kSlabFloats * 4);
+                const uint32_t cols = slab + (kk * C::kColPitch + first) * 4;
                 const uint32_t at = from + (t & 1) * C::kCols;
                 auto release = [&] {  // the buffer has been read and may be filled again
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(map_to_rank(read_bar(t & 1), 0));
-                        else mbar_arrive(read_bar(t & 1));
+                        if (PAIR) mbar_arrive_cluster(read + 8u * (t & 1));
+                        else mbar_arrive(read + 8u * (t & 1));
                     }
                 };
-                if constexpr (WIDE) {
-                    // 64 columns of 16 rows at a time
-                    constexpr int kChunks = CW / 32;
-                    float r[2][32];
-                    tmem_ld_rows(at, r[0]);
+                const uint32_t rows = slab + own_row + kk * C::kRowPitch * 4;
+                if constexpr (WIDE && !BOTH) {
+                    const float v = ld_shared_f(rows) * ld_shared_f(slab + (kk * C::kColPitch + (first >> 7)) * 4);
+                    const uint64_t s2 = pk2(v, v);
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
+                    for (int c = 0; c < CW; c += 32) {
+                        uint32_t r[32];
+                        tmem_ld(at + c, r);
+                        tmem_wait(r);
+                        if (c + 32 == CW) release();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c / 2 + j] = fma2(pair(r[2 * j], r[2 * j + 1]), s2, acc[c / 2 + j]);
+                    }
+                } else if constexpr (WIDE) {
+                    uint64_t rs[4];  // the scales of the lane's rows
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = ld_shared_f(rows + 32 * i);
+                        rs[i] = pk2(v, v);
+                    }
+                    // 64 columns of 16 rows at a time
+#pragma unroll
+                    for (int c = 0; c < CW / 32; ++c) {
                         const int half = c & 1, col = (c >> 1) * 64;
-                        tmem_wait(r[c & 1]);
-                        if (c + 1 < kChunks)  // on its way while this one is added
-                            tmem_ld_rows(at + ((c + 1) >> 1) * 64 + ((uint32_t)((c + 1) & 1) << 20), r[(c + 1) & 1]);
-                        else
-                            release();
+                        uint32_t r[32];
+                        tmem_ld_rows(at + col + ((uint32_t)half << 20), r);
+                        tmem_wait(r);
+                        if (c + 1 == CW / 32) release();
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float* v = r[c & 1] + 4 * j;
-                            uint64_t x = pk2(v[0], v[1]), y = pk2(v[2], v[3]);
-                            if (BOTH) {
-                                const uint64_t w = ld_shared_pair(cols + (first + col + 8 * j + 2 * (lane & 3)) * 4);
-                                x = mul2(x, w);
-                                y = mul2(y, w);
+                            const uint64_t w2 = ld_shared_pair(cols + (col + 8 * j + 2 * (lane & 3)) * 4);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint64_t x = pair(r[4 * j + 2 * i], r[4 * j + 2 * i + 1]);
+                                uint64_t& a = acc[(2 * half + i) * (CW / 8) + col / 8 + j];
+                                a = fma2(mul2(x, w2), rs[2 * half + i], a);
                             }
-                            uint64_t& ax = acc[(2 * half) * (CW / 8) + col / 8 + j];
-                            uint64_t& ay = acc[(2 * half + 1) * (CW / 8) + col / 8 + j];
-                            ax = fma2(x, rs[2 * half], ax);
-                            ay = fma2(y, rs[2 * half + 1], ay);
                         }
                     }
                 } else {
-                    constexpr int kChunk = CW < 32 ? CW : 32, kChunks = CW / kChunk;
-                    float r[2][kChunk];
-                    tmem_ld(at, r[0]);
+                    const float v = BOTH ? ld_shared_f(rows) : 1.0f;
+                    const uint64_t s2 = pk2(v, v);
+                    constexpr int kChunk = CW < 32 ? CW : 32;
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        tmem_wait(r[c & 1]);
-                        if (c + 1 < kChunks) tmem_ld(at + (c + 1) * kChunk, r[(c + 1) & 1]);
-                        else release();
+                    for (int c = 0; c < CW; c += kChunk) {
+                        uint32_t r[kChunk];
+                        tmem_ld(at + c, r);
+                        tmem_wait(r);
+                        if (c + kChunk == CW) release();
 #pragma unroll
                         for (int j = 0; j < kChunk; j += 4) {
                             uint64_t wx, wy;
-                            ld_shared_pairs(cols + (first + c * kChunk + j) * 4, wx, wy);
-                            const float* v = r[c & 1] + j;
-                            const uint64_t x = pk2(v[0], v[1]), y = pk2(v[2], v[3]);
-                            uint64_t &ax = acc[(c * kChunk + j) / 2], &ay = acc[(c * kChunk + j) / 2 + 1];
-                            ax = BOTH ? fma2(mul2(x, wx), rs[0], ax) : fma2(x, wx, ax);
-                            ay = BOTH ? fma2(mul2(y, wy), rs[0], ay) : fma2(y, wy, ay);
+                            ld_shared_pairs(cols + (c + j) * 4, wx, wy);
+                            const uint64_t x = pair(r[j], r[j + 1]), y = pair(r[j + 2], r[j + 3]);
+                            uint64_t &ax = acc[(c + j) / 2], &ay = acc[(c + j) / 2 + 1];
+                            ax = BOTH ? fma2(mul2(x, wx), s2, ax) : fma2(x, wx, ax);
+                            ay = BOTH ? fma2(mul2(y, wy), s2, ay) : fma2(y, wy, ay);
                         }
                     }
                 }
@@ -688,7 +747,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 }
                 if (kk == kSlab - 1 || kb + 1 == k_blocks) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(slabe_bar(u & 1));
+                    if (lane == 0) mbar_arrive(slabe_bar(u % kSlabs));
                     ++u;
                 }
             }
@@ -699,7 +758,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             if (!PAIR && p.shares > 1) {
                 // every copy and MMA of this CTA is done: the sums take the stages' place, neighbouring results side by side
                 float* sums = reinterpret_cast<float*>(gbase);
-                if constexpr (WIDE) {
+                if constexpr (WIDE && !BOTH) {
+                    // 16-byte units of a row, unit u of row i at u ^ (i & 7): a warp's stores meet no bank twice
+#pragma unroll
+                    for (int c = 0; c < CW; c += 4)
+                        *reinterpret_cast<ulonglong2*>(sums + (quad * 32 + lane) * C::kCols + (((first + c) >> 2) ^ (lane & 7)) * 4) =
+                            make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
+                } else if constexpr (WIDE) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -718,7 +783,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             tile_at(p, tile, pt, qt);
             const int p0 = pt * C::kRows + peer * kLanes + quad * 32, q0 = qt * C::kCols + first;
             if constexpr (WIDE) {
-                store_wide<CW>(p, acc, p0 + (lane >> 2), q0);
+                if constexpr (BOTH) store_wide<CW>(p, acc, p0 + (lane >> 2), q0);
+                else store_rows<CW>(p, acc, p0, q0, gbase + C::kOffOut + (warp - kOthers) * 4096);
             } else {
                 const int live = p0 + lane < p.p_rows ? p.q_rows - q0 : 0;
                 const int64_t at = (int64_t)q0 * p.ldd + p0 + lane;
@@ -742,10 +808,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         const int rows = min(kDRows, M - m0), share = (rows + p.shares - 1) / p.shares;
         const int begin = (int)rank * share, end = min(rows, begin + share);
         for (int i = begin * kDCols + (int)threadIdx.x; i < end * kDCols; i += C::kThreads) {
+            const uint32_t at = base + 4u * (WIDE && !BOTH ? i ^ (i / kDCols & 7) << 2 : i);
             float v[kMaxShares];
 #pragma unroll
-            for (int r = 0; r < kMaxShares; ++r)
-                v[r] = r < p.shares ? __int_as_float(ld_cluster(map_to_rank(base + 4u * i, r))) : 0.0f;
+            for (int r = 0; r < kMaxShares; ++r) v[r] = r < p.shares ? __int_as_float(ld_cluster(map_to_rank(at, r))) : 0.0f;
             float sum = v[0];
 #pragma unroll
             for (int r = 1; r < kMaxShares; ++r)
@@ -759,7 +825,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         // A wait gave up (both CTAs of a pair know): stages that were filled but not used may still be on their way into
         // either CTA.  They are waited for before any CTA leaves, with a limit, since a stage that only one of the
         // copiers filled never completes.
-        if (threadIdx.x == 0 && peer == 0) {
+        if (warp == 0 && peer == 0) {
             int most = stages_of[0];
             if (PAIR) most = max(most, ld_cluster(map_to_rank(base + C::kOffWords + 8, 1)));
             for (int i = stages_of[1]; i < most; ++i) mbar_wait(full_bar(i % S), (i / S) & 1, 0, kDrainLimit);
