@@ -6,9 +6,9 @@
 //
 // An fp32 scale cannot ride in a block-scaled MMA, whose scales are powers of
 // two (or E4M3).  So the tensor core sums one block of 128 at a time, in fp32,
-// into one of two buffers in tensor memory, and while it sums the next one into
-// the other, other warps read the finished block and add it, scaled, to fp32 sums
-// in registers.
+// into one of two to four buffers in tensor memory, and while it sums the next
+// ones, other warps read the finished block and add it, scaled, to fp32 sums in
+// registers.
 //
 // One operand's rows (P) lie along the lanes of tensor memory, the other's (Q)
 // along its columns; three shapes:
@@ -19,10 +19,11 @@
 // the large ones.  A block of a pair's tile is 512 cycles of the tensor core.
 // With square blocks of B a lane that holds a row needs one scale for 128 columns,
 // and the sums are read a row a lane, the layout that tensor memory reads fastest
-// (128 x 256 sums of an SM in about 155 cycles; 16 lanes x 256 bits: 512).  With
-// scales for the rows of either operand (WGRAD) every column has its own: brought
-// from shared memory to every lane that would be 1024 cycles, so the sums are read
-// 16 lanes x 256 bits, which gives a thread four rows and a quarter of the columns.
+// (128 x 256 sums of an SM in about 155 cycles; 16 lanes x 128 bits 260, x 256
+// bits 510).  With scales for the rows of either operand (WGRAD) every column has
+// its own: brought from shared memory to every lane that would be 1024 cycles, so the
+// sums are read 16 lanes x 128 bits, which gives a thread four rows and a quarter of
+// the columns.
 //
 // Few tokens (up to 64): P is B, Q is A, so that the tile is as wide as there
 // are tokens and the weights are read once.  A lane holds a row of B, and 32
@@ -79,11 +80,12 @@ struct Cfg {
     static constexpr int kOffScales = kStages * kStage;
     static constexpr int kOffOut = kOffScales + (kSlabs * kSlabFloats * 4 + 15) / 16 * 16;  // 4 KB for each scaling warp
     static constexpr int kOffBars = kOffOut + (WIDE ? 4 * GROUPS * 4096 : 0);
-    // full, done; partial sums read x2; slabs full, empty; drain
-    static constexpr int kNumBars = 2 * kStages + 2 + 2 * kSlabs + 1;
+    static constexpr int kBufs = PAIR ? 2 : 4;  // buffers of partial sums
+    // full, done; partial sums read; slabs full, empty; drain
+    static constexpr int kNumBars = 2 * kStages + kBufs + 2 * kSlabs + 1;
     static constexpr int kOffWords = kOffBars + 8 * kNumBars;  // tensor memory address, abort flag, stages filled and used
     static constexpr int kSmem = kOffWords + 16 + 1024;
-    static constexpr int kTmem = 2 * kCols;
+    static constexpr int kTmem = kBufs * kCols;
     static_assert(kTmem >= 32 && (kTmem & (kTmem - 1)) == 0 && kTmem <= 512, "tensor memory columns");
     static_assert(kSmem <= 232448, "shared memory overflow");
     static_assert(kCols * kLanes * 4 <= kStages * kStage, "a share's sums take the stages' place");
@@ -104,6 +106,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives once this thread's copies so far have landed.
+__device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ int ld_shared(uint32_t saddr) {
     int v;
@@ -267,16 +276,13 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&u)[16]) {
           "=r"(u[15])
         : "r"(taddr));
 }
-// ... or 64 columns of 16 lanes: r[4 j + e] is row lane / 4, r[4 j + 2 + e] row lane / 4 + 8, column 8 j + 2 (lane % 4) + e.
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&u)[32]) {
+// ... or 32 columns of 16 lanes: r[2 j] is row lane / 4, r[2 j + 1] row lane / 4 + 8, column 4 j + lane % 4.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&u)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
           "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]),
-          "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]),
-          "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]),
-          "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+          "=r"(u[15])
         : "r"(taddr));
 }
 // One lane of a whole warp.
@@ -347,72 +353,16 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A wide tile's sums of a warp that reads 16 lanes x 256 bits (rows row0 + 8 i, i = 0..3, of the lane's quad; pairs of columns 8 j + 2 (lane % 4), j = 0 ..
-// CW / 8 - 1, acc[i * CW / 8 + j]) into D.  bf16: four lanes turn four groups of 8 columns around, so that each stores 16
-// bytes, 64 of a row in a piece; fp32 pairs fill whole sectors as they are.
-template <int CW>
-__device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&acc)[CW / 2], int row0, int col0) {
-    const int q = threadIdx.x & 3;
-    const bool whole = col0 + CW <= p.q_rows && p.d_vec == 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = row0 + 8 * i;
-        const bool live = row < p.p_rows;
-        const int64_t at = (int64_t)row * p.ldd + col0;
-        const uint64_t* a = acc + i * (CW / 8);
-        if (whole && !p.d_f32) {
-#pragma unroll
-            for (int j = 0; j < CW / 8; j += 4) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = pack_bf16(a[j + k]);
-                // lane q ends with what the quad's lanes hold of group j + q
-#pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                    const uint32_t give = q & 1 ? v[k] : v[k + 1];
-                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-                    if (q & 1) v[k] = got;
-                    else v[k + 1] = got;
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t give = q & 2 ? v[k] : v[k + 2];
-                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 2);
-                    if (q & 2) v[k] = got;
-                    else v[k + 2] = got;
-                }
-                if (live) *reinterpret_cast<uint4*>((__nv_bfloat16*)p.d + at + 8 * (j + q)) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        } else if (live) {
-#pragma unroll
-            for (int j = 0; j < CW / 8; ++j) {
-                const int c = 8 * j + 2 * q;
-                float x, y;
-                up2(a[j], x, y);
-                if (whole) {
-                    float2* d = reinterpret_cast<float2*>((float*)p.d + at + c);
-                    if (p.accumulate) {
-                        const float2 o = *d;
-                        x = o.x + x;
-                        y = o.y + y;
-                    }
-                    *d = make_float2(x, y);
-                } else {
-                    if (col0 + c < p.q_rows) put(p, at + c, x);
-                    if (col0 + c + 1 < p.q_rows) put(p, at + c + 1, y);
-                }
-            }
-        }
-    }
-}
-
-// The same of a warp whose lanes hold a row each (row0 + lane; columns col0 on in order).  A lane's own stores would touch 32
-// rows at a time; instead 128 bytes of every row are turned around in `stage` (16-byte units, unit u of row i at u ^ (i & 7))
-// and stored four whole rows of them an instruction.
-template <int CW>
-__device__ __forceinline__ void store_rows(const Fp8Params& p, const uint64_t (&acc)[CW / 2], int row0, int col0,
+// The sums of a wide tile's warp: 32 rows by CW columns.  Where 128 rows of B share a scale a lane holds a row, acc[c / 2] two
+// of its columns; with scales for either's rows (BOTH) acc[h * CW / 4 + j] holds rows 16 h + lane / 4 and that + 8 of column 4 j
+// + lane % 4.
+//
+// Their stores from the registers would touch 32 rows, or 16 bytes, at a time; instead 128 bytes of every row are turned around in
+// `stage` (16-byte units, unit u of row i at u ^ (i & 7)) and stored four whole rows of them an instruction.
+template <bool BOTH, int CW>
+__device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&acc)[CW / 2], int row0, int col0,
                                            uint8_t* stage) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, q = lane & 3;
     if (col0 + CW <= p.q_rows && p.d_vec == 16) {
         uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
         auto flush = [&](int c, int bytes) {  // the stage holds columns col0 + c on
@@ -436,13 +386,31 @@ __device__ __forceinline__ void store_rows(const Fp8Params& p, const uint64_t (&
             }
             __syncwarp();
         };
+        // BOTH: the pair of rows of column 4 j + q, the j-th four of the 128 bytes (all rows are lane / 4 modulo 8)
+        auto put_pair = [&](int h, int j, int bytes, uint64_t v) {
+            float x, y;
+            up2(v, x, y);
+            uint8_t* at = stage + (16 * h + (lane >> 2)) * 128 + (((j * bytes) >> 2) ^ (lane >> 2)) * 16;
+            if (bytes == 4) {
+                reinterpret_cast<float*>(at)[q] = x;
+                reinterpret_cast<float*>(at + 8 * 128)[q] = y;
+            } else {
+                reinterpret_cast<__nv_bfloat16*>(at)[4 * (j & 1) + q] = __float2bfloat16_rn(x);
+                reinterpret_cast<__nv_bfloat16*>(at + 8 * 128)[4 * (j & 1) + q] = __float2bfloat16_rn(y);
+            }
+        };
         if (p.d_f32) {
 #pragma unroll
             for (int c = 0; c < CW; c += 32) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const uint64_t x = acc[c / 2 + 2 * u], y = acc[c / 2 + 2 * u + 1];
-                    mine[u ^ (lane & 7)] = make_uint4((uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32));
+                    if (BOTH) {
+                        put_pair(0, u, 4, acc[c / 4 + u]);
+                        put_pair(1, u, 4, acc[CW / 4 + c / 4 + u]);
+                    } else {
+                        const uint64_t x = acc[c / 2 + 2 * u], y = acc[c / 2 + 2 * u + 1];
+                        mine[u ^ (lane & 7)] = make_uint4((uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32));
+                    }
                 }
                 flush(c, 4);
             }
@@ -451,17 +419,28 @@ __device__ __forceinline__ void store_rows(const Fp8Params& p, const uint64_t (&
             for (int c = 0; c < CW; c += 64) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const uint64_t* a = acc + c / 2 + 4 * u;
-                    mine[u ^ (lane & 7)] = make_uint4(pack_bf16(a[0]), pack_bf16(a[1]), pack_bf16(a[2]), pack_bf16(a[3]));
+                    if (BOTH) {
+#pragma unroll
+                        for (int j = 2 * u; j < 2 * u + 2; ++j) {
+                            put_pair(0, j, 2, acc[c / 4 + j]);
+                            put_pair(1, j, 2, acc[CW / 4 + c / 4 + j]);
+                        }
+                    } else {
+                        const uint64_t* a = acc + c / 2 + 4 * u;
+                        mine[u ^ (lane & 7)] = make_uint4(pack_bf16(a[0]), pack_bf16(a[1]), pack_bf16(a[2]), pack_bf16(a[3]));
+                    }
                 }
                 flush(c, 2);
             }
         }
-    } else if (row0 + lane < p.p_rows) {
-        const int64_t at = (int64_t)(row0 + lane) * p.ldd + col0;
+        return;
+    }
+    // ragged or unaligned columns
 #pragma unroll
-        for (int c = 0; c < CW; ++c)
-            if (col0 + c < p.q_rows) put(p, at + c, column(acc, c));
+    for (int i = 0; i < CW; ++i) {
+        const int row = row0 + (BOTH ? 16 * (i / (CW / 2)) + 8 * (i & 1) + (lane >> 2) : lane);
+        const int col = col0 + (BOTH ? 4 * (i % (CW / 2) / 2) + q : i);
+        if (row < p.p_rows && col < p.q_rows) put(p, (int64_t)row * p.ldd + col, column(acc, i));
     }
 }
 
@@ -482,9 +461,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto done_bar = [&](int s) { return bars + 8u * (S + s); };
     auto read_bar = [&](int b) { return bars + 8u * (2 * S + b); };
-    auto slabf_bar = [&](int i) { return bars + 8u * (2 * S + 2 + i); };
-    auto slabe_bar = [&](int i) { return bars + 8u * (2 * S + 2 + kSlabs + i); };
-    const uint32_t drain_bar = bars + 8u * (2 * S + 2 + 2 * kSlabs);
+    auto slabf_bar = [&](int i) { return bars + 8u * (2 * S + C::kBufs + i); };
+    auto slabe_bar = [&](int i) { return slabf_bar(kSlabs + i); };
+    const uint32_t drain_bar = slabf_bar(2 * kSlabs);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffWords);
     const uint32_t abort_flag = base + C::kOffWords + 4;
     volatile int* stages_of = reinterpret_cast<volatile int*>(gbase + C::kOffWords + 8);  // filled, used
@@ -505,7 +484,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             mbar_init(full_bar(s), 1);  // the leader's expect_tx arrival (both CTAs' bytes)
             mbar_init(done_bar(s), 1);  // the leader's commit: the stage may be filled, its sums be read
         }
-        for (int b = 0; b < 2; ++b) mbar_init(read_bar(b), (PAIR ? 2 : 1) * 4 * GROUPS);  // every scaling warp
+        for (int b = 0; b < C::kBufs; ++b) mbar_init(read_bar(b), (PAIR ? 2 : 1) * 4 * GROUPS);  // every scaling warp
         for (int i = 0; i < kSlabs; ++i) {
             mbar_init(slabf_bar(i), kLoaders);
             mbar_init(slabe_bar(i), 4 * GROUPS);
@@ -572,11 +551,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             const bool acts = elect_one();
             constexpr uint32_t idesc = make_idesc(C::kRows, C::kCols);
             int s = 0, stages = 0;
-            uint32_t ph = 0, t = 0;  // t: blocks so far, buffer t & 1
+            uint32_t ph = 0, t = 0;  // t: blocks so far, buffer t % kBufs
             bool ok = true;
             for (int tile = cluster_id; tile < num_tiles && ok; tile += num_clusters) {
                 for (int kb = 0; kb < k_blocks; ++kb) {
-                    ok = mbar_wait(full_bar(s), ph, 0, p.wait_limit) && mbar_wait(read_bar(t & 1), (t >> 1 & 1) ^ 1u, abort_flag);
+                    ok = mbar_wait(full_bar(s), ph, 0, p.wait_limit) && mbar_wait(read_bar(t % C::kBufs), (t / C::kBufs & 1) ^ 1u, abort_flag);
                     if (!ok) break;
                     ++stages;
                     tc_fence_after();
@@ -584,7 +563,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         const uint64_t dp = sw128_desc(base + s * C::kStage), dq = sw128_desc(base + s * C::kStage + kAtom);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)  // 32 bytes of the summed index each
-                            mma<PAIR>(tmem + (t & 1) * C::kCols, dp + 2 * i, dq + 2 * i, idesc, i > 0 ? 1u : 0u);
+                            mma<PAIR>(tmem + t % C::kBufs * C::kCols, dp + 2 * i, dq + 2 * i, idesc, i > 0 ? 1u : 0u);
                         tc_commit<PAIR>(done_bar(s));
                     }
                     ++t;
@@ -602,12 +581,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         } else if (warp >= 2) {
             // ---------------------------------------------------- scales
             // A slab is the scales of up to kSlab blocks: those of the tile's columns and of the CTA's rows, each block's apart.
-            // A thread takes one block, and every 16th column or row, and loads them before the slab is free.  What lies past
-            // the operands is read at their edge instead; nothing looks at it.
+            // A thread takes one block, and every 16th column or row.  What lies past the operands is read at their edge
+            // instead; nothing looks at it.  Few of them are loaded before the slab is free; where every row and every column
+            // has its own, which is more than a thread's registers hold, they are copied straight into it.
             const int tid = threadIdx.x - 64;
             const int kk = tid & (kSlab - 1), each = tid >> 2;
             constexpr bool kOfCols = !WIDE || BOTH;  // every column its scale; otherwise one for each 128
-            constexpr bool kOfRows = WIDE || BOTH;   // every row its scale; otherwise in the columns'
+            constexpr bool kOfRows = WIDE || BOTH;   // every row its scale; otherwise one, which is multiplied into the columns'
+            constexpr bool kCopied = WIDE && BOTH;
             constexpr int kC = kOfCols ? C::kCols / 16 : 1, kR = kOfRows ? kLanes / 16 : 1;
             uint32_t u = 0;
             bool ok = true;
@@ -619,32 +600,44 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                     const int64_t b = min(k0 + kb + kk, p.blocks - 1);
                     const float* sp = p.sp + b;
                     const float* sq = p.sq + b;
-                    float v[kC], w[kR];
-#pragma unroll
-                    for (int j = 0; j < kC; ++j) {
+                    auto of_p = [&](int j) {
+                        return sp + (int64_t)(min(p0 + (kOfRows ? each + 16 * j : 0), p.p_rows - 1) >> p.p_shift) * p.ld_sp;
+                    };
+                    auto of_q = [&](int j) {
                         const int r = kOfCols ? each + 16 * j : min(each * 128, C::kCols - 1);
-                        v[j] = sq[(int64_t)(min(q0 + r, p.q_rows - 1) >> p.q_shift) * p.ld_sq];
-                    }
+                        return sq + (int64_t)(min(q0 + r, p.q_rows - 1) >> p.q_shift) * p.ld_sq;
+                    };
+                    float v[kC], w[kR];
+                    if (!kCopied) {
 #pragma unroll
-                    for (int j = 0; j < kR; ++j) {
-                        const int r = kOfRows ? each + 16 * j : 0;
-                        w[j] = sp[(int64_t)(min(p0 + r, p.p_rows - 1) >> p.p_shift) * p.ld_sp];
+                        for (int j = 0; j < kC; ++j) v[j] = *of_q(j);
+#pragma unroll
+                        for (int j = 0; j < kR; ++j) w[j] = *of_p(j);
                     }
                     ok = mbar_wait(slabe_bar(u % kSlabs), (u / kSlabs & 1) ^ 1u, abort_flag);
                     if (!ok) break;
                     float* cols = reinterpret_cast<float*>(gbase + C::kOffScales) + (u % kSlabs) * C::kSlabFloats +
                                   kk * C::kColPitch + each;
                     float* rows = cols + (kSlab - kk) * C::kColPitch + kk * C::kRowPitch;
+                    if (kCopied) {
+#pragma unroll 2
+                        for (int j = 0; j < kC; ++j) copy4(smem_u32(cols) + 64 * j, of_q(j));
+#pragma unroll 2
+                        for (int j = 0; j < kR; ++j) copy4(smem_u32(rows) + 64 * j, of_p(j));
+                        mbar_arrive_copies(slabf_bar(u % kSlabs));
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < kC; ++j) cols[16 * j] = kOfRows ? v[j] : v[j] * w[0];
-                    if (kOfRows) {
+                        for (int j = 0; j < kC; ++j) cols[16 * j] = kOfRows ? v[j] : v[j] * w[0];
+                        if (kOfRows) {
 #pragma unroll
-                        for (int j = 0; j < kR; ++j) rows[16 * j] = w[j];
+                            for (int j = 0; j < kR; ++j) rows[16 * j] = w[j];
+                        }
+                        mbar_arrive(slabf_bar(u % kSlabs));
                     }
-                    mbar_arrive(slabf_bar(u % kSlabs));
                 }
             }
             if (!ok) give_up();
+            if (kCopied) asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         // ------------------------------------------------- scaling and adding
@@ -654,7 +647,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         const uint32_t slabs = base + C::kOffScales;
         const uint32_t read = PAIR ? map_to_rank(read_bar(0), 0) : read_bar(0);  // the issuer's
         const uint32_t own_row = (kSlab * C::kColPitch + quad * 32 + (WIDE && BOTH ? lane >> 2 : lane)) * 4;
-        uint32_t t = 0, u = 0;  // blocks and slabs so far: buffer t & 1, slab u % kSlabs
+        uint32_t t = 0, u = 0;  // blocks and slabs so far: buffer t % kBufs, slab u % kSlabs
         int s = 0;              // stage of block t
         uint32_t ph = 0;
         bool ok = true;
@@ -671,13 +664,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 tc_fence_after();
                 const uint32_t slab = slabs + (u % kSlabs) * (C::kSlabFloats * 4);
                 const uint32_t cols = slab + (kk * C::kColPitch + first) * 4;
-                const uint32_t at = from + (t & 1) * C::kCols;
+                const uint32_t at = from + t % C::kBufs * C::kCols;
                 auto release = [&] {  // the buffer has been read and may be filled again
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(read + 8u * (t & 1));
-                        else mbar_arrive(read + 8u * (t & 1));
+                        if (PAIR) mbar_arrive_cluster(read + 8u * (t % C::kBufs));
+                        else mbar_arrive(read + 8u * (t % C::kBufs));
                     }
                 };
                 const uint32_t rows = slab + own_row + kk * C::kRowPitch * 4;
@@ -694,28 +687,24 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         for (int j = 0; j < 16; ++j) acc[c / 2 + j] = fma2(pair(r[2 * j], r[2 * j + 1]), s2, acc[c / 2 + j]);
                     }
                 } else if constexpr (WIDE) {
-                    uint64_t rs[4];  // the scales of the lane's rows
+                    uint64_t rs[2];  // the scales of the lane's pairs of rows
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = ld_shared_f(rows + 32 * i);
-                        rs[i] = pk2(v, v);
-                    }
-                    // 64 columns of 16 rows at a time
+                    for (int h = 0; h < 2; ++h) rs[h] = pk2(ld_shared_f(rows + 64 * h), ld_shared_f(rows + 64 * h + 32));
 #pragma unroll
-                    for (int c = 0; c < CW / 32; ++c) {
-                        const int half = c & 1, col = (c >> 1) * 64;
-                        uint32_t r[32];
-                        tmem_ld_rows(at + col + ((uint32_t)half << 20), r);
-                        tmem_wait(r);
-                        if (c + 1 == CW / 32) release();
+                    for (int c = 0; c < CW; c += 32) {
+                        float wv[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint64_t w2 = ld_shared_pair(cols + (col + 8 * j + 2 * (lane & 3)) * 4);
+                        for (int j = 0; j < 8; ++j) wv[j] = ld_shared_f(cols + (c + 4 * j + (lane & 3)) * 4);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint64_t x = pair(r[4 * j + 2 * i], r[4 * j + 2 * i + 1]);
-                                uint64_t& a = acc[(2 * half + i) * (CW / 8) + col / 8 + j];
-                                a = fma2(mul2(x, w2), rs[2 * half + i], a);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[16];
+                            tmem_ld_rows(at + c + ((uint32_t)h << 20), r);
+                            tmem_wait(r);
+                            if (c + 32 == CW && h == 1) release();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                uint64_t& a = acc[h * (CW / 4) + c / 4 + j];
+                                a = fma2(mul2(pair(r[2 * j], r[2 * j + 1]), pk2(wv[j], wv[j])), rs[h], a);
                             }
                         }
                     }
@@ -766,13 +755,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                             make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
                 } else if constexpr (WIDE) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < CW / 8; ++j) {
-                            const int row = quad * 32 + 8 * i + (lane >> 2);
-                            *reinterpret_cast<uint64_t*>(sums + row * C::kCols + first + 8 * j + 2 * (lane & 3)) =
-                                acc[i * (CW / 8) + j];
-                        }
+                    for (int i = 0; i < CW; ++i) {
+                        const int row = quad * 32 + 16 * (i / (CW / 2)) + 8 * (i & 1) + (lane >> 2);
+                        const int col = first + 4 * (i % (CW / 2) / 2) + (lane & 3);
+                        sums[row * C::kCols + (col ^ (row & 7) << 2)] = column(acc, i);
+                    }
                 } else {
 #pragma unroll
                     for (int c = 0; c < CW; ++c) sums[(first + c) * kLanes + quad * 32 + lane] = column(acc, c);
@@ -783,8 +770,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             tile_at(p, tile, pt, qt);
             const int p0 = pt * C::kRows + peer * kLanes + quad * 32, q0 = qt * C::kCols + first;
             if constexpr (WIDE) {
-                if constexpr (BOTH) store_wide<CW>(p, acc, p0 + (lane >> 2), q0);
-                else store_rows<CW>(p, acc, p0, q0, gbase + C::kOffOut + (warp - kOthers) * 4096);
+                store_wide<BOTH, CW>(p, acc, p0, q0, gbase + C::kOffOut + (warp - kOthers) * 4096);
             } else {
                 const int live = p0 + lane < p.p_rows ? p.q_rows - q0 : 0;
                 const int64_t at = (int64_t)q0 * p.ldd + p0 + lane;
@@ -808,7 +794,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         const int rows = min(kDRows, M - m0), share = (rows + p.shares - 1) / p.shares;
         const int begin = (int)rank * share, end = min(rows, begin + share);
         for (int i = begin * kDCols + (int)threadIdx.x; i < end * kDCols; i += C::kThreads) {
-            const uint32_t at = base + 4u * (WIDE && !BOTH ? i ^ (i / kDCols & 7) << 2 : i);
+            const uint32_t at = base + 4u * (WIDE ? i ^ (i / kDCols & 7) << 2 : i);
             float v[kMaxShares];
 #pragma unroll
             for (int r = 0; r < kMaxShares; ++r) v[r] = r < p.shares ? __int_as_float(ld_cluster(map_to_rank(at, r))) : 0.0f;
@@ -843,21 +829,49 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
 // By how much the polls of a stage's arrival are lowered, per device.
 std::atomic<uint32_t> g_lowered[64];
 
-// Clusters of the pairs' kernel that fit the device at once.
-template <bool BOTH>
-int max_pairs(int dev, const cudaLaunchConfig_t& cfg) {
-    static DeviceFigure clusters;
-    return clusters.get(dev, [&] {
+// Clusters of `ctas` CTAs (up to kMaxShares) that fit the device at once.
+template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
+int max_clusters(int dev, int ctas) {
+    using C = Cfg<WIDE, PAIR, CW, GROUPS>;
+    static DeviceFigure clusters[kMaxShares];
+    return clusters[ctas - 1].get(dev, [&] {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(C::kThreads);
+        cfg.dynamicSmemBytes = C::kSmem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)ctas;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
         int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<true, true, BOTH, 128, 2>, &cfg) == cudaSuccess ? n : 0;
+        return cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<WIDE, PAIR, BOTH, CW, GROUPS>, &cfg) == cudaSuccess ? n : 0;
     });
 }
 
+// Shares of the summed index, for tiles of which each cluster computes one: the fewest blocks in a row, with two blocks' time
+// for a round of tiles and its join.
+template <bool BOTH, bool WIDE, int CW, int GROUPS>
+int best_shares(int dev, int64_t tiles, int64_t blocks) {
+    int shares = 1;
+    int64_t best = 1ll << 60;
+    for (int s = 1; s <= kMaxShares && s <= blocks; ++s) {
+        const int64_t room = max_clusters<WIDE, false, BOTH, CW, GROUPS>(dev, s);
+        if (room <= 0) continue;
+        const int64_t cost = (tiles + room - 1) / room * ((blocks + s - 1) / s + 2);
+        if (cost < best) {
+            best = cost;
+            shares = s;
+        }
+    }
+    return shares;
+}
+
 template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
-cudaError_t run(const Fp8GemmArgs& a, int shares, cudaStream_t st) {
+cudaError_t run(const Fp8GemmArgs& a, int dev, cudaStream_t st) {
     using C = Cfg<WIDE, PAIR, CW, GROUPS>;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     const Fp8Operand &op = WIDE ? a.a : a.b, &oq = WIDE ? a.b : a.a;
     const int64_t p_rows = WIDE ? a.M : a.N, q_rows = WIDE ? a.N : a.M;
     Fp8Params p = {};
@@ -867,7 +881,10 @@ cudaError_t run(const Fp8GemmArgs& a, int shares, cudaStream_t st) {
     p.p_tiles = (int)((p_rows + C::kRows - 1) / C::kRows);
     p.q_tiles = (int)((q_rows + C::kCols - 1) / C::kCols);
     p.group = kGroup;
-    p.shares = PAIR ? 1 : shares;
+    const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
+    int shares = 1;
+    if constexpr (!PAIR) shares = best_shares<BOTH, WIDE, CW, GROUPS>(dev, tiles, p.blocks);
+    p.shares = shares;
     p.per = (p.blocks + p.shares - 1) / p.shares;
     p.q_box = WIDE ? C::kQRows : (int)std::min<int64_t>(C::kQRows, (q_rows + 7) / 8 * 8);
     p.wait_limit = kWaitLimit - g_lowered[dev].load(std::memory_order_relaxed);
@@ -902,10 +919,8 @@ cudaError_t run(const Fp8GemmArgs& a, int shares, cudaStream_t st) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
     if (PAIR) {
-        const int most = max_pairs<BOTH>(dev, cfg);
+        const int most = max_clusters<WIDE, PAIR, BOTH, CW, GROUPS>(dev, 2);
         if (most <= 0) return cudaErrorLaunchOutOfResources;
         cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, most));
     } else {
@@ -915,33 +930,16 @@ cudaError_t run(const Fp8GemmArgs& a, int shares, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k, mp, mq, p);
 }
 
-// Shares of the summed index: the fewest blocks for the busiest SM, of which each holds `room` CTAs.
-int best_shares(int64_t tiles, int64_t blocks, int64_t room) {
-    int shares = 1;
-    int64_t best = 1ll << 60;
-    for (int s = 1; s <= kMaxShares && s <= blocks; ++s) {
-        const int64_t rounds = (tiles * s + room - 1) / room;
-        const int64_t cost = rounds * ((blocks + s - 1) / s + 2);
-        if (cost < best) {
-            best = cost;
-            shares = s;
-        }
-    }
-    return shares;
-}
-
 template <bool BOTH>
 cudaError_t launch(const Fp8GemmArgs& a, int num_sms, cudaStream_t st) {
-    const int64_t blocks = (a.K + kStep - 1) / kStep, lanes = (a.N + kLanes - 1) / kLanes;
-    if (a.M <= 64) {
-        const int shares = best_shares(lanes, blocks, 2 * (int64_t)num_sms);
-        if (a.M <= 16) return run<false, false, BOTH, 16, 1>(a, shares, st);
-        if (a.M <= 32) return run<false, false, BOTH, 32, 1>(a, shares, st);
-        return run<false, false, BOTH, 64, 1>(a, shares, st);
-    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (a.M <= 16) return run<false, false, BOTH, 16, 1>(a, dev, st);
+    if (a.M <= 32) return run<false, false, BOTH, 32, 1>(a, dev, st);
+    if (a.M <= 64) return run<false, false, BOTH, 64, 1>(a, dev, st);
     const int64_t pair_tiles = (a.M + 255) / 256 * ((a.N + 255) / 256);
-    if (pair_tiles >= num_sms / 4) return run<true, true, BOTH, 128, 2>(a, 1, st);
-    return run<true, false, BOTH, 64, 2>(a, best_shares((a.M + 127) / 128 * lanes, blocks, num_sms), st);
+    if (pair_tiles >= num_sms / 4) return run<true, true, BOTH, 128, 2>(a, dev, st);
+    return run<true, false, BOTH, 64, 2>(a, dev, st);
 }
 
 template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
