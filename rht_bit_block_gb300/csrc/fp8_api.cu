@@ -78,7 +78,8 @@ ufp4_status ufp4_fp8_gemm(const ufp4_qtensor* A, int32_t a_block_rows, const ufp
     a.ldd = ldd;
     a.d_f32 = d_dtype == UFP4_F32;
     a.accumulate = accumulate;
-    return to_status(launch_fp8_gemm(a, current_num_sms(), stream));
+    current_num_sms();  // loads the kernels
+    return to_status(launch_fp8_gemm(a, stream));
 }
 
 }  // extern "C"

@@ -179,6 +179,14 @@ __device__ __forceinline__ int ld_cluster(uint32_t caddr) {
     asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
     return v;
 }
+__device__ __forceinline__ float4 ld_cluster4(uint32_t caddr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(caddr)
+                 : "memory");
+    return v;
+}
 // TMA box into this CTA's shared memory, counted on a barrier of either CTA of a pair.
 template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t cbar) {
@@ -341,6 +349,28 @@ __device__ __forceinline__ void put(const Fp8Params& p, int64_t at, float v) {
         ((__nv_bfloat16*)p.d)[at] = __float2bfloat16_rn(v);
     }
 }
+// Four neighbouring results, of which `live` exist.
+__device__ __forceinline__ void put4(const Fp8Params& p, int64_t at, float4 v, int live) {
+    if (live >= 4 && p.d_vec == 16) {
+        if (p.d_f32) {
+            float4* d = reinterpret_cast<float4*>((float*)p.d + at);
+            if (p.accumulate) {
+                const float4 o = *d;
+                v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+            }
+            *d = v;
+        } else {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2*>((__nv_bfloat16*)p.d + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        }
+        return;
+    }
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < live) put(p, at + i, f[i]);
+}
 __device__ __forceinline__ float column(const uint64_t* acc, int c) {
     float x, y;
     up2(acc[c >> 1], x, y);
@@ -448,7 +478,7 @@ __device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&
 // MMAs, warps 2 and 3 lay out the scales, the rest scale and add.  BOTH: the
 // rows of either operand have scales of their own; otherwise 128 rows of B share one.
 template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
-__global__ void __launch_bounds__((Cfg<WIDE, PAIR, CW, GROUPS>::kThreads), 1)
+__global__ void __launch_bounds__((Cfg<WIDE, PAIR, CW, GROUPS>::kThreads), WIDE ? 1 : 2)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                 const __grid_constant__ Fp8Params p) {
     using C = Cfg<WIDE, PAIR, CW, GROUPS>;
@@ -478,6 +508,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     // this CTA's share of the summed index
     const int k0 = PAIR ? 0 : (int)rank * p.per;
     const int k_blocks = PAIR ? p.blocks : max(0, min(p.per, p.blocks - k0));
+    // Where each cluster has one tile they all walk the blocks at the same pace, and the tiles of a few tokens are what many
+    // of them read: each starts at a block of its own and comes round, or the few lines of the block they share keep them
+    // waiting (256 x 7168 x 7168 on single tiles: 46 us).
+    const int turn = num_tiles <= num_clusters ? (int)((int64_t)cluster_id * k_blocks / num_tiles) : 0;
+    auto block_at = [&](int i) { return k0 + i + turn - (i + turn >= k_blocks ? k_blocks : 0); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -534,8 +569,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                     if (acts) {
                         if (peer == 0) mbar_expect_tx(full_bar(s), tx);
                         const uint32_t dst = base + s * C::kStage;
-                        tma_load<PAIR>(dst, &map_p, (k0 + kb) * kStep, prow, remote + 8u * s);
-                        tma_load<PAIR>(dst + kAtom, &map_q, (k0 + kb) * kStep, qrow, remote + 8u * s);
+                        tma_load<PAIR>(dst, &map_p, block_at(kb) * kStep, prow, remote + 8u * s);
+                        tma_load<PAIR>(dst + kAtom, &map_q, block_at(kb) * kStep, qrow, remote + 8u * s);
                     }
                     __syncwarp();
                     if (++s == S) {
@@ -597,7 +632,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 tile_at(p, tile, pt, qt);
                 const int p0 = pt * C::kRows + peer * kLanes, q0 = qt * C::kCols;
                 for (int kb = 0; kb < k_blocks; kb += kSlab, ++u) {
-                    const int64_t b = min(k0 + kb + kk, p.blocks - 1);
+                    const int64_t b = block_at(min(kb + kk, k_blocks - 1));
                     const float* sp = p.sp + b;
                     const float* sq = p.sq + b;
                     auto of_p = [&](int j) {
@@ -793,17 +828,19 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         const int M = WIDE ? p.p_rows : p.q_rows, N = WIDE ? p.q_rows : p.p_rows;
         const int rows = min(kDRows, M - m0), share = (rows + p.shares - 1) / p.shares;
         const int begin = (int)rank * share, end = min(rows, begin + share);
-        for (int i = begin * kDCols + (int)threadIdx.x; i < end * kDCols; i += C::kThreads) {
-            const uint32_t at = base + 4u * (WIDE ? i ^ (i / kDCols & 7) << 2 : i);
-            float v[kMaxShares];
+        constexpr int kUnits = kDCols / 4;  // of four neighbouring results
+        for (int i = begin * kUnits + (int)threadIdx.x; i < end * kUnits; i += C::kThreads) {
+            const int row = i / kUnits, unit = i % kUnits;
+            const uint32_t at = base + 16u * (row * kUnits + (WIDE ? unit ^ (row & 7) : unit));
+            float4 v[kMaxShares];
 #pragma unroll
-            for (int r = 0; r < kMaxShares; ++r) v[r] = r < p.shares ? __int_as_float(ld_cluster(map_to_rank(at, r))) : 0.0f;
-            float sum = v[0];
+            for (int r = 0; r < kMaxShares; ++r)
+                if (r < p.shares) v[r] = ld_cluster4(map_to_rank(at, r));
+            float4 sum = v[0];
 #pragma unroll
             for (int r = 1; r < kMaxShares; ++r)
-                if (r < p.shares) sum += v[r];
-            const int n = n0 + i % kDCols;
-            if (n < N) put(p, (int64_t)(m0 + i / kDCols) * p.ldd + n, sum);
+                if (r < p.shares) sum = make_float4(sum.x + v[r].x, sum.y + v[r].y, sum.z + v[r].z, sum.w + v[r].w);
+            put4(p, (int64_t)(m0 + row) * p.ldd + n0 + 4 * unit, sum, N - (n0 + 4 * unit));
         }
         cluster_sync_all();  // no CTA leaves while another reads its sums
     }
@@ -851,22 +888,27 @@ int max_clusters(int dev, int ctas) {
     });
 }
 
-// Shares of the summed index, for tiles of which each cluster computes one: the fewest blocks in a row, with two blocks' time
-// for a round of tiles and its join.
+// Shares of the summed index, for tiles of which each cluster computes one: the fewest blocks in a row, with kRound blocks' time
+// for a round of tiles (its start, its first copies and its join).  (768 x 7168 x 7168 on singles: 73 us with 10, 58 with 20.)
+constexpr int kRound = 20;
+struct Shared {
+    int shares;
+    int64_t rounds, per;  // of tiles, and blocks of each
+};
 template <bool BOTH, bool WIDE, int CW, int GROUPS>
-int best_shares(int dev, int64_t tiles, int64_t blocks) {
-    int shares = 1;
-    int64_t best = 1ll << 60;
+Shared best_shares(int dev, int64_t tiles, int64_t blocks) {
+    Shared b = {1, tiles, blocks};
+    int64_t least = 1ll << 60;
     for (int s = 1; s <= kMaxShares && s <= blocks; ++s) {
         const int64_t room = max_clusters<WIDE, false, BOTH, CW, GROUPS>(dev, s);
         if (room <= 0) continue;
-        const int64_t cost = (tiles + room - 1) / room * ((blocks + s - 1) / s + 2);
-        if (cost < best) {
-            best = cost;
-            shares = s;
+        const int64_t rounds = (tiles + room - 1) / room, per = (blocks + s - 1) / s, cost = rounds * (per + kRound);
+        if (cost < least) {
+            least = cost;
+            b = {s, rounds, per};
         }
     }
-    return shares;
+    return b;
 }
 
 template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
@@ -883,7 +925,7 @@ cudaError_t run(const Fp8GemmArgs& a, int dev, cudaStream_t st) {
     p.group = kGroup;
     const int64_t tiles = (int64_t)p.p_tiles * p.q_tiles;
     int shares = 1;
-    if constexpr (!PAIR) shares = best_shares<BOTH, WIDE, CW, GROUPS>(dev, tiles, p.blocks);
+    if constexpr (!PAIR) shares = best_shares<BOTH, WIDE, CW, GROUPS>(dev, tiles, p.blocks).shares;
     p.shares = shares;
     p.per = (p.blocks + p.shares - 1) / p.shares;
     p.q_box = WIDE ? C::kQRows : (int)std::min<int64_t>(C::kQRows, (q_rows + 7) / 8 * 8);
@@ -931,14 +973,20 @@ cudaError_t run(const Fp8GemmArgs& a, int dev, cudaStream_t st) {
 }
 
 template <bool BOTH>
-cudaError_t launch(const Fp8GemmArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (a.M <= 16) return run<false, false, BOTH, 16, 1>(a, dev, st);
     if (a.M <= 32) return run<false, false, BOTH, 32, 1>(a, dev, st);
     if (a.M <= 64) return run<false, false, BOTH, 64, 1>(a, dev, st);
-    const int64_t pair_tiles = (a.M + 255) / 256 * ((a.N + 255) / 256);
-    if (pair_tiles >= num_sms / 4) return run<true, true, BOTH, 128, 2>(a, dev, st);
+    // Measured: a block takes 0.33 us of a single tile and 0.475 of a pair's (0.40 and 0.68 with scales for the rows of both
+    // operands), a round of singles 3.3 us more, a pair's kernel 2.6.  256 x 7168 x 7168: singles 20.9 us, pairs 27.8; 512: 45.5
+    // and 28.7; 768 x 2816 x 2048: 8.9 and 11.7; 1024: 16.8 and 12.4.
+    const int64_t blocks = (a.K + kStep - 1) / kStep;
+    const int64_t pairs = std::max(1, max_clusters<true, true, BOTH, 128, 2>(dev, 2));
+    const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256), rounds = (tiles + pairs - 1) / pairs;
+    const Shared s = best_shares<BOTH, true, 64, 2>(dev, (a.M + kLanes - 1) / kLanes * ((a.N + kLanes - 1) / kLanes), blocks);
+    if ((rounds * blocks + 6) * (BOTH ? 17 : 14) <= s.rounds * (s.per + 10) * 10) return run<true, true, BOTH, 128, 2>(a, dev, st);
     return run<true, false, BOTH, 64, 2>(a, dev, st);
 }
 
@@ -958,8 +1006,8 @@ cudaError_t preload_all() {
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, int num_sms, cudaStream_t st) {
-    return a.b_square ? launch<false>(a, num_sms, st) : launch<true>(a, num_sms, st);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
+    return a.b_square ? launch<false>(a, st) : launch<true>(a, st);
 }
 
 cudaError_t fp8_error_read_clear(int* value) {

@@ -126,7 +126,7 @@ struct Fp8GemmArgs {
     int64_t ldd;
     bool d_f32, accumulate;
 };
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
 cudaError_t fp8_error_read_clear(int* value);
 // Polls of a stage's arrival before the product gives up, up to its default.
 cudaError_t set_fp8_wait_limit(uint32_t polls);
