@@ -41,20 +41,70 @@ struct Scale {
     float s, inv;
     bool bad;  // not finite
 };
-// The scale of a block whose largest magnitude has bit pattern m.
+// The scale of a block whose largest magnitude has bit pattern m.  M / 448 is M / 7 (div_known_rn, correctly rounded) times
+// 2^-6, which is exact down to the least scale.
 __device__ __forceinline__ Scale make_scale(uint32_t m) {
     Scale q;
-    q.s = __fdiv_rn(__uint_as_float(m), 448.0f);
     q.bad = m >= 0x7F800000u;
-    if (!q.bad) q.s = fmaxf(q.s, 1.17549435e-38f);
-    q.inv = q.bad ? __uint_as_float(0x7FFFFFFFu) : __frcp_rn(q.s);  // NaN: every code of the block becomes 0x7F or 0xFF
+    q.s = q.bad ? __uint_as_float(m) : fmaxf(div_known_rn(__uint_as_float(m), 7.0f, 0x1.24924ap-3f) * 0.015625f, 0x1p-126f);
+    q.inv = __frcp_rn(q.s);  // of a block that is not finite unused
     return q;
 }
-// Four codes of values times the reciprocal scale; zeros as +0, NaN as 0x7F.
+// Four codes of values times the reciprocal scale; zeros as +0.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, uint64_t inv2) {
     return ckpt_pack4(mul2(pk2(a, b), inv2), mul2(pk2(c, d), inv2));
 }
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// N neighbouring elements of a row as they are read (two bf16 a word, or an fp32).  Magnitudes order like integers, a NaN's
+// above an infinity's, so that maxima are taken of the bit patterns, of two bf16 at once.
+template <bool F32, int N>
+struct Elems {
+    static constexpr int kWords = F32 ? N : N / 2;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const void* p) {  // aligned to the vector
+        if (kWords == 2) {
+            const uint2 a = __ldcs((const uint2*)p);
+            w[0] = a.x;
+            w[1] = a.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 a = __ldcs((const uint4*)p + i / 4);
+                w[i] = a.x;
+                w[i + 1] = a.y;
+                w[i + 2] = a.z;
+                w[i + 3] = a.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void load(const void* p, int n) {  // the first n, zeros after
+        zero();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) {
+                if (F32) w[i] = ((const uint32_t*)p)[i];
+                else w[i / 2] |= (uint32_t)((const uint16_t*)p)[i] << (16 * (i & 1));
+            }
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if (F32) return __uint_as_float(w[i]);
+        return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+    __device__ __forceinline__ uint32_t codes(int i, uint64_t inv2) const { return codes4(at(i), at(i + 1), at(i + 2), at(i + 3), inv2); }
+    static constexpr uint32_t kMagnitude = F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return F32 ? max(a, b) : __vmaxu2(a, b); }
+    // The largest magnitude of all, as a float's bit pattern.
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = w[0] & kMagnitude;
+#pragma unroll
+        for (int i = 1; i < kWords; ++i) m = larger(m, w[i] & kMagnitude);
+        return F32 ? m : max(m << 16, m & 0xFFFF0000u);
+    }
+};
 
 // Rows alone, blocks of 1 x 128: half a warp a block, kUnroll of them apart by the CTA's 16.
 constexpr int kUnroll = 4;
@@ -67,7 +117,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Q8Params p) {
     const int64_t row0 = first / p.col_blocks;
     const uint32_t at = (uint32_t)(first - row0 * p.col_blocks) + (threadIdx.x >> 4);
     const uint32_t blocks = (uint32_t)p.col_blocks;
-    float v[kUnroll][kVec];
+    Elems<F32, kVec> v[kUnroll];
     int64_t row[kUnroll];
     int blk[kUnroll], n[kUnroll];
 #pragma unroll
@@ -77,22 +127,35 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Q8Params p) {
         blk[u] = (int)(i % blocks);
         const int64_t c = (int64_t)blk[u] * kBlock + lane * kVec;
         n[u] = row[u] < p.rows ? (int)min(p.cols - c, (int64_t)kVec) : 0;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) v[u][i] = 0.0f;
-        if (n[u] > 0) load8<F32, VEC>((const char*)p.x + (row[u] * p.ld + c) * (F32 ? 4 : 2), n[u], v[u]);
+        v[u].zero();
+        const char* src = (const char*)p.x + (row[u] * p.ld + c) * (F32 ? 4 : 2);
+        if (n[u] > 0) {
+            if (VEC) v[u].load(src);
+            else v[u].load(src, n[u]);
+        }
     }
+    // The blocks' maxima: lanes 4 u to 4 u + 3 end with block u's, and the scales are computed once for four lanes.
+    uint32_t m[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) m[u] = v[u].top();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint32_t give = lane & 8 ? m[u] : m[u + 2];
+        m[u] = max(lane & 8 ? m[u + 2] : m[u], __shfl_xor_sync(0xFFFFFFFFu, give, 8));
+    }
+    const uint32_t give = lane & 4 ? m[0] : m[1];
+    uint32_t top = max(lane & 4 ? m[1] : m[0], __shfl_xor_sync(0xFFFFFFFFu, give, 4));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    const Scale mine = make_scale(top);
+    const uint32_t lost = __ballot_sync(0xFFFFFFFFu, mine.bad) >> (threadIdx.x & 16);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) m = max(m, magnitude(v[u][i]));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (n[u] <= 0) continue;  // whole half-warps past the rows, or lanes past a short block
-        const Scale q = make_scale(m);
-        const uint64_t inv2 = pk2(q.inv, q.inv);
-        uint2 c = make_uint2(codes4(v[u][0], v[u][1], v[u][2], v[u][3], inv2), codes4(v[u][4], v[u][5], v[u][6], v[u][7], inv2));
-        if (q.bad) c = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        const float inv = __shfl_sync(0xFFFFFFFFu, mine.inv, 4 * u, 16);
+        if (n[u] <= 0) continue;  // half-warps past the rows, or lanes past a short block
+        const uint64_t inv2 = pk2(inv, inv);
+        uint2 c = make_uint2(v[u].codes(0, inv2), v[u].codes(4, inv2));
+        if (lost >> (4 * u) & 1u) c = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
         uint8_t* dst = p.row.codes + row[u] * p.row.codes_ld + (int64_t)blk[u] * kBlock + lane * kVec;
         if (VEC) {
             __stcs(reinterpret_cast<uint2*>(dst), c);
@@ -101,8 +164,10 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Q8Params p) {
             for (int i = 0; i < kVec; ++i)
                 if (i < n[u]) dst[i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
         }
-        if (lane == 0) p.row.scales[row[u] * p.row.scales_ld + blk[u]] = q.s;
     }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        if (lane == 4 * u && row[u] < p.rows) p.row.scales[row[u] * p.row.scales_ld + blk[u]] = mine.s;
 }
 
 // Tiles of 128 x 128.
@@ -117,39 +182,30 @@ __global__ void __launch_bounds__(256, 2) fp8_tile_kernel(const Q8Params p, int 
     const int64_t r0 = tr * kBlock + warp * 16, c0 = tc * kBlock + lane * 4;
     const int rows = (int)max((int64_t)0, min(p.rows - r0, (int64_t)16));
     const int cols = (int)max((int64_t)0, min(p.cols - c0, (int64_t)4));
-    float v[16][4];
+    Elems<F32, 4> v[16];
     const char* x = (const char*)p.x + (r0 * p.ld + c0) * (F32 ? 4 : 2);
     const int64_t pitch = p.ld * (F32 ? 4 : 2);
+    if (vec && rows == 16 && cols == 4) {  // sixteen loads in flight
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < 16; ++r) v[r].load(x + r * pitch);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[r][i] = 0.0f;
-        if (r >= rows || cols <= 0) continue;
-        const char* src = x + r * pitch;
-        if (vec && cols == 4) {
-            if (F32) {
-                const float4 t = __ldcs(reinterpret_cast<const float4*>(src));
-                v[r][0] = t.x; v[r][1] = t.y; v[r][2] = t.z; v[r][3] = t.w;
-            } else {
-                const uint2 t = __ldcs(reinterpret_cast<const uint2*>(src));
-                v[r][0] = __uint_as_float(t.x << 16);
-                v[r][1] = __uint_as_float(t.x & 0xFFFF0000u);
-                v[r][2] = __uint_as_float(t.y << 16);
-                v[r][3] = __uint_as_float(t.y & 0xFFFF0000u);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < cols)
-                    v[r][i] = F32 ? reinterpret_cast<const float*>(src)[i]
-                                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src)[i]);
-        }
+        for (int r = 0; r < 16; ++r) v[r].load(x + r * pitch, r < rows ? cols : 0);
     }
-    uint32_t top[4] = {0, 0, 0, 0};  // of the lane's columns
+    uint32_t top[4];  // of the lane's columns
+    {
+        constexpr int kW = Elems<F32, 4>::kWords;
+        constexpr uint32_t kMagnitude = Elems<F32, 4>::kMagnitude;
+        uint32_t m[kW];
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
+        for (int i = 0; i < kW; ++i) m[i] = v[0].w[i] & kMagnitude;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = max(top[i], magnitude(v[r][i]));
+        for (int r = 1; r < 16; ++r)
+#pragma unroll
+            for (int i = 0; i < kW; ++i) m[i] = Elems<F32, 4>::larger(m[i], v[r].w[i] & kMagnitude);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = F32 ? m[i % kW] : (i & 1 ? m[i / 2] & 0xFFFF0000u : m[i / 2] << 16);
+    }
     // the reciprocal scales of the lane's columns; of a square block in all four
     float inv[4];
     bool bad[4];
@@ -180,8 +236,7 @@ __global__ void __launch_bounds__(256, 2) fp8_tile_kernel(const Q8Params p, int 
             uint32_t m = 0;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const uint32_t t = __reduce_max_sync(
-                    0xFFFFFFFFu, max(max(magnitude(v[r][0]), magnitude(v[r][1])), max(magnitude(v[r][2]), magnitude(v[r][3]))));
+                const uint32_t t = __reduce_max_sync(0xFFFFFFFFu, v[r].top());
                 if (lane == r) m = t;
             }
             mine = make_scale(m);
@@ -192,7 +247,7 @@ __global__ void __launch_bounds__(256, 2) fp8_tile_kernel(const Q8Params p, int 
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const float f = SQUARE ? mine.inv : __shfl_sync(0xFFFFFFFFu, mine.inv, r);
-            uint32_t c = codes4(v[r][0], v[r][1], v[r][2], v[r][3], pk2(f, f));
+            uint32_t c = v[r].codes(0, pk2(f, f));
             if (lost >> r & 1u) c = 0x7F7F7F7Fu;
             if (r >= rows) continue;
             uint8_t* d = dst + r * p.row.codes_ld;
@@ -229,7 +284,7 @@ __global__ void __launch_bounds__(256, 2) fp8_tile_kernel(const Q8Params p, int 
         uint32_t c[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            c[k] = codes4(v[4 * k][i], v[4 * k + 1][i], v[4 * k + 2][i], v[4 * k + 3][i], inv2);
+            c[k] = codes4(v[4 * k].at(i), v[4 * k + 1].at(i), v[4 * k + 2].at(i), v[4 * k + 3].at(i), inv2);
             if (bad[i]) c[k] = 0x7F7F7F7Fu;
         }
         const int col = lane * 4 + i;
