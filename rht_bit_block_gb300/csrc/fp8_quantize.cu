@@ -67,13 +67,13 @@ struct Elems {
     }
     __device__ __forceinline__ void load(const void* p) {  // aligned to the vector
         if (kWords == 2) {
-            const uint2 a = __ldcs((const uint2*)p);
+            const uint2 a = __ldg((const uint2*)p);
             w[0] = a.x;
             w[1] = a.y;
         } else {
 #pragma unroll
             for (int i = 0; i < kWords; i += 4) {
-                const uint4 a = __ldcs((const uint4*)p + i / 4);
+                const uint4 a = __ldg((const uint4*)p + i / 4);
                 w[i] = a.x;
                 w[i + 1] = a.y;
                 w[i + 2] = a.z;
@@ -109,7 +109,7 @@ struct Elems {
 // Rows alone, blocks of 1 x 128: half a warp a block, kUnroll of them apart by the CTA's 16.
 constexpr int kUnroll = 4;
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(256) fp8_rows_kernel(const Q8Params p) {
+__global__ void __launch_bounds__(256, F32 ? 3 : 6) fp8_rows_kernel(const Q8Params p) {
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 15;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Q8Params p) {
 
 // Tiles of 128 x 128.
 template <bool F32, bool SQUARE>
-__global__ void __launch_bounds__(256, 2) fp8_tile_kernel(const Q8Params p, int vec) {
+__global__ void __launch_bounds__(256, F32 ? (SQUARE ? 3 : 2) : 4) fp8_tile_kernel(const Q8Params p, int vec) {
     __shared__ __align__(16) uint32_t tops[8][kBlock];        // columns' maxima by warp; a square block's by warp
     __shared__ __align__(16) uint8_t turned[kBlock * kBlock];  // transposed codes: 16-byte unit w of column c at w ^ (c / 4 % 8)
     griddep_wait();

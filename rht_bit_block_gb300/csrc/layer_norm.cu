@@ -396,6 +396,13 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* part
 }
 
 // ------------------------------------------------------------------- shapes
+// Forward, a lane takes up to two steps (up to 16384 columns: 32 warps); with four its 64 registers do not hold the row and what
+// two sums and beta take besides (16384 x 7168: 210 us, 190 with two).
+Shape row_shape(int64_t cols) {
+    const int64_t steps = (cols + kStepCols - 1) / kStepCols;
+    const int iter = steps == 1 ? 1 : (steps <= 64 ? 2 : 4);
+    return {iter, (int)((steps + iter - 1) / iter), 1};
+}
 // Backward, a lane takes up to two steps (up to 8192 columns: 512 threads hold
 // their sums without a spill), then four (up to 16384); wider rows' sums are
 // the columns kernel's.
@@ -445,8 +452,8 @@ struct Fwd {
 template <bool F32, bool COPIED, typename F>
 cudaError_t forward_by_shape(const Shape& s, F&& f) {
     if (s.iter == 1) return f(Fwd<F32, COPIED, 1, 256>());
-    if (s.iter == 2) return f(Fwd<F32, COPIED, 2, 256>());
-    return s.threads() > 256 ? f(Fwd<F32, COPIED, 4, 1024>()) : f(Fwd<F32, COPIED, 4, 256>());
+    if (s.iter == 4) return f(Fwd<F32, COPIED, 4, 1024>());
+    return s.threads() > 512 ? f(Fwd<F32, COPIED, 2, 1024>()) : f(Fwd<F32, COPIED, 2, 512>());
 }
 template <typename F>
 cudaError_t forward_kernel(bool f32, bool copied, const Shape& s, F&& f) {
@@ -525,7 +532,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t 
     p.vec = a.cols % kVec == 0 && vec_ok(a.x, a.ldx, a.x_f32 ? 4 : 2, 16) && vec_ok(a.gamma, 0, 1, 16) &&
             (!a.beta || vec_ok(a.beta, 0, 1, 16)) && vec_ok(a.y, a.ldy, 2, 16) &&
             (!a.residual || vec_ok(a.residual, a.ld_residual, 2, 16)) && (!a.total || vec_ok(a.total, a.ld_total, 2, 16));
-    const Shape s = forward_shape(a.cols);
+    const Shape s = row_shape(a.cols);
     p.group_warps = s.warps;
     p.groups = s.groups;
     return forward_kernel(a.x_f32, p.vec != 0, s, [&](auto k) { return k.run(p, s, num_sms, st); });
@@ -564,7 +571,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cuda
 }
 
 cudaError_t preload_layer_norm_kernels() {
-    const Shape fwd[] = {{1, 1, 1}, {2, 1, 1}, {4, 1, 1}, {4, 32, 1}};
+    const Shape fwd[] = {{1, 1, 1}, {2, 16, 1}, {2, 32, 1}, {4, 32, 1}};
     const Shape bwd[] = {{1, 1, 8}, {2, 8, 1}, {2, 16, 1}, {4, 16, 1}, {4, 32, 1}};
     for (const Shape& s : fwd)
         for (int i = 0; i < 4; ++i) forward_kernel(i & 1, i & 2, s, [](auto k) { return k.load(); });
