@@ -243,6 +243,19 @@ layer_norm_backward_kernel(const LnParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dgamma[k][i] = dbeta[k][i] = 0;
     }
+    // gamma of the lane's columns, as long as registers hold it (16384 x 7168: 166 us; read again for each row 211)
+    constexpr bool kKept = ITER <= 2;
+    auto weights = [&](int k, uint64_t w[4]) {
+        const int c = first + k * kStepCols;
+        float v[kVec] = {};
+        if (c < p.cols) load_weight8(p.gamma, p.gamma_f32, vec, c, p.cols - c, v);
+        pair8(v, w);
+    };
+    uint64_t gamma[kKept ? ITER : 1][4];
+    if (kKept) {
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) weights(k, gamma[k]);
+    }
     int at = 0;
     for (; row < p.rows; row += stride) {
         const float mean = mean_next, r = rstd_next;
@@ -272,11 +285,10 @@ layer_norm_backward_kernel(const LnParams p) {
             const int c = first + k * kStepCols;
             const int n = p.cols - c;
             if (n <= 0) break;
-            uint64_t dy[4], h[4], w[4];
-            float v[kVec];
+            uint64_t dy[4], h[4], other_w[4];
             load(k, c, n, dy, h);  // past the row's end dy is 0
-            load_weight8(p.gamma, p.gamma_f32, vec, c, n, v);
-            pair8(v, w);
+            if (!kKept) weights(k, other_w);
+            const uint64_t* w = kKept ? gamma[k] : other_w;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (SUMS) {
@@ -300,11 +312,11 @@ layer_norm_backward_kernel(const LnParams p) {
             const int c = first + k * kStepCols;
             const int n = p.cols - c;
             if (n <= 0) break;
-            uint64_t dy[4], h[4], w[4], add[4] = {0, 0, 0, 0};
+            uint64_t dy[4], h[4], other_w[4], add[4] = {0, 0, 0, 0};
             float v[kVec];
             load(k, c, n, dy, h);
-            load_weight8(p.gamma, p.gamma_f32, vec, c, n, v);
-            pair8(v, w);
+            if (!kKept) weights(k, other_w);
+            const uint64_t* w = kKept ? gamma[k] : other_w;
             if (p.add) {
                 if (COPIED) A::read(src + D::kBytes + X::kBytes, k, v);
                 else load8_any(p.add, row * p.ld_add + c, 0, vec, n, v);
