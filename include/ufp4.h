@@ -522,6 +522,7 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
  *             may be NULL (zeros)
  *   eps       > 0
  *   mean, rstd  device float, rows elements, written unless NULL
+ * y or total may be x or residual, where types and pitches agree.
  * 1 <= cols <= 32768 (UFP4_ERR_UNSUPPORTED beyond). */
 ufp4_status ufp4_layer_norm(const void* x, int64_t ldx, int32_t x_dtype, const void* residual, int64_t ld_residual,
                             const void* gamma, const void* beta, int32_t gamma_dtype, int64_t rows, int64_t cols, float eps,
@@ -540,7 +541,8 @@ ufp4_status ufp4_layer_norm(const void* x, int64_t ldx, int32_t x_dtype, const v
  *              relative to s, and the gradient depends on s - m.
  *   mean, rstd what ufp4_layer_norm wrote
  *   dtotal     device bf16, the gradient of `total`, or NULL
- *   dx         device bf16, written
+ *   dx         device bf16, written; may be dy, x or dtotal, where types and
+ *              pitches agree
  *   dgamma, dbeta  device float, cols elements, written (zeros when rows is 0)
  *   workspace  at least ufp4_layer_norm_backward_workspace_size bytes,
  *              256-byte aligned; contents on entry are ignored. */

@@ -567,12 +567,11 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cuda
     p.groups = s.groups;
     const int parts = layer_norm_parts(a.rows, a.cols, num_sms);  // with no rows: one part of zeros
     cudaError_t e = cudaSuccess;
-    if (a.cols > kMostSummed) {
+    if (a.cols > kMostSummed) {  // the sums first: dx may lie where dy does
+        e = launch_pdl(layer_norm_columns_kernel, dim3((unsigned)((a.cols + 255) / 256), (unsigned)parts), dim3(256), 0, st, p);
         const int64_t grid = std::min<int64_t>(a.rows, num_sms);
-        if (grid)
+        if (e == cudaSuccess && grid)
             e = backward_kernel(a.dy_f32, a.x_f32, false, s, [&](auto k) { return k.run(p, s, (int)grid, st); });
-        if (e == cudaSuccess)
-            e = launch_pdl(layer_norm_columns_kernel, dim3((unsigned)((a.cols + 255) / 256), (unsigned)parts), dim3(256), 0, st, p);
     } else {
         const bool copied = p.vec && copies_fit(s, a.dy_f32, a.x_f32);
         e = backward_kernel(a.dy_f32, a.x_f32, copied, s, [&](auto k) { return k.run(p, s, parts, st); });

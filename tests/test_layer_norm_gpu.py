@@ -197,6 +197,31 @@ def test_gradient_against_differences():
         assert abs(float(sum(p.sum() for p in parts)) - num) <= BF * size + 1e-5 * size
 
 
+@pytest.mark.parametrize("cols", [96, 101, 2048, 9000, 16384, 20000])
+def test_results_in_place_of_operands(cols):
+    """y over x, total over residual; dx over dy, over x and over dtotal."""
+    rows = 40
+    x, residual = _rows(rows, cols, 61, torch.bfloat16, shift=1.0), _rows(rows, cols, 62, torch.bfloat16)
+    dy, dtotal = _rows(rows, cols, 63, torch.bfloat16), _rows(rows, cols, 64, torch.bfloat16)
+    gamma, beta = _weights(cols, 65, torch.bfloat16)
+    y, total = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    ufp4.ufp4_layer_norm(x, gamma, y, mean, rstd, beta=beta, residual=residual, total=total, eps=EPS)
+    x2, residual2 = x.clone(), residual.clone()
+    ufp4.ufp4_layer_norm(x2, gamma, x2, beta=beta, residual=residual2, total=residual2, eps=EPS)
+    assert torch.equal(x2, y) and torch.equal(residual2, total)
+    ws = torch.empty(ufp4.ufp4_layer_norm_backward_workspace_size(rows, cols), dtype=torch.uint8, device=DEV)
+    want = None
+    for place in (None, 0, 1, 2):
+        ops = [t.clone() for t in (dy, total, dtotal)]
+        dx = torch.empty_like(x) if place is None else ops[place]
+        dg, db = torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+        ufp4.ufp4_layer_norm_backward(ops[0], ops[1], mean, rstd, gamma, dx, dg, db, ws, dtotal=ops[2])
+        got = [dx, dg, db]
+        want = got if want is None else want
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), place
+
+
 def test_no_rows():
     x = torch.empty((0, 100), device=DEV)
     gamma, _ = _weights(100, 4, torch.float32)
