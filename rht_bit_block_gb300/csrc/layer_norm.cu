@@ -380,28 +380,26 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const LnParams 
     dst[p.cols] = dbeta;
 }
 
-// dgamma and dbeta: sums over the parts, in their order; a CTA takes 8 of the
-// 2 cols columns (one 32-byte sector a part), 128 slices of parts, then the slices.
+// dgamma and dbeta: sums over the parts, in their order.  A CTA takes 32 of the 2 cols columns, a 128-byte line of a part a warp,
+// 32 slices of the parts, then the slices.  (With 8 columns a CTA, a sector of a part each: 4096 x 16384 142 us in all, 129 so.)
 __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* partials, int parts, int cols, float* dgamma,
                                                                float* dbeta) {
-    __shared__ float slice[8][128 + 1];
+    __shared__ float slice[32][32 + 1];
     griddep_wait();
     griddep_launch();
-    const int i = threadIdx.x & 7, j = threadIdx.x >> 3;
-    const int c = blockIdx.x * 8 + i;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < 2 * cols) {
 #pragma unroll 4
-        for (int q = j; q < parts; q += 128) s += partials[(int64_t)q * 2 * cols + c];
+        for (int q = w; q < parts; q += 32) s += partials[(int64_t)q * 2 * cols + c];
     }
-    slice[i][j] = s;
+    slice[w][lane] = s;
     __syncthreads();
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (w >= 8) return;
-    s = (slice[w][lane] + slice[w][lane + 32]) + (slice[w][lane + 64] + slice[w][lane + 96]);
+    s = slice[lane][w];
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const int at = blockIdx.x * 8 + w;
+    const int at = blockIdx.x * 32 + w;
     if (lane || at >= 2 * cols) return;
     if (at < cols) dgamma[at] = s;
     else dbeta[at - cols] = s;
@@ -577,7 +575,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cuda
         e = backward_kernel(a.dy_f32, a.x_f32, copied, s, [&](auto k) { return k.run(p, s, parts, st); });
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(layer_norm_join_kernel, dim3((unsigned)((2 * a.cols + 7) / 8)), dim3(1024), 0, st,
+    return launch_pdl(layer_norm_join_kernel, dim3((unsigned)((2 * a.cols + 31) / 32)), dim3(1024), 0, st,
                       (const float*)a.partials, parts, (int)a.cols, a.dgamma, a.dbeta);
 }
 
