@@ -890,6 +890,10 @@ int max_clusters(int dev, int ctas) {
 
 // Shares of the summed index, for tiles of which each cluster computes one: the fewest blocks in a row, with kRound blocks' time
 // for a round of tiles (its start, its first copies and its join).  (768 x 7168 x 7168 on singles: 73 us with 10, 58 with 20.)
+// Two CTAs of the kernels for few tokens run on an SM, though the occupancy query counts one (K = 128: 304 tiles 3.4 us, 312
+// tiles 5.2); where they do, a block of each takes half as long again.  (37 x 7168 x 7168: 2 shares 15.6 us, 4 or 5 shares
+// 14.1; 1 x 7168 x 7168: 12.5 and 11.7; 37 x 16384 x 4096: 1 share 17.2, 2 shares 16.3; 37 x 2816 x 2048: 6 shares on 132 SMs
+// 5.6, 8 shares on two CTAs an SM 6.3.)
 constexpr int kRound = 20;
 struct Shared {
     int shares;
@@ -900,9 +904,10 @@ Shared best_shares(int dev, int64_t tiles, int64_t blocks) {
     Shared b = {1, tiles, blocks};
     int64_t least = 1ll << 60;
     for (int s = 1; s <= kMaxShares && s <= blocks; ++s) {
-        const int64_t room = max_clusters<WIDE, false, BOTH, CW, GROUPS>(dev, s);
+        const int64_t one = max_clusters<WIDE, false, BOTH, CW, GROUPS>(dev, s), room = WIDE ? one : 2 * one;
         if (room <= 0) continue;
-        const int64_t rounds = (tiles + room - 1) / room, per = (blocks + s - 1) / s, cost = rounds * (per + kRound);
+        const int64_t rounds = (tiles + room - 1) / room, per = (blocks + s - 1) / s;
+        const int64_t cost = rounds * (2 * (per + kRound) + (!WIDE && tiles > one ? per : 0));
         if (cost < least) {
             least = cost;
             b = {s, rounds, per};
