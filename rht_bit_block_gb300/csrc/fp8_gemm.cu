@@ -32,6 +32,19 @@
 // Singles and few tokens share the summed index out over a cluster of up to eight
 // CTAs, which add their sums through distributed shared memory, in the order of
 // their ranks: no workspace, no atomics, and the same bits every time.
+//
+// What bounds it.  Pairs: 16384 x 7168 x 7168 takes 600 us in a burst (2800 TFLOP/s
+// of 3777, twice the measured bf16 rate) and 675 under the power cap, 8192 x 5632 x
+// 2048 90 us.  A block takes 820 cycles of which its MMAs are 512: with two buffers
+// of 256 columns, all of tensor memory, the next block but one cannot start before
+// this one is read (155), released, and its commit seen.  Four buffers of half the
+// columns cost more hand-offs than they hide (645 us).  With scales for the rows of
+// both operands a block takes 1400 cycles, of which the reads are 260 and the
+// scaling's issue slots most of the rest: 4096 x 4096 x 8192 175 us (1570 TFLOP/s;
+// 115 us and 2390 with square blocks).  Singles: 0.33 us a block, for about 3 us of
+// start and join beside (256 x 7168 x 7168 20.5 us).  Few tokens: reading B, at 4.5
+// TB/s of 6.8 with 1 x 7168 x 7168 (11.5 us) and 5.1 with 1 x 32000 x 2048 (12.9 us),
+// about 3 us of it the start, the first copies and the join.
 #include <algorithm>
 #include <atomic>
 #include <cuda.h>
@@ -88,6 +101,8 @@ struct Cfg {
     static constexpr int kTmem = kBufs * kCols;
     static_assert(kTmem >= 32 && (kTmem & (kTmem - 1)) == 0 && kTmem <= 512, "tensor memory columns");
     static_assert(kSmem <= 232448, "shared memory overflow");
+    // CTAs of an SM take tensor memory while they wait for their cluster's others: all that shared memory lets in must fit.
+    static_assert(233472 / (kSmem + 1024) * kTmem <= 512, "CTAs that could wait for each other's tensor memory");
     static_assert(kCols * kLanes * 4 <= kStages * kStage, "a share's sums take the stages' place");
     static_assert(kQRows % 8 == 0 && kQ % 1024 == 0, "swizzle atoms");
     static_assert(!WIDE || CW % 64 == 0, "a wide tile's columns are read 64 at a time");
@@ -122,11 +137,6 @@ __device__ __forceinline__ int ld_shared(uint32_t saddr) {
 __device__ __forceinline__ float ld_shared_f(uint32_t saddr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(saddr));
-    return v;
-}
-__device__ __forceinline__ uint64_t ld_shared_pair(uint32_t saddr) {
-    uint64_t v;
-    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(saddr));
     return v;
 }
 // Two pairs of floats, 16-byte aligned.
@@ -474,8 +484,7 @@ __device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&
     }
 }
 
-// Warp 0 copies the operands (one thread), warp 1 of the leader issues the
-// MMAs, warps 2 and 3 lay out the scales, the rest scale and add.  BOTH: the
+// Warp 0 copies the operands, warp 1 of the leader issues the MMAs, warps 2 and 3 lay out the scales, the rest scale and add.  BOTH: the
 // rows of either operand have scales of their own; otherwise 128 rows of B share one.
 template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
 __global__ void __launch_bounds__((Cfg<WIDE, PAIR, CW, GROUPS>::kThreads), WIDE ? 1 : 2)

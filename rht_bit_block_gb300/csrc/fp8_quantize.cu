@@ -21,6 +21,13 @@
 // integers) and a column's is 16 of a lane's own values, joined over the warps in
 // shared memory; the transposed codes, 16 rows of a column a lane, are turned
 // around in shared memory and leave as whole 128-byte rows.
+//
+// Measured: rows of 16384 x 7168 bf16 64 us (5.5 TB/s, DRAM 63 % active, issue 73
+// %); both ways of it 93 us; 8192 x 5632 fp32 both ways 55 us (5.1 TB/s; DRAM 57 %,
+// 16 loads a thread in flight, 118 registers, two CTAs an SM); a square-blocked 7168 x
+// 7168 fp32 both ways 60 us, bf16 43.  Loads and stores take turns within a CTA, and
+// the few CTAs of an SM do not hide it all; with the elements widened to fp32 on
+// arrival (twice the registers) the bf16 square took 127 us.
 #include "ckpt8.cuh"
 #include "internal.h"
 #include "train.h"

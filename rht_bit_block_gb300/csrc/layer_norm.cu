@@ -19,6 +19,12 @@
 // dx, so that registers hold nothing of it but the running dgamma and dbeta of the
 // lane's columns.  A CTA adds its groups' sums, and a second kernel the CTAs', in
 // their order: results do not depend on timing.
+//
+// Measured: forward 16384 x 7168 fp32 190 us (6.2 TB/s, DRAM 77 % active), bf16 148,
+// 8192 x 2048 bf16 24, 2048 x 32768 bf16 120.  Backward 16384 x 7168 bf16 161 us (5.8
+// TB/s with dtotal; 122 registers, 16 warps an SM: issue 50 %, DRAM 54 %), 8192 x 2048
+// 32 us, of which start, ramp and the joining kernel are about 12; 2048 x 32768, whose
+// rows no CTA can keep the sums of, 282 us for two passes over dy and x.
 #include <algorithm>
 
 #include "ckpt8.cuh"

@@ -120,8 +120,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ufp4_fp8_quantize.argtypes = [P, i64, i32, i64, i64, i32, QT, QT, P]
     L.ufp4_fp8_gemm.argtypes = [QT, i32, QT, i32, P, i64, i32, i32, P]
     for name in ("ufp4_layer_norm", "ufp4_layer_norm_backward_workspace_size", "ufp4_layer_norm_backward",
-                 "ufp4_fp8_quantize", "ufp4_fp8_gemm", "ufp4_glu", "ufp4_glu_backward", "ufp4_rms_norm", "ufp4_rms_norm_backward_workspace_size",
-                 "ufp4_rms_norm_backward", "ufp4_head_loss_workspace_size", "ufp4_head_loss",
+                 "ufp4_fp8_quantize", "ufp4_fp8_gemm", "ufp4_glu", "ufp4_glu_backward", "ufp4_rms_norm",
+                 "ufp4_rms_norm_backward_workspace_size", "ufp4_rms_norm_backward", "ufp4_head_loss_workspace_size", "ufp4_head_loss",
                  "ufp4_head_loss_backward_workspace_size", "ufp4_head_loss_backward",
                  "ufp4_rht_quantize", "ufp4_rht_quantize_grouped", "ufp4_rht_transform", "ufp4_dequantize",
                  "ufp4_gemm_workspace_size", "ufp4_gemm", "ufp4_sign_vector", "ufp4_device_error",
