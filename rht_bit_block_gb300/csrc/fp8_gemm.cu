@@ -398,22 +398,27 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
 // + lane % 4.
 //
 // Their stores from the registers would touch 32 rows, or 16 bytes, at a time; instead 128 bytes of every row are turned around in
-// `stage` (16-byte units, unit u of row i at u ^ (i & 7)) and stored four whole rows of them an instruction.
+// `stage` (16-byte units, unit u of row i at u ^ (i & 7)) and stored four whole rows of them an instruction, or, where D's rows
+// are not aligned or the tile is cut short, 32 neighbouring elements (4096 x 4095 x 2048: 40 us, 35 where aligned; from the
+// registers 165).
 template <bool BOTH, int CW>
 __device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&acc)[CW / 2], int row0, int col0,
                                            uint8_t* stage) {
     const int lane = threadIdx.x & 31, q = lane & 3;
-    if (col0 + CW <= p.q_rows && p.d_vec == 16) {
-        uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
-        auto flush = [&](int c, int bytes) {  // the stage holds columns col0 + c on
-            __syncwarp();
-            char* base = (char*)p.d + ((int64_t)(row0 + (lane >> 3)) * p.ldd + col0 + c) * bytes + (lane & 7) * 16;
+    const bool vec = col0 + CW <= p.q_rows && p.d_vec == 16;
+    uint4* mine = reinterpret_cast<uint4*>(stage + lane * 128);
+    auto flush = [&](int c, auto element) {  // the stage holds columns col0 + c on
+        using T = decltype(element);
+        constexpr int kBytes = sizeof(T);
+        __syncwarp();
+        if (vec) {
+            char* base = (char*)p.d + ((int64_t)(row0 + (lane >> 3)) * p.ldd + col0 + c) * kBytes + (lane & 7) * 16;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int row = i * 4 + (lane >> 3);
                 uint4 v = reinterpret_cast<const uint4*>(stage + row * 128)[(lane & 7) ^ (row & 7)];
                 if (row0 + row < p.p_rows) {
-                    uint4* d = reinterpret_cast<uint4*>(base + (int64_t)i * 4 * p.ldd * bytes);
+                    uint4* d = reinterpret_cast<uint4*>(base + (int64_t)i * 4 * p.ldd * kBytes);
                     if (p.accumulate) {
                         const uint4 o = *d;
                         v = make_uint4(__float_as_uint(__uint_as_float(o.x) + __uint_as_float(v.x)),
@@ -424,68 +429,78 @@ __device__ __forceinline__ void store_wide(const Fp8Params& p, const uint64_t (&
                     *d = v;
                 }
             }
-            __syncwarp();
-        };
-        // BOTH: the pair of rows of column 4 j + q, the j-th four of the 128 bytes (all rows are lane / 4 modulo 8)
-        auto put_pair = [&](int h, int j, int bytes, uint64_t v) {
-            float x, y;
-            up2(v, x, y);
-            uint8_t* at = stage + (16 * h + (lane >> 2)) * 128 + (((j * bytes) >> 2) ^ (lane >> 2)) * 16;
-            if (bytes == 4) {
-                reinterpret_cast<float*>(at)[q] = x;
-                reinterpret_cast<float*>(at + 8 * 128)[q] = y;
-            } else {
-                reinterpret_cast<__nv_bfloat16*>(at)[4 * (j & 1) + q] = __float2bfloat16_rn(x);
-                reinterpret_cast<__nv_bfloat16*>(at + 8 * 128)[4 * (j & 1) + q] = __float2bfloat16_rn(y);
-            }
-        };
-        if (p.d_f32) {
-#pragma unroll
-            for (int c = 0; c < CW; c += 32) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    if (BOTH) {
-                        put_pair(0, u, 4, acc[c / 4 + u]);
-                        put_pair(1, u, 4, acc[CW / 4 + c / 4 + u]);
-                    } else {
-                        const uint64_t x = acc[c / 2 + 2 * u], y = acc[c / 2 + 2 * u + 1];
-                        mine[u ^ (lane & 7)] = make_uint4((uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32));
-                    }
-                }
-                flush(c, 4);
-            }
         } else {
+            const int rows = min(32, p.p_rows - row0);
 #pragma unroll
-            for (int c = 0; c < CW; c += 64) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    if (BOTH) {
-#pragma unroll
-                        for (int j = 2 * u; j < 2 * u + 2; ++j) {
-                            put_pair(0, j, 2, acc[c / 4 + j]);
-                            put_pair(1, j, 2, acc[CW / 4 + c / 4 + j]);
-                        }
-                    } else {
-                        const uint64_t* a = acc + c / 2 + 4 * u;
-                        mine[u ^ (lane & 7)] = make_uint4(pack_bf16(a[0]), pack_bf16(a[1]), pack_bf16(a[2]), pack_bf16(a[3]));
-                    }
+            for (int e = lane; e < 128 / kBytes; e += 32) {
+                if (col0 + c + e >= p.q_rows) break;
+                T* d = (T*)p.d + (int64_t)row0 * p.ldd + col0 + c + e;
+                const uint8_t* from = stage + e % (16 / kBytes) * kBytes;
+                const int unit = e / (16 / kBytes);
+#pragma unroll 4
+                for (int row = 0; row < rows; ++row) {
+                    T v = *reinterpret_cast<const T*>(from + row * 128 + ((unit ^ (row & 7)) << 4));
+                    if constexpr (kBytes == 4)
+                        if (p.accumulate) v += *d;
+                    *d = v;
+                    d += p.ldd;
                 }
-                flush(c, 2);
             }
         }
-        return;
-    }
-    // ragged or unaligned columns
+        __syncwarp();
+    };
+    // BOTH: the pair of rows of column 4 j + q, the j-th four of the 128 bytes (all rows are lane / 4 modulo 8)
+    auto put_pair = [&](int h, int j, int bytes, uint64_t v) {
+        float x, y;
+        up2(v, x, y);
+        uint8_t* at = stage + (16 * h + (lane >> 2)) * 128 + (((j * bytes) >> 2) ^ (lane >> 2)) * 16;
+        if (bytes == 4) {
+            reinterpret_cast<float*>(at)[q] = x;
+            reinterpret_cast<float*>(at + 8 * 128)[q] = y;
+        } else {
+            reinterpret_cast<__nv_bfloat16*>(at)[4 * (j & 1) + q] = __float2bfloat16_rn(x);
+            reinterpret_cast<__nv_bfloat16*>(at + 8 * 128)[4 * (j & 1) + q] = __float2bfloat16_rn(y);
+        }
+    };
+    if (p.d_f32) {
 #pragma unroll
-    for (int i = 0; i < CW; ++i) {
-        const int row = row0 + (BOTH ? 16 * (i / (CW / 2)) + 8 * (i & 1) + (lane >> 2) : lane);
-        const int col = col0 + (BOTH ? 4 * (i % (CW / 2) / 2) + q : i);
-        if (row < p.p_rows && col < p.q_rows) put(p, (int64_t)row * p.ldd + col, column(acc, i));
+        for (int c = 0; c < CW; c += 32) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (BOTH) {
+                    put_pair(0, u, 4, acc[c / 4 + u]);
+                    put_pair(1, u, 4, acc[CW / 4 + c / 4 + u]);
+                } else {
+                    const uint64_t x = acc[c / 2 + 2 * u], y = acc[c / 2 + 2 * u + 1];
+                    mine[u ^ (lane & 7)] = make_uint4((uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32));
+                }
+            }
+            flush(c, 0.0f);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < CW; c += 64) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (BOTH) {
+#pragma unroll
+                    for (int j = 2 * u; j < 2 * u + 2; ++j) {
+                        put_pair(0, j, 2, acc[c / 4 + j]);
+                        put_pair(1, j, 2, acc[CW / 4 + c / 4 + j]);
+                    }
+                } else {
+                    const uint64_t* a = acc + c / 2 + 4 * u;
+                    mine[u ^ (lane & 7)] = make_uint4(pack_bf16(a[0]), pack_bf16(a[1]), pack_bf16(a[2]), pack_bf16(a[3]));
+                }
+            }
+            flush(c, __nv_bfloat16());
+        }
     }
 }
 
-// Warp 0 copies the operands, warp 1 of the leader issues the MMAs, warps 2 and 3 lay out the scales, the rest scale and add.  BOTH: the
-// rows of either operand have scales of their own; otherwise 128 rows of B share one.
+// Warp 0 copies the operands, warp 1 of the leader issues the MMAs, warps 2
+// and 3 lay out the scales, the rest scale and add.  BOTH: the rows of either
+// operand have scales of their own; otherwise 128 rows of B share one.
 template <bool WIDE, bool PAIR, bool BOTH, int CW, int GROUPS>
 __global__ void __launch_bounds__((Cfg<WIDE, PAIR, CW, GROUPS>::kThreads), WIDE ? 1 : 2)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
