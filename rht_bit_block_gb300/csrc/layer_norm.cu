@@ -49,6 +49,7 @@ struct LnParams {
     int64_t ldx, ld_dy, ld_add;
     int x_f32, dy_f32, gamma_f32;  // x and dy: where they are read without copies
     int vec;                       // the same: all rows are aligned to their vectors
+    int vec_weights;               // gamma and beta are
     int64_t rows;
     int cols;
     int group_warps, groups;       // warps a row, rows a CTA works on at once
@@ -82,6 +83,11 @@ __device__ __forceinline__ void load_weight8(const void* p, int f32, int vec, in
         widen8(__ldg((const uint4*)((const __nv_bfloat16*)p + c)), v);
     }
 }
+// Whether they are aligned to vectors and the row has all eight.
+template <bool SHIFTED>
+__device__ __forceinline__ int weight_vec(const LnParams& p, int n) {
+    return SHIFTED ? p.vec_weights && n >= kVec : 1;
+}
 __device__ __forceinline__ void store8_any(__nv_bfloat16* p, int vec, int n, const float v[kVec]) {
     if (vec) store8_bf16<true>(p, n, v);
     else store8_bf16<false>(p, n, v);
@@ -89,35 +95,148 @@ __device__ __forceinline__ void store8_any(__nv_bfloat16* p, int vec, int n, con
 
 // A warp's share of a row in shared memory: one matrix, ITER steps of 256
 // columns.  Copied 16 consecutive bytes a lane, so that every 32-byte sector is
-// fetched once; read as a lane's 8 elements.
-template <bool F32, int ITER>
+// fetched once; read as a lane's 8 elements.  SHIFTED: rows may start anywhere.
+// The 16-byte units of memory that hold the share are copied as they are, and a
+// lane's elements taken out of two or three of them; what lies beside the share
+// in its first unit, which belongs to the matrix too or is left out, is not
+// looked at.  (8192 x 4999 bf16: forward 113 us, backward 158; 222 and 311 with the
+// elements loaded and stored one by one, 59 and 83 of 5000 columns.)
+template <bool F32, int ITER, bool SHIFTED>
 struct Copy {
-    static constexpr int kStepBytes = F32 ? 1024 : 512;
-    static constexpr int kBytes = ITER * kStepBytes;
+    static constexpr int kElem = F32 ? 4 : 2;
+    static constexpr int kStepBytes = kStepCols * kElem;
+    static constexpr int kBytes = ITER * kStepBytes + (SHIFTED ? 16 : 0);
+    // Bytes of the first unit in front of a row's share: shares start at multiples of 16 bytes of the row.
+    static __device__ __forceinline__ int shift(const void* base, int64_t ld, int64_t row) {
+        return SHIFTED ? (int)((uint32_t)(uintptr_t)base + (uint32_t)row * (uint32_t)ld * kElem) & 15 : 0;
+    }
     static __device__ __forceinline__ void fetch(uint32_t dst, const void* base, int64_t ld, int64_t row, int c0, int cols) {
         const int lane = threadIdx.x & 31;
-        const char* src = (const char*)base + (row * ld + c0) * (F32 ? 4 : 2) + lane * 16;
+        const char* src = (const char*)base + (row * ld + c0) * kElem + lane * 16;
+        if constexpr (SHIFTED) {
+            if (cols <= c0) return;
+            const int before = shift(base, ld, row), bytes = before + min(cols - c0, ITER * kStepCols) * kElem;
+            src -= before;
 #pragma unroll
-        for (int k = 0; k < ITER; ++k) {
-            const int left = cols - c0 - k * kStepCols;
-            if (left <= 0) break;
-            if (lane * (F32 ? 4 : 8) < left) copy16(dst + k * kStepBytes + lane * 16, src + k * kStepBytes);
-            if (F32 && 128 + lane * 4 < left) copy16(dst + k * kStepBytes + 512 + lane * 16, src + k * kStepBytes + 512);
+            for (int k = 0; k <= ITER * kStepBytes / 512; ++k) {
+                const int left = bytes - k * 512 - lane * 16;
+                if (left <= 0) break;
+                if (src + k * 512 < (const char*)base) {  // the matrix starts within this unit
+                    for (int i = before; i < min(left, 16); i += kElem) {
+                        if (F32) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + i), "r"(*(const uint32_t*)(src + i)) : "memory");
+                        else asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + i), "h"(*(const uint16_t*)(src + i)) : "memory");
+                    }
+                } else {
+                    copy16_part(dst + k * 512 + lane * 16, src + k * 512, min(left, 16));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < ITER; ++k) {
+                const int left = cols - c0 - k * kStepCols;
+                if (left <= 0) break;
+                if (lane * (F32 ? 4 : 8) < left) copy16(dst + k * kStepBytes + lane * 16, src + k * kStepBytes);
+                if (F32 && 128 + lane * 4 < left) copy16(dst + k * kStepBytes + 512 + lane * 16, src + k * kStepBytes + 512);
+            }
         }
     }
-    static __device__ __forceinline__ void read(const uint8_t* src, int k, float v[kVec]) {
-        const uint8_t* p = src + k * kStepBytes + (threadIdx.x & 31) * (F32 ? 32 : 16);
-        if (F32) widen8(*(const float4*)p, *(const float4*)(p + 16), v);
-        else widen8(*(const uint4*)p, v);
+    // Step k's elements of the lane, of which n (SHIFTED: or none) exist; zeros after.
+    static __device__ __forceinline__ void read(const uint8_t* src, int k, int shift, int n, float v[kVec]) {
+        const uint8_t* p = src + k * kStepBytes + (threadIdx.x & 31) * (kVec * kElem);
+        if (!SHIFTED) {
+            if (F32) widen8(*(const float4*)p, *(const float4*)(p + 16), v);
+            else widen8(*(const uint4*)p, v);
+            return;
+        }
+        constexpr int kWords = kVec * kElem / 4;
+        uint32_t w[kWords + 4];
+#pragma unroll
+        for (int i = 0; i < kWords + 4; i += 4) {
+            const uint4 u = *(const uint4*)(p + i * 4);
+            w[i] = u.x;
+            w[i + 1] = u.y;
+            w[i + 2] = u.z;
+            w[i + 3] = u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < kWords + 3; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+#pragma unroll
+        for (int i = 0; i < kWords + 1; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+        if (F32) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+            widen8(make_uint4(w[0], w[1], w[2], w[3]), v);
+        }
+        if (n < kVec) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (i >= n) v[i] = 0.0f;
+        }
     }
 };
 
-// COPIED: rows are copied ahead (all of them aligned); otherwise they are read
-// where they are, by vectors or by elements.  THREADS: the most a CTA has.
-template <bool F32, bool COPIED, int ITER, int THREADS>
+// Stores a warp's share of a bf16 row that may start anywhere, step by step: the 16-byte units of memory are put together from
+// neighbouring lanes' elements and stored whole, those at either end of the share by elements.  All lanes call it.
+struct ShiftedRow {
+    char* first;        // of the lane: its unit of step 0
+    int shift, bytes;   // in front of the share, in its first unit; of the share
+    uint32_t last[4];   // lane 0: what the step before left of its last lane
+    __device__ __forceinline__ ShiftedRow(__nv_bfloat16* share, int cols) {
+        shift = (int)(uintptr_t)share & 15;
+        bytes = cols * 2;
+        first = (char*)share - shift + (threadIdx.x & 31) * 16;
+    }
+    __device__ __forceinline__ void units(int k, const uint32_t before[4], const uint32_t w[4]) const {
+        const int at = k * 512 + (int)(threadIdx.x & 31) * 16 - shift;  // of the unit, in the share
+        if (at >= bytes) return;
+        uint32_t t[8] = {before[0], before[1], before[2], before[3], w[0], w[1], w[2], w[3]};
+        const int from = 16 - shift;  // where the unit starts in the two lanes' bytes
+        // from a multiple of 4: words from / 4; otherwise half a word further on
+#pragma unroll
+        for (int i = 0; i < 7; ++i) t[i] = from & 4 ? t[i + 1] : t[i];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) t[i] = from & 8 ? t[i + 2] : t[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = from & 16 ? t[i + 4] : t[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = __funnelshift_r(t[i], t[i + 1], (from & 2) * 8);
+        char* d = first + k * 512;
+        if (at >= 0 && at + 16 <= bytes) {
+            __stcs(reinterpret_cast<uint4*>(d), make_uint4(t[0], t[1], t[2], t[3]));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (at + 2 * i >= 0 && at + 2 * i < bytes) *reinterpret_cast<uint16_t*>(d + 2 * i) = (uint16_t)(t[i / 2] >> (16 * (i & 1)));
+    }
+    __device__ __forceinline__ void step(int k, const float v[kVec]) {
+        const int lane = threadIdx.x & 31;
+        uint32_t w[4], before[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            const uint32_t o = __shfl_sync(0xFFFFFFFFu, w[i], (lane + 31) & 31);
+            before[i] = lane ? o : last[i];
+            last[i] = o;
+        }
+        units(k, before, w);
+    }
+    // What is left after `steps` steps.
+    __device__ __forceinline__ void finish(int steps) const {
+        const uint32_t none[4] = {0, 0, 0, 0};
+        if ((threadIdx.x & 31) == 0) units(steps, last, none);
+    }
+};
+
+// SHIFTED: some row is not aligned to 16 bytes or no whole number of lanes'
+// elements.  THREADS: the most a CTA has.
+template <bool F32, bool SHIFTED, int ITER, int THREADS>
 __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm_kernel(const LnParams p) {
-    using X = Copy<F32, ITER>;
-    using A = Copy<false, ITER>;
+    using X = Copy<F32, ITER, SHIFTED>;
+    using A = Copy<false, ITER, SHIFTED>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float slots[32];
     griddep_wait();
@@ -125,7 +244,6 @@ __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm
     const Group<true> g(p.group_warps);
     const int first = g.template first<ITER>();
     const int c0 = first - g.lane * kVec;  // the warp's first column
-    const int vec = COPIED ? 1 : p.vec;
     const uint8_t* mine = smem + (threadIdx.x >> 5) * (X::kBytes + A::kBytes);
     const uint32_t saddr = (uint32_t)__cvta_generic_to_shared(mine);
     auto fetch = [&](int64_t row) {
@@ -133,27 +251,23 @@ __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm
         X::fetch(saddr, p.x, p.ldx, row, c0, p.cols);
         if (p.add) A::fetch(saddr + X::kBytes, p.add, p.ld_add, row, c0, p.cols);
     };
-    if (COPIED) fetch(blockIdx.x);
+    fetch(blockIdx.x);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         float s[ITER][kVec];
         float sum = 0.0f;
-        if (COPIED) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-        }
+        const int of_x = X::shift(p.x, p.ldx, row), of_add = A::shift(p.add, p.ld_add, row);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
-            const int c = first + k * kStepCols;
-            const int n = p.cols - c;
+            const int n = p.cols - (first + k * kStepCols);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) s[k][i] = 0.0f;
             if (n > 0) {
-                if (COPIED) X::read(mine, k, s[k]);
-                else load8_any(p.x, row * p.ldx + c, F32, vec, n, s[k]);
+                X::read(mine, k, of_x, n, s[k]);
                 if (p.add) {
                     float r[kVec];
-                    if (COPIED) A::read(mine + X::kBytes, k, r);
-                    else load8_any(p.add, row * p.ld_add + c, 0, vec, n, r);
+                    A::read(mine + X::kBytes, k, of_add, n, r);
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) s[k][i] += r[i];
                 }
@@ -161,10 +275,8 @@ __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm
 #pragma unroll
             for (int i = 0; i < kVec; ++i) sum += s[k][i];
         }
-        if (COPIED) {  // the warp's copies are in registers
-            __syncwarp();
-            fetch(row + gridDim.x);
-        }
+        __syncwarp();  // the warp's copies are in registers
+        fetch(row + gridDim.x);
         const float mean = g.sum(sum, slots) * p.inv_cols;
         float var = 0.0f;
 #pragma unroll
@@ -181,37 +293,70 @@ __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = r;
         }
-        __nv_bfloat16* y = p.y + row * p.ldy + first;
-        __nv_bfloat16* out = p.out + row * p.ld_out + first;
-#pragma unroll
-        for (int k = 0; k < ITER; ++k) {
+        auto result = [&](int k, int n, float w[kVec]) {
             const int c = first + k * kStepCols;
-            const int n = p.cols - c;
-            if (n <= 0) break;
-            if (p.out) store8_any(out + k * kStepCols, vec, n, s[k]);
-            float w[kVec], b[kVec];
-            load_weight8(p.gamma, p.gamma_f32, vec, c, n, w);
+            float b[kVec];
+            load_weight8(p.gamma, p.gamma_f32, weight_vec<SHIFTED>(p, n), c, n, w);
             if (p.beta) {
-                load_weight8(p.beta, p.gamma_f32, vec, c, n, b);
+                load_weight8(p.beta, p.gamma_f32, weight_vec<SHIFTED>(p, n), c, n, b);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) w[i] = fmaf((s[k][i] - mean) * r, w[i], b[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) w[i] = (s[k][i] - mean) * r * w[i];
             }
-            store8_any(y + k * kStepCols, vec, n, w);
+        };
+        if (SHIFTED) {
+            const int share = min(p.cols - c0, ITER * kStepCols);
+            if (share <= 0) continue;
+            const int steps = (share + kStepCols - 1) / kStepCols;
+            if (p.out) {
+                ShiftedRow to(p.out + row * p.ld_out + c0, share);
+#pragma unroll
+                for (int k = 0; k < ITER; ++k)
+                    if (k < steps) to.step(k, s[k]);
+                to.finish(steps);
+            }
+            ShiftedRow to(p.y + row * p.ldy + c0, share);
+#pragma unroll
+            for (int k = 0; k < ITER; ++k) {
+                if (k >= steps) break;
+                float w[kVec];
+                result(k, p.cols - (first + k * kStepCols), w);
+                to.step(k, w);
+            }
+            to.finish(steps);
+            continue;
+        }
+        __nv_bfloat16* y = p.y + row * p.ldy + first;
+        __nv_bfloat16* out = p.out + row * p.ld_out + first;
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int n = p.cols - (first + k * kStepCols);
+            if (n <= 0) break;
+            if (p.out) store8_bf16<true>(out + k * kStepCols, n, s[k]);
+            float w[kVec];
+            result(k, n, w);
+            store8_bf16<true>(y + k * kStepCols, n, w);
         }
     }
 }
 
+// How the backward pass gets at its rows.
+enum Rows {
+    kInPlace,   // read where they are, by vectors or by elements: what is too wide for two rows' copies
+    kAligned,   // copied ahead
+    kShifted    // the same, of rows that start anywhere
+};
 // The types of dy and x are given for copied rows (DY32, X32) and looked up
 // otherwise.  SUMS: dgamma and dbeta are summed.
-template <bool DY32, bool X32, bool COPIED, bool SUMS, int ITER, int THREADS>
+template <bool DY32, bool X32, Rows ROWS, bool SUMS, int ITER, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > kBackwardThreads ? 1 : kBackwardThreads / THREADS)
 layer_norm_backward_kernel(const LnParams p) {
-    using D = Copy<DY32, ITER>;
-    using X = Copy<X32, ITER>;
-    using A = Copy<false, ITER>;
+    constexpr bool COPIED = ROWS != kInPlace, SHIFTED = ROWS == kShifted;
+    using D = Copy<DY32, ITER, SHIFTED>;
+    using X = Copy<X32, ITER, SHIFTED>;
+    using A = Copy<false, ITER, SHIFTED>;
     constexpr int kWarp = D::kBytes + X::kBytes + A::kBytes;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(8) float slots[64];
@@ -220,7 +365,6 @@ layer_norm_backward_kernel(const LnParams p) {
     const Group<false> g(p.group_warps);
     const int first = g.template first<ITER>();
     const int c0 = first - g.lane * kVec;
-    const int vec = COPIED ? 1 : p.vec;
     const int64_t stride = (int64_t)gridDim.x * p.groups;
     const int other = (blockDim.x >> 5) * kWarp;  // from one of the two rows to the other
     const uint8_t* mine = smem + (threadIdx.x >> 5) * kWarp;
@@ -254,7 +398,8 @@ layer_norm_backward_kernel(const LnParams p) {
     auto weights = [&](int k, uint64_t w[4]) {
         const int c = first + k * kStepCols;
         float v[kVec] = {};
-        if (c < p.cols) load_weight8(p.gamma, p.gamma_f32, vec, c, p.cols - c, v);
+        const int n = p.cols - c;
+        if (n > 0) load_weight8(p.gamma, p.gamma_f32, COPIED ? weight_vec<SHIFTED>(p, n) : p.vec, c, n, v);
         pair8(v, w);
     };
     uint64_t gamma[kKept ? ITER : 1][4];
@@ -273,14 +418,15 @@ layer_norm_backward_kernel(const LnParams p) {
         }
         stats(row + stride);
         const uint8_t* src = mine + at;
+        const int of_dy = D::shift(p.dy, p.ld_dy, row), of_x = X::shift(p.x, p.ldx, row);
         // dy and the normalised row, step k
         auto load = [&](int k, int c, int n, uint64_t dy[4], uint64_t h[4]) {
             float v[kVec];
-            if (COPIED) D::read(src, k, v);
-            else load8_any(p.dy, row * p.ld_dy + c, p.dy_f32, vec, n, v);
+            if (COPIED) D::read(src, k, of_dy, n, v);
+            else load8_any(p.dy, row * p.ld_dy + c, p.dy_f32, p.vec, n, v);
             pair8(v, dy);
-            if (COPIED) X::read(src + D::kBytes, k, v);
-            else load8_any(p.x, row * p.ldx + c, p.x_f32, vec, n, v);
+            if (COPIED) X::read(src + D::kBytes, k, of_x, n, v);
+            else load8_any(p.x, row * p.ldx + c, p.x_f32, p.vec, n, v);
             pair8(v, h);
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = mul2(add2(h[i], minus), r2);
@@ -312,26 +458,46 @@ layer_norm_backward_kernel(const LnParams p) {
         const float2 sums = g.sum2(make_float2(t.x + t.y, u.x + u.y), slots);
         const float mq = -sums.x * p.inv_cols, mqh = -sums.y * p.inv_cols;
         const uint64_t mq2 = pk2(mq, mq), mqh2 = pk2(mqh, mqh);
-        __nv_bfloat16* out = p.out + row * p.ld_out + first;
-#pragma unroll
-        for (int k = 0; k < ITER; ++k) {
-            const int c = first + k * kStepCols;
-            const int n = p.cols - c;
-            if (n <= 0) break;
+        const int of_add = A::shift(p.add, p.ld_add, row);
+        auto result = [&](int k, float v[kVec]) {
+            const int c = first + k * kStepCols, n = p.cols - c;
             uint64_t dy[4], h[4], other_w[4], add[4] = {0, 0, 0, 0};
-            float v[kVec];
             load(k, c, n, dy, h);
             if (!kKept) weights(k, other_w);
             const uint64_t* w = kKept ? gamma[k] : other_w;
             if (p.add) {
-                if (COPIED) A::read(src + D::kBytes + X::kBytes, k, v);
-                else load8_any(p.add, row * p.ld_add + c, 0, vec, n, v);
+                if (COPIED) A::read(src + D::kBytes + X::kBytes, k, of_add, n, v);
+                else load8_any(p.add, row * p.ld_add + c, 0, p.vec, n, v);
                 pair8(v, add);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 up2(fma2(r2, fma2(h[i], mqh2, fma2(dy[i], w[i], mq2)), add[i]), v[2 * i], v[2 * i + 1]);
-            store8_any(out + k * kStepCols, vec, n, v);
+        };
+        if (SHIFTED) {
+            const int share = min(p.cols - c0, ITER * kStepCols);
+            if (share > 0) {
+                const int steps = (share + kStepCols - 1) / kStepCols;
+                ShiftedRow to(p.out + row * p.ld_out + c0, share);
+#pragma unroll
+                for (int k = 0; k < ITER; ++k) {
+                    if (k >= steps) break;
+                    float v[kVec];
+                    result(k, v);
+                    to.step(k, v);
+                }
+                to.finish(steps);
+            }
+        } else {
+            __nv_bfloat16* out = p.out + row * p.ld_out + first;
+#pragma unroll
+            for (int k = 0; k < ITER; ++k) {
+                const int n = p.cols - (first + k * kStepCols);
+                if (n <= 0) break;
+                float v[kVec];
+                result(k, v);
+                store8_any(out + k * kStepCols, COPIED ? 1 : p.vec, n, v);
+            }
         }
         if (COPIED) {
             __syncwarp();  // the warp is done with this row's copies
@@ -431,79 +597,88 @@ Shape backward_shape(int64_t cols) {
     return s;
 }
 
-template <bool F32, bool COPIED, int ITER>
+template <bool F32, bool SHIFTED, int ITER>
 constexpr int forward_smem(int warps) {
-    return COPIED ? warps * (Copy<F32, ITER>::kBytes + Copy<false, ITER>::kBytes) : 0;
+    return warps * (Copy<F32, ITER, SHIFTED>::kBytes + Copy<false, ITER, SHIFTED>::kBytes);
 }
 // Two rows, and at least the sums that the groups but the last leave there.
-template <bool DY32, bool X32, bool COPIED, int ITER>
+template <bool DY32, bool X32, Rows ROWS, int ITER>
 constexpr int backward_smem(int warps, int groups, int cols) {
-    const int rows = COPIED ? 2 * warps * groups * (Copy<DY32, ITER>::kBytes + Copy<X32, ITER>::kBytes + Copy<false, ITER>::kBytes) : 0;
+    constexpr bool s = ROWS == kShifted;
+    const int rows = ROWS == kInPlace ? 0 : 2 * warps * groups * (Copy<DY32, ITER, s>::kBytes + Copy<X32, ITER, s>::kBytes +
+                                                                  Copy<false, ITER, s>::kBytes);
     const int sums = groups > 1 ? 2 * cols * 4 : 0;
     return rows > sums ? rows : sums;
 }
-int step_bytes(bool dy_f32, bool x_f32) { return kStepCols * ((dy_f32 ? 4 : 2) + (x_f32 ? 4 : 2) + 2); }
+// Of a warp's two rows, shifted ones.
+size_t warp_bytes(const Shape& s, bool dy_f32, bool x_f32) {
+    return 2 * (size_t)(s.iter * kStepCols * ((dy_f32 ? 4 : 2) + (x_f32 ? 4 : 2) + 2) + 3 * 16);
+}
 bool copies_fit(const Shape& s, bool dy_f32, bool x_f32) {
-    return (size_t)2 * s.warps * s.groups * s.iter * step_bytes(dy_f32, x_f32) <= kMostSmem;
+    return s.warps * s.groups * warp_bytes(s, dy_f32, x_f32) <= kMostSmem;
 }
 
-template <bool F32, bool COPIED, int ITER, int THREADS>
+template <bool F32, bool SHIFTED, int ITER, int THREADS>
 struct Fwd {
     static cudaError_t run(const LnParams& p, const Shape& s, int num_sms, cudaStream_t st) {
-        const size_t smem = forward_smem<F32, COPIED, ITER>(s.warps * s.groups);
+        const size_t smem = forward_smem<F32, SHIFTED, ITER>(s.warps * s.groups);
         const int64_t grid = std::min<int64_t>(p.rows, (int64_t)num_sms * ctas_per_sm(s, kForwardThreads, smem));
-        return launch_pdl(layer_norm_kernel<F32, COPIED, ITER, THREADS>, dim3((unsigned)grid), dim3(s.threads()), smem, st, p);
+        return launch_pdl(layer_norm_kernel<F32, SHIFTED, ITER, THREADS>, dim3((unsigned)grid), dim3(s.threads()), smem, st, p);
     }
     // Loads the kernel and lets it have what the widest row it serves takes: the limit belongs to the kernel, which
     // calls of other widths use at the same time.
     static cudaError_t load() {
-        constexpr int smem = forward_smem<F32, COPIED, ITER>(THREADS / 32);
+        constexpr int smem = forward_smem<F32, SHIFTED, ITER>(THREADS / 32);
         static_assert(smem <= (int)kMostSmem, "shared memory overflow");
         cudaFuncAttributes at;
-        cudaFuncGetAttributes(&at, layer_norm_kernel<F32, COPIED, ITER, THREADS>);
-        return cudaFuncSetAttribute(layer_norm_kernel<F32, COPIED, ITER, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncGetAttributes(&at, layer_norm_kernel<F32, SHIFTED, ITER, THREADS>);
+        return cudaFuncSetAttribute(layer_norm_kernel<F32, SHIFTED, ITER, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     smem);
     }
 };
-template <bool F32, bool COPIED, typename F>
+template <bool F32, bool SHIFTED, typename F>
 cudaError_t forward_by_shape(const Shape& s, F&& f) {
-    if (s.iter == 1) return f(Fwd<F32, COPIED, 1, 256>());
-    if (s.iter == 4) return f(Fwd<F32, COPIED, 4, 1024>());
-    return s.threads() > 512 ? f(Fwd<F32, COPIED, 2, 1024>()) : f(Fwd<F32, COPIED, 2, 512>());
+    if (s.iter == 1) return f(Fwd<F32, SHIFTED, 1, 256>());
+    if (s.iter == 4) return f(Fwd<F32, SHIFTED, 4, 1024>());
+    return s.threads() > 512 ? f(Fwd<F32, SHIFTED, 2, 1024>()) : f(Fwd<F32, SHIFTED, 2, 512>());
 }
 template <typename F>
-cudaError_t forward_kernel(bool f32, bool copied, const Shape& s, F&& f) {
-    if (f32) return copied ? forward_by_shape<true, true>(s, f) : forward_by_shape<true, false>(s, f);
-    return copied ? forward_by_shape<false, true>(s, f) : forward_by_shape<false, false>(s, f);
+cudaError_t forward_kernel(bool f32, bool shifted, const Shape& s, F&& f) {
+    if (f32) return shifted ? forward_by_shape<true, true>(s, f) : forward_by_shape<true, false>(s, f);
+    return shifted ? forward_by_shape<false, true>(s, f) : forward_by_shape<false, false>(s, f);
 }
 
-template <bool DY32, bool X32, bool COPIED, bool SUMS, int ITER, int THREADS>
+template <bool DY32, bool X32, Rows ROWS, bool SUMS, int ITER, int THREADS>
 struct Bwd {
     static cudaError_t run(const LnParams& p, const Shape& s, int parts, cudaStream_t st) {
-        const size_t smem = backward_smem<DY32, X32, COPIED, ITER>(s.warps, s.groups, p.cols);
-        return launch_pdl(layer_norm_backward_kernel<DY32, X32, COPIED, SUMS, ITER, THREADS>, dim3((unsigned)parts),
+        const size_t smem = backward_smem<DY32, X32, ROWS, ITER>(s.warps, s.groups, p.cols);
+        return launch_pdl(layer_norm_backward_kernel<DY32, X32, ROWS, SUMS, ITER, THREADS>, dim3((unsigned)parts),
                           dim3(s.threads()), smem, st, p);
     }
     static cudaError_t load() {
         cudaFuncAttributes at;
-        cudaFuncGetAttributes(&at, layer_norm_backward_kernel<DY32, X32, COPIED, SUMS, ITER, THREADS>);
-        return cudaFuncSetAttribute(layer_norm_backward_kernel<DY32, X32, COPIED, SUMS, ITER, THREADS>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, COPIED ? (int)kMostSmem : 64 * 1024);
+        cudaFuncGetAttributes(&at, layer_norm_backward_kernel<DY32, X32, ROWS, SUMS, ITER, THREADS>);
+        return cudaFuncSetAttribute(layer_norm_backward_kernel<DY32, X32, ROWS, SUMS, ITER, THREADS>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, ROWS == kInPlace ? 64 * 1024 : (int)kMostSmem);
     }
 };
-template <bool DY32, bool X32, bool COPIED, typename F>
+template <bool DY32, bool X32, Rows ROWS, typename F>
 cudaError_t backward_by_shape(const Shape& s, F&& f) {
-    if (s.iter == 1) return f(Bwd<DY32, X32, COPIED, true, 1, 256>());
+    if (s.iter == 1) return f(Bwd<DY32, X32, ROWS, true, 1, 256>());
     if (s.iter == 2)
-        return s.threads() > 256 ? f(Bwd<DY32, X32, COPIED, true, 2, 512>()) : f(Bwd<DY32, X32, COPIED, true, 2, 256>());
-    return f(Bwd<DY32, X32, COPIED, true, 4, 512>());
+        return s.threads() > 256 ? f(Bwd<DY32, X32, ROWS, true, 2, 512>()) : f(Bwd<DY32, X32, ROWS, true, 2, 256>());
+    return f(Bwd<DY32, X32, ROWS, true, 4, 512>());
+}
+template <Rows ROWS, typename F>
+cudaError_t backward_by_type(bool dy_f32, bool x_f32, const Shape& s, F&& f) {
+    if (dy_f32) return x_f32 ? backward_by_shape<true, true, ROWS>(s, f) : backward_by_shape<true, false, ROWS>(s, f);
+    return x_f32 ? backward_by_shape<false, true, ROWS>(s, f) : backward_by_shape<false, false, ROWS>(s, f);
 }
 template <typename F>
-cudaError_t backward_kernel(bool dy_f32, bool x_f32, bool copied, const Shape& s, F&& f) {
-    if (s.threads() > kBackwardThreads) return f(Bwd<false, false, false, false, 4, 1024>());
-    if (!copied) return backward_by_shape<false, false, false>(s, f);
-    if (dy_f32) return x_f32 ? backward_by_shape<true, true, true>(s, f) : backward_by_shape<true, false, true>(s, f);
-    return x_f32 ? backward_by_shape<false, true, true>(s, f) : backward_by_shape<false, false, true>(s, f);
+cudaError_t backward_kernel(bool dy_f32, bool x_f32, Rows rows, const Shape& s, F&& f) {
+    if (s.threads() > kBackwardThreads) return f(Bwd<false, false, kInPlace, false, 4, 1024>());
+    if (rows == kInPlace) return f(Bwd<false, false, kInPlace, true, 4, 512>());
+    return rows == kAligned ? backward_by_type<kAligned>(dy_f32, x_f32, s, f) : backward_by_type<kShifted>(dy_f32, x_f32, s, f);
 }
 
 LnParams common(const LayerNormArgs& a) {
@@ -531,7 +706,7 @@ int layer_norm_parts(int64_t rows, int64_t cols, int num_sms) {
         const int64_t chunks = (cols + 255) / 256;
         return (int)std::max<int64_t>(1, std::min<int64_t>(rows, 8 * (int64_t)num_sms / chunks));
     }
-    const size_t smem = (size_t)2 * s.warps * s.groups * s.iter * step_bytes(true, true);  // narrower types take as many
+    const size_t smem = s.warps * s.groups * warp_bytes(s, true, true);  // narrower types take as many
     return (int)std::max<int64_t>(1, std::min<int64_t>((rows + s.groups - 1) / s.groups,
                                                        (int64_t)num_sms * ctas_per_sm(s, kBackwardThreads, smem)));
 }
@@ -551,7 +726,8 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t 
     const Shape s = row_shape(a.cols);
     p.group_warps = s.warps;
     p.groups = s.groups;
-    return forward_kernel(a.x_f32, p.vec != 0, s, [&](auto k) { return k.run(p, s, num_sms, st); });
+    p.vec_weights = vec_ok(a.gamma, 0, 1, 16) && (!a.beta || vec_ok(a.beta, 0, 1, 16));
+    return forward_kernel(a.x_f32, !p.vec, s, [&](auto k) { return k.run(p, s, num_sms, st); });
 }
 
 cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cudaStream_t st) {
@@ -566,6 +742,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cuda
     p.partials = a.partials;
     p.vec = a.cols % kVec == 0 && vec_ok(a.dy, a.ld_dy, a.dy_f32 ? 4 : 2, 16) && vec_ok(a.x, a.ldx, a.x_f32 ? 4 : 2, 16) &&
             vec_ok(a.gamma, 0, 1, 16) && vec_ok(a.dx, a.ld_dx, 2, 16) && (!a.dtotal || vec_ok(a.dtotal, a.ld_dtotal, 2, 16));
+    p.vec_weights = vec_ok(a.gamma, 0, 1, 16);
     const Shape s = backward_shape(a.cols);
     p.group_warps = s.warps;
     p.groups = s.groups;
@@ -575,10 +752,11 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cuda
         e = launch_pdl(layer_norm_columns_kernel, dim3((unsigned)((a.cols + 255) / 256), (unsigned)parts), dim3(256), 0, st, p);
         const int64_t grid = std::min<int64_t>(a.rows, num_sms);
         if (e == cudaSuccess && grid)
-            e = backward_kernel(a.dy_f32, a.x_f32, false, s, [&](auto k) { return k.run(p, s, (int)grid, st); });
+            e = backward_kernel(a.dy_f32, a.x_f32, kInPlace, s, [&](auto k) { return k.run(p, s, (int)grid, st); });
     } else {
-        const bool copied = p.vec && copies_fit(s, a.dy_f32, a.x_f32);
-        e = backward_kernel(a.dy_f32, a.x_f32, copied, s, [&](auto k) { return k.run(p, s, parts, st); });
+        // (what does not fit has four steps a lane)
+        const Rows how = !copies_fit(s, a.dy_f32, a.x_f32) ? kInPlace : (p.vec ? kAligned : kShifted);
+        e = backward_kernel(a.dy_f32, a.x_f32, how, s, [&](auto k) { return k.run(p, s, parts, st); });
     }
     if (e != cudaSuccess) return e;
     return launch_pdl(layer_norm_join_kernel, dim3((unsigned)((2 * a.cols + 31) / 32)), dim3(1024), 0, st,
@@ -591,7 +769,7 @@ cudaError_t preload_layer_norm_kernels() {
     for (const Shape& s : fwd)
         for (int i = 0; i < 4; ++i) forward_kernel(i & 1, i & 2, s, [](auto k) { return k.load(); });
     for (const Shape& s : bwd)
-        for (int i = 0; i < 8; ++i) backward_kernel(i & 1, i & 2, i & 4, s, [](auto k) { return k.load(); });
+        for (int i = 0; i < 12; ++i) backward_kernel(i & 1, i & 2, (Rows)(i / 4), s, [](auto k) { return k.load(); });
     cudaFuncAttributes at;
     cudaFuncGetAttributes(&at, layer_norm_columns_kernel);
     return cudaFuncGetAttributes(&at, layer_norm_join_kernel);
