@@ -25,7 +25,7 @@
 // Measured: rows of 16384 x 7168 bf16 64 us (5.5 TB/s, DRAM 63 % active, issue 73
 // %); both ways of it 93 us; 8192 x 5632 fp32 both ways 55 us (5.1 TB/s; DRAM 57 %,
 // 16 loads a thread in flight, 118 registers, two CTAs an SM); a square-blocked 7168 x
-// 7168 fp32 both ways 60 us, bf16 43.  Loads and stores take turns within a CTA, and
+// 7168 fp32 both ways 49 us, bf16 35.  Loads and stores take turns within a CTA, and
 // the few CTAs of an SM do not hide it all; with the elements widened to fp32 on
 // arrival (twice the registers) the bf16 square took 127 us.
 #include "ckpt8.cuh"
@@ -97,6 +97,11 @@ struct Elems {
                 else w[i / 2] |= (uint32_t)((const uint16_t*)p)[i] << (16 * (i & 1));
             }
     }
+    __device__ __forceinline__ void load_each(const void* p) {  // all of them, unaligned
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            w[i] = F32 ? ((const uint32_t*)p)[i] : __byte_perm(((const uint16_t*)p)[2 * i], ((const uint16_t*)p)[2 * i + 1], 0x5410);
+    }
     __device__ __forceinline__ float at(int i) const {
         if (F32) return __uint_as_float(w[i]);
         return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(256, F32 ? 3 : 6) fp8_rows_kernel(const Q8Para
         uint2 c = make_uint2(v[u].codes(0, inv2), v[u].codes(4, inv2));
         if (lost >> (4 * u) & 1u) c = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
         uint8_t* dst = p.row.codes + row[u] * p.row.codes_ld + (int64_t)blk[u] * kBlock + lane * kVec;
-        if (VEC) {
+        if (VEC || n[u] == kVec) {
             __stcs(reinterpret_cast<uint2*>(dst), c);
         } else {
 #pragma unroll
@@ -195,6 +200,9 @@ __global__ void __launch_bounds__(256, F32 ? (SQUARE ? 3 : 2) : 4) fp8_tile_kern
     if (vec && rows == 16 && cols == 4) {  // sixteen loads in flight
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r].load(x + r * pitch);
+    } else if (!F32 && rows == 16 && cols == 4) {  // (8192 x 4999 square both ways: 40 us, with a test of each element 63)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r].load_each(x + r * pitch);
     } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r].load(x + r * pitch, r < rows ? cols : 0);
