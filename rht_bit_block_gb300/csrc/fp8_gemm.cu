@@ -33,18 +33,19 @@
 // CTAs, which add their sums through distributed shared memory, in the order of
 // their ranks: no workspace, no atomics, and the same bits every time.
 //
-// What bounds it.  Pairs: 16384 x 7168 x 7168 takes 600 us in a burst (2800 TFLOP/s
-// of 3777, twice the measured bf16 rate) and 675 under the power cap, 8192 x 5632 x
-// 2048 90 us.  A block takes 820 cycles of which its MMAs are 512: with two buffers
+// What bounds it.  Pairs: 16384 x 7168 x 7168 takes 570 us in a burst (2950 TFLOP/s
+// of 3777, twice the measured bf16 rate) and 670 under the power cap, 8192 x 5632 x
+// 2048 82 us.  A block takes 820 cycles of which its MMAs are 512: with two buffers
 // of 256 columns, all of tensor memory, the next block but one cannot start before
 // this one is read (155), released, and its commit seen.  Four buffers of half the
-// columns cost more hand-offs than they hide (645 us).  With scales for the rows of
-// both operands a block takes 1400 cycles, of which the reads are 260 and the
-// scaling's issue slots most of the rest: 4096 x 4096 x 8192 175 us (1570 TFLOP/s;
-// 115 us and 2390 with square blocks).  Singles: 0.33 us a block, for about 3 us of
-// start and join beside (256 x 7168 x 7168 20.5 us).  Few tokens: reading B, at 4.5
-// TB/s of 6.8 with 1 x 7168 x 7168 (11.5 us) and 5.1 with 1 x 32000 x 2048 (12.9 us),
-// about 3 us of it the start, the first copies and the join.
+// columns cost more hand-offs than they hide (8 % slower), and reads issued ahead of
+// the additions change nothing.  With scales for the rows of both operands a block
+// takes 1300 cycles, of which the reads are 260 and the scaling's issue slots most of
+// the rest: 4096 x 4096 x 8192 167 us (1650 TFLOP/s; 107 us and 2580 with square
+// blocks).  Singles: 0.33 us a block, near what an SM takes in from L2 (32 KB, 620
+// cycles), for about 3 us of start and join beside (256 x 7168 x 7168 20 us).  Few
+// tokens: reading B, at 4.5 TB/s of 6.8 with 1 x 7168 x 7168 (11.5 us) and 5.1 with
+// 1 x 32000 x 2048 (12.9 us), about 3 us of it the start, the first copies and the join.
 #include <algorithm>
 #include <atomic>
 #include <cuda.h>
