@@ -21,10 +21,10 @@
 // their order: results do not depend on timing.
 //
 // Measured: forward 16384 x 7168 fp32 190 us (6.2 TB/s, DRAM 77 % active), bf16 148,
-// 8192 x 2048 bf16 24, 2048 x 32768 bf16 120.  Backward 16384 x 7168 bf16 161 us (5.8
-// TB/s with dtotal; 122 registers, 16 warps an SM: issue 50 %, DRAM 54 %), 8192 x 2048
-// 32 us, of which start, ramp and the joining kernel are about 12; 2048 x 32768, whose
-// rows no CTA can keep the sums of, 282 us for two passes over dy and x.
+// 8192 x 2048 bf16 24, 2048 x 32768 bf16 120.  Backward 16384 x 7168 bf16 155 us (6.1
+// TB/s with dtotal; 122 registers, 16 warps an SM: issue 50 %, DRAM 55 %), 8192 x 2048
+// 27.6 us, of which start, ramp and the joining kernel are about 8; 2048 x 32768, whose
+// rows no CTA can keep the sums of, 284 us for two passes over dy and x.
 #include <algorithm>
 
 #include "ckpt8.cuh"
@@ -59,8 +59,9 @@ struct LnParams {
     int64_t ldy, ld_out;
     float* mean;
     float* rstd;
-    float* partials;               // backward, [part][2][cols]; null: no sums
+    float* partials;               // backward, [part][2][partials_pitch(cols)]
 };
+__host__ __device__ constexpr int partials_pitch(int cols) { return (cols + kVec - 1) / kVec * kVec; }
 
 __device__ __forceinline__ void load8_any(const void* p, int64_t at, int f32, int vec, int n, float v[kVec]) {
     const char* src = (const char*)p + at * (f32 ? 4 : 2);
@@ -99,8 +100,8 @@ __device__ __forceinline__ void store8_any(__nv_bfloat16* p, int vec, int n, con
 // The 16-byte units of memory that hold the share are copied as they are, and a
 // lane's elements taken out of two or three of them; what lies beside the share
 // in its first unit, which belongs to the matrix too or is left out, is not
-// looked at.  (8192 x 4999 bf16: forward 113 us, backward 158; 222 and 311 with the
-// elements loaded and stored one by one, 59 and 83 of 5000 columns.)
+// looked at.  (8192 x 4999 bf16: forward 113 us, backward 154; 222 and 311 with the
+// elements loaded and stored one by one, 59 and 79 of 5000 columns.)
 template <bool F32, int ITER, bool SHIFTED>
 struct Copy {
     static constexpr int kElem = F32 ? 4 : 2;
@@ -393,7 +394,7 @@ layer_norm_backward_kernel(const LnParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dgamma[k][i] = dbeta[k][i] = 0;
     }
-    // gamma of the lane's columns, as long as registers hold it (16384 x 7168: 166 us; read again for each row 211)
+    // gamma of the lane's columns, as long as registers hold it (16384 x 7168: 155 us; read again for each row 45 more)
     constexpr bool kKept = ITER <= 2;
     auto weights = [&](int k, uint64_t w[4]) {
         const int c = first + k * kStepCols;
@@ -505,17 +506,19 @@ layer_norm_backward_kernel(const LnParams p) {
         }
     }
     if (!SUMS) return;
-    // the groups' sums, added in their order by the last one; no copy is in flight (those past the last row copy
-    // nothing), and their memory is free once every group is here
+    // the groups' sums, added in their order by the last one, whole lanes' elements (8192 x 2048: 27.7 us; element by element,
+    // 32 bytes apart, 32.1); no copy is in flight (those past the last row copy nothing), and their memory is free once every
+    // group is here
     __syncthreads();
     float* sums = reinterpret_cast<float*>(smem);
+    const int pitch = partials_pitch(p.cols);
     for (int j = 0; j < p.groups; ++j) {
         if (j) __syncthreads();
         if (g.index != j) continue;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            float* dst = (j == p.groups - 1 ? p.partials + (int64_t)blockIdx.x * 2 * p.cols : sums) + which * p.cols;
-            const float* before = sums + which * p.cols;
+            float* dst = (j == p.groups - 1 ? p.partials + (int64_t)blockIdx.x * 2 * pitch : sums) + which * pitch;
+            const float* before = sums + which * pitch;
 #pragma unroll
             for (int k = 0; k < ITER; ++k) {
                 const int c = first + k * kStepCols;
@@ -524,8 +527,14 @@ layer_norm_backward_kernel(const LnParams p) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) up2(which ? dbeta[k][i] : dgamma[k][i], v[2 * i], v[2 * i + 1]);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i)
-                    if (c + i < p.cols) dst[c + i] = j ? before[c + i] + v[i] : v[i];
+                for (int i = 0; i < kVec; i += 4) {
+                    float4 t = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    if (j) {
+                        const float4 o = *reinterpret_cast<const float4*>(before + c + i);
+                        t = make_float4(o.x + t.x, o.y + t.y, o.z + t.z, o.w + t.w);
+                    }
+                    *reinterpret_cast<float4*>(dst + c + i) = t;
+                }
             }
         }
     }
@@ -547,12 +556,13 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const LnParams 
         dgamma = fmaf(dy, (x - p.mean[row]) * p.rstd[row], dgamma);
         dbeta += dy;
     }
-    float* dst = p.partials + (int64_t)blockIdx.y * 2 * p.cols + c;
+    const int pitch = partials_pitch(p.cols);
+    float* dst = p.partials + (int64_t)blockIdx.y * 2 * pitch + c;
     dst[0] = dgamma;
-    dst[p.cols] = dbeta;
+    dst[pitch] = dbeta;
 }
 
-// dgamma and dbeta: sums over the parts, in their order.  A CTA takes 32 of the 2 cols columns, a 128-byte line of a part a warp,
+// dgamma and dbeta: sums over the parts, in their order.  A CTA takes 32 of the 2 pitch columns, a 128-byte line of a part a warp,
 // 32 slices of the parts, then the slices.  (With 8 columns a CTA, a sector of a part each: 4096 x 16384 142 us in all, 129 so.)
 __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* partials, int parts, int cols, float* dgamma,
                                                                float* dbeta) {
@@ -562,9 +572,10 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* part
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    if (c < 2 * cols) {
+    const int pitch = partials_pitch(cols);
+    if (c < 2 * pitch) {
 #pragma unroll 4
-        for (int q = w; q < parts; q += 32) s += partials[(int64_t)q * 2 * cols + c];
+        for (int q = w; q < parts; q += 32) s += partials[(int64_t)q * 2 * pitch + c];
     }
     slice[w][lane] = s;
     __syncthreads();
@@ -572,9 +583,9 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* part
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     const int at = blockIdx.x * 32 + w;
-    if (lane || at >= 2 * cols) return;
+    if (lane) return;
     if (at < cols) dgamma[at] = s;
-    else dbeta[at - cols] = s;
+    else if (at >= pitch && at < pitch + cols) dbeta[at - pitch] = s;
 }
 
 // ------------------------------------------------------------------- shapes
@@ -607,7 +618,7 @@ constexpr int backward_smem(int warps, int groups, int cols) {
     constexpr bool s = ROWS == kShifted;
     const int rows = ROWS == kInPlace ? 0 : 2 * warps * groups * (Copy<DY32, ITER, s>::kBytes + Copy<X32, ITER, s>::kBytes +
                                                                   Copy<false, ITER, s>::kBytes);
-    const int sums = groups > 1 ? 2 * cols * 4 : 0;
+    const int sums = groups > 1 ? 2 * partials_pitch(cols) * 4 : 0;
     return rows > sums ? rows : sums;
 }
 // Of a warp's two rows, shifted ones.
@@ -700,6 +711,8 @@ LnParams common(const LayerNormArgs& a) {
 
 }  // namespace
 
+size_t layer_norm_part_bytes(int64_t cols) { return 2 * sizeof(float) * (size_t)partials_pitch((int)cols); }
+
 int layer_norm_parts(int64_t rows, int64_t cols, int num_sms) {
     const Shape s = backward_shape(cols);
     if (cols > kMostSummed) {  // shares of the rows, for about eight CTAs an SM
@@ -759,7 +772,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cuda
         e = backward_kernel(a.dy_f32, a.x_f32, how, s, [&](auto k) { return k.run(p, s, parts, st); });
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(layer_norm_join_kernel, dim3((unsigned)((2 * a.cols + 31) / 32)), dim3(1024), 0, st,
+    return launch_pdl(layer_norm_join_kernel, dim3((unsigned)((2 * partials_pitch((int)a.cols) + 31) / 32)), dim3(1024), 0, st,
                       (const float*)a.partials, parts, (int)a.cols, a.dgamma, a.dbeta);
 }
 

@@ -94,10 +94,11 @@ struct LayerNormArgs {
     int64_t ld_dx;
     float* dgamma;
     float* dbeta;
-    float* partials;       // layer_norm_parts() x 2 cols
+    float* partials;       // layer_norm_parts() of layer_norm_part_bytes()
 };
 // Row groups whose dgamma and dbeta sums the backward pass writes apart.
 int layer_norm_parts(int64_t rows, int64_t cols, int num_sms);
+size_t layer_norm_part_bytes(int64_t cols);  // of the workspace, for each of them
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_layer_norm_backward(const LayerNormArgs& a, int num_sms, cudaStream_t st);
 cudaError_t preload_layer_norm_kernels();

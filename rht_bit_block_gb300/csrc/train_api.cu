@@ -208,7 +208,7 @@ ufp4_status ufp4_layer_norm(const void* x, int64_t ldx, int32_t x_dtype, const v
 }
 
 static size_t layer_norm_bytes(int64_t rows, int64_t cols, int sms) {
-    return (size_t)layer_norm_parts(rows, cols, sms) * 2 * (size_t)cols * sizeof(float);
+    return (size_t)layer_norm_parts(rows, cols, sms) * layer_norm_part_bytes(cols);
 }
 
 ufp4_status ufp4_layer_norm_backward_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
