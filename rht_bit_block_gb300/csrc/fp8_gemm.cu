@@ -42,8 +42,8 @@
 // the additions change nothing.  With scales for the rows of both operands a block
 // takes 1300 cycles, of which the reads are 260 and the scaling's issue slots most of
 // the rest: 4096 x 4096 x 8192 167 us (1650 TFLOP/s; 107 us and 2580 with square
-// blocks).  Singles: 0.33 us a block, near what an SM takes in from L2 (32 KB, 620
-// cycles), for about 3 us of start and join beside (256 x 7168 x 7168 20 us).  Few
+// blocks).  Singles: 0.29 us a block, what an SM takes in from L2 (32 KB, about 600
+// cycles), for about 4 us of start and join beside (256 x 7168 x 7168 20 us).  Few
 // tokens: reading B, at 4.5 TB/s of 6.8 with 1 x 7168 x 7168 (11.5 us) and 5.1 with
 // 1 x 32000 x 2048 (12.9 us), about 3 us of it the start, the first copies and the join.
 #include <algorithm>
@@ -1009,9 +1009,11 @@ cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t st) {
     if (a.M <= 16) return run<false, false, BOTH, 16, 1>(a, dev, st);
     if (a.M <= 32) return run<false, false, BOTH, 32, 1>(a, dev, st);
     if (a.M <= 64) return run<false, false, BOTH, 64, 1>(a, dev, st);
-    // Measured: a block takes 0.33 us of a single tile and 0.475 of a pair's (0.40 and 0.68 with scales for the rows of both
-    // operands), a round of singles 3.3 us more, a pair's kernel 2.6.  256 x 7168 x 7168: singles 20.9 us, pairs 27.8; 512: 45.5
-    // and 28.7; 768 x 2816 x 2048: 8.9 and 11.7; 1024: 16.8 and 12.4.
+    // Measured, us, singles and pairs: 256 x 7168 x 7168 20.3 and 25.8; 512 x 7168 x 7168 45.7 and 27.3; 768 x 2816 x 2048 8.8 and
+    // 11.2; 1024 x 2816 x 2048 16.4 and 11.7; 2048 x 1024 x 2048 8.8 and 11.1; 640 x 5632 x 2048 16.6 and 12.2.  With scales for the
+    // rows of both operands: 256 x 7168 x 7168 26.3 and 39.1; 512 54.0 and 40.0; 1408 x 1408 x 4096 16.8 and 24.3; 1000 x 7168 x
+    // 512 16.1 and 12.1.  A block of a pair's tile takes 1.3 (1.5) times a single tile's, of each round; start and join of either
+    // as much as 10 to 14 blocks.
     const int64_t blocks = (a.K + kStep - 1) / kStep;
     const int64_t pairs = std::max(1, max_clusters<true, true, BOTH, 128, 2>(dev, 2));
     const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256), rounds = (tiles + pairs - 1) / pairs;
