@@ -540,6 +540,7 @@ ufp4_status ufp4_layer_norm(const void* x, int64_t ldx, int32_t x_dtype, const v
  *              There is no 8-bit checkpoint of a layer norm: its error is
  *              relative to s, and the gradient depends on s - m.
  *   mean, rstd what ufp4_layer_norm wrote
+ *   gamma      as in the forward call; read for any rows, 0 among them
  *   dtotal     device bf16, the gradient of `total`, or NULL
  *   dx         device bf16, written; may be dy, x or dtotal, where types and
  *              pitches agree

@@ -231,10 +231,10 @@ ufp4_status ufp4_layer_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_d
         UFP4_CHECK(check_matrix(x, cols, ldx, size_of(x_dtype), false));
         UFP4_CHECK(check_matrix(mean, 1, 1, 4, false));
         UFP4_CHECK(check_matrix(rstd, 1, 1, 4, false));
-        UFP4_CHECK(check_matrix(gamma, cols, cols, size_of(gamma_dtype), false));
         UFP4_CHECK(check_matrix(dtotal, cols, ld_dtotal, 2, true));
         UFP4_CHECK(check_matrix(dx, cols, ld_dx, 2, false));
     }
+    UFP4_CHECK(check_matrix(gamma, cols, cols, size_of(gamma_dtype), false));  // of no rows too: the kernel loads it first
     UFP4_CHECK(check_matrix(dgamma, cols, cols, 4, false));
     UFP4_CHECK(check_matrix(dbeta, cols, cols, 4, false));
     const int sms = current_num_sms();
