@@ -57,6 +57,7 @@ class QTensor(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("codes_ld", ctypes.c_int64), ("scales_ld", ctypes.c_int64),
                 ("tensor_amax", ctypes.c_void_p)]
     device = None  # CUDA device index of the tensors it describes (-1: host memory), where known
+    held = None    # the same of them: bytes of a code, code of the scales' type (_code), and the scales' shape
 
 
 class Ufp4Error(RuntimeError):
@@ -173,6 +174,7 @@ def qtensor(codes, scales, rows: int, cols: int, tensor_amax=None) -> QTensor:
     q.device = codes.get_device()
     if scales.get_device() != q.device:
         raise ValueError(f"codes are on {codes.device}, their scales on {scales.device}")
+    q.held = codes.element_size(), _code(scales), scales.shape
     return q
 
 
@@ -558,25 +560,47 @@ def ufp4_layer_norm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, worksp
     _check(load().ufp4_layer_norm_backward(*args, _stream(stream)), "ufp4_layer_norm_backward")
 
 
+def _check_blocks(q, name: str, block_rows: int):
+    """The library is given addresses and block_rows: the scales have to be those of such blocks, or they are read, or written,
+    in other places."""
+    if q is None or q.held is None or block_rows not in (1, FP8_BLOCK):  # a QTensor of addresses; what the library refuses
+        return
+    code_bytes, scale_type, shape = q.held
+    if code_bytes != 1 or scale_type != F32:
+        raise TypeError(f"{name} is not one byte an element with float32 scales")
+    rows, n = q.rows, shape[0]
+    if n * block_rows < rows or (len(shape) > 1 and shape[1] * FP8_BLOCK < q.cols):
+        raise ValueError(f"{name} has scales of shape {tuple(shape)}, too few for {rows} x {q.cols} in blocks of "
+                         f"{block_rows} x {FP8_BLOCK}")
+    if block_rows > 1 and n >= rows > 1:
+        raise ValueError(f"{name} has scales of shape {tuple(shape)}, those of single rows: its block_rows is 1")
+
+
 def ufp4_fp8_quantize(x, rowwise: QTensor | None, colwise: QTensor | None = None, block_rows=1, stream=None):
     """E4M3 codes and fp32 scales of x (rowwise) and of its transpose (colwise), one scale for each 1 x 128 block
-    (block_rows 1) or 128 x 128 block (block_rows 128)."""
+    (block_rows 1) or 128 x 128 block (block_rows 128), as the operands were allocated."""
     shape = rows, cols = x.shape
     args = (*_matrix(x, "x", shape), _dtype(x, "x"), rows, cols, block_rows, rowwise, colwise)
+    _check_blocks(rowwise, "rowwise", block_rows)
+    _check_blocks(colwise, "colwise", block_rows)
     _check_devices("ufp4_fp8_quantize", (x,), rowwise, colwise)
     _check(load().ufp4_fp8_quantize(*args, _stream(stream)), "ufp4_fp8_quantize")
 
 
 def ufp4_fp8_gemm(A: QTensor, B: QTensor, D, a_block_rows=1, b_block_rows=128, accumulate=False, stream=None):
-    """D = A B^T of two operands of ufp4_fp8_quantize; added to D with accumulate (float32)."""
+    """D = A B^T of two operands of ufp4_fp8_quantize, each with the block_rows it was quantized with; added to D with
+    accumulate (float32)."""
     args = (A, a_block_rows, B, b_block_rows, *_matrix(D, "D", (A.rows, B.rows)), _dtype(D, "D"), int(accumulate))
+    _check_blocks(A, "A", a_block_rows)
+    _check_blocks(B, "B", b_block_rows)
     _check_devices("ufp4_fp8_gemm", (D,), A, B)
     _check(load().ufp4_fp8_gemm(*args, _stream(stream)), "ufp4_fp8_gemm")
 
 
 # ------------------------------------------------------------- conveniences
 def alloc_fp8(rows: int, cols: int, block_rows: int, device):
-    """torch buffers (codes, scales) of one 8-bit operand; describe them with qtensor(codes, scales, rows, cols)."""
+    """torch buffers (codes, scales) of one 8-bit operand; describe them with qtensor(codes, scales, rows, cols), fewer rows of
+    square blocks with the scales of those blocks alone."""
     import torch
     codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
     scales = torch.empty(((rows + block_rows - 1) // block_rows, (cols + FP8_BLOCK - 1) // FP8_BLOCK), dtype=torch.float32,
