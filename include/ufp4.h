@@ -515,8 +515,11 @@ ufp4_status ufp4_rms_norm_backward(const void* dy, int64_t ld_dy, int32_t dy_dty
 
 /* ufp4_layer_norm -- residual add and layer norm of each row: s = x + residual
  * (fp32), m = mean(s), rstd = 1 / sqrt(mean((s - m)^2) + eps), y = (s - m) rstd
- * gamma + beta.  Mean and variance are fp32, the variance in a second pass over
- * the row; a row that holds a NaN or an infinity becomes NaN.
+ * gamma + beta.  Mean and variance are fp32, the variance, and what the mean
+ * lacks after a first pass, in a second pass over the row: roundings in y go by
+ * the row's deviations, however far from zero it lies (mean itself is written
+ * as one fp32 number).  A row that holds a NaN or an infinity becomes NaN; sums
+ * or squared differences beyond fp32's range are not rescaled.
  *   x, residual, total, y   as in ufp4_rms_norm
  *   gamma, beta  device bf16 or fp32 (gamma_dtype, both), cols elements; beta
  *             may be NULL (zeros)

@@ -10,7 +10,14 @@
 //
 // The variance is the mean of squared differences from the mean, in a second
 // pass over the row, which is in registers: the mean square minus the squared
-// mean loses all digits of a row that lies far from zero.
+// mean loses all digits of a row that lies far from zero.  The mean of the first
+// pass is off by roundings of the size of the row's elements (of 7168 elements of
+// 1e5 by 0.008, 1 / 7168 being no fp32 number), which may be many deviations.  The
+// second pass therefore sums the differences too: their mean is what the first
+// one lacks, to roundings of the size of a difference, and its square is what the
+// squares have too much.  Two columns an instruction there: beside what it adds that
+// saves the registers of rows above 16384 columns (2048 x 32768: 95 us; 126 by single
+// columns), and elsewhere the second sum costs 2 % at most.
 //
 // Memory bounds both passes.  As in the RMS norm (norm.cu) a warp takes 256
 // neighbouring columns a step and each lane copies its elements of the group's
@@ -20,8 +27,8 @@
 // lane's columns.  A CTA adds its groups' sums, and a second kernel the CTAs', in
 // their order: results do not depend on timing.
 //
-// Measured: forward 16384 x 7168 fp32 190 us (6.2 TB/s, DRAM 77 % active), bf16 148,
-// 8192 x 2048 bf16 24, 2048 x 32768 bf16 120.  Backward 16384 x 7168 bf16 155 us (6.1
+// Measured: forward 16384 x 7168 fp32 193 us (6.1 TB/s, DRAM 77 % active), bf16 146,
+// 8192 x 2048 bf16 25, 2048 x 32768 bf16 95.  Backward 16384 x 7168 bf16 155 us (6.1
 // TB/s with dtotal; 122 registers, 16 warps an SM: issue 50 %, DRAM 55 %), 8192 x 2048
 // 27.6 us, of which start, ramp and the joining kernel are about 8; 2048 x 32768, whose
 // rows no CTA can keep the sums of, 284 us for two passes over dy and x.
@@ -100,7 +107,7 @@ __device__ __forceinline__ void store8_any(__nv_bfloat16* p, int vec, int n, con
 // The 16-byte units of memory that hold the share are copied as they are, and a
 // lane's elements taken out of two or three of them; what lies beside the share
 // in its first unit, which belongs to the matrix too or is left out, is not
-// looked at.  (8192 x 4999 bf16: forward 113 us, backward 154; 222 and 311 with the
+// looked at.  (8192 x 4999 bf16: forward 116 us, backward 154; 222 and 311 with the
 // elements loaded and stored one by one, 59 and 79 of 5000 columns.)
 template <bool F32, int ITER, bool SHIFTED>
 struct Copy {
@@ -239,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm
     using X = Copy<F32, ITER, SHIFTED>;
     using A = Copy<false, ITER, SHIFTED>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float slots[32];
+    __shared__ __align__(8) float slots[64];
     griddep_wait();
     griddep_launch();
     const Group<true> g(p.group_warps);
@@ -279,19 +286,33 @@ __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm
         __syncwarp();  // the warp's copies are in registers
         fetch(row + gridDim.x);
         const float mean = g.sum(sum, slots) * p.inv_cols;
-        float var = 0.0f;
+        uint64_t d2 = 0, q2 = 0;  // differences from the first mean and their squares, two columns each
+        const uint64_t minus = pk2(-mean, -mean);
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int n = p.cols - (first + k * kStepCols);
+            if (n < kVec) {  // what is missing lies at the mean
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const float d = s[k][i] - mean;
-                if (i < n) var = fmaf(d, d, var);
+                for (int i = 0; i < kVec; ++i)
+                    if (i >= n) s[k][i] = mean;
+            }
+#pragma unroll
+            for (int i = 0; i < kVec; i += 2) {
+                const uint64_t t = add2(pk2(s[k][i], s[k][i + 1]), minus);
+                d2 = add2(t, d2);
+                q2 = fma2(t, t, q2);
             }
         }
-        const float r = rsqrtf(fmaf(g.sum(var, slots), p.inv_cols, p.eps));
+        float2 d, q;
+        up2(d2, d.x, q.x);
+        up2(q2, d.y, q.y);
+        d = g.sum2(make_float2(d.x + q.x, d.y + q.y), slots);
+        const float rest = d.x * p.inv_cols;  // of the mean
+        const float v = fmaf(-rest, rest, d.y * p.inv_cols);
+        const float r = rsqrtf((v < 0.0f ? 0.0f : v) + p.eps);  // a NaN stays
+        const float less = -rest * r;  // (s - mean - rest) r = (s - mean) r + less
         if (g.warp == 0 && g.lane == 0) {
-            if (p.mean) p.mean[row] = mean;
+            if (p.mean) p.mean[row] = mean + rest;
             if (p.rstd) p.rstd[row] = r;
         }
         auto result = [&](int k, int n, float w[kVec]) {
@@ -301,10 +322,10 @@ __global__ void __launch_bounds__(THREADS, kForwardThreads / THREADS) layer_norm
             if (p.beta) {
                 load_weight8(p.beta, p.gamma_f32, weight_vec<SHIFTED>(p, n), c, n, b);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) w[i] = fmaf((s[k][i] - mean) * r, w[i], b[i]);
+                for (int i = 0; i < kVec; ++i) w[i] = fmaf(fmaf(s[k][i] - mean, r, less), w[i], b[i]);
             } else {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) w[i] = (s[k][i] - mean) * r * w[i];
+                for (int i = 0; i < kVec; ++i) w[i] = fmaf(s[k][i] - mean, r, less) * w[i];
             }
         };
         if (SHIFTED) {
