@@ -148,8 +148,8 @@ struct Copy {
             }
         }
     }
-    // Step k's elements of the lane, of which n (SHIFTED: or none) exist; zeros after.
-    static __device__ __forceinline__ void read(const uint8_t* src, int k, int shift, int n, float v[kVec]) {
+    // Step k's elements of the lane, of which n (SHIFTED: or none) exist; `rest` after.
+    static __device__ __forceinline__ void read(const uint8_t* src, int k, int shift, int n, float v[kVec], float rest = 0.0f) {
         const uint8_t* p = src + k * kStepBytes + (threadIdx.x & 31) * (kVec * kElem);
         if (!SHIFTED) {
             if (F32) widen8(*(const float4*)p, *(const float4*)(p + 16), v);
@@ -181,7 +181,7 @@ struct Copy {
         if (n < kVec) {
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
-                if (i >= n) v[i] = 0.0f;
+                if (i >= n) v[i] = rest;
         }
     }
 };
@@ -441,14 +441,23 @@ layer_norm_backward_kernel(const LnParams p) {
         stats(row + stride);
         const uint8_t* src = mine + at;
         const int of_dy = D::shift(p.dy, p.ld_dy, row), of_x = X::shift(p.x, p.ldx, row);
-        // dy and the normalised row, step k
+        // dy and the normalised row, step k; past the row's end x is the mean, so that h is 0 there as dy is (0 times a mean rstd
+        // beyond fp32 is no 0)
         auto load = [&](int k, int c, int n, uint64_t dy[4], uint64_t h[4]) {
             float v[kVec];
             if (COPIED) D::read(src, k, of_dy, n, v);
             else load8_any(p.dy, row * p.ld_dy + c, p.dy_f32, p.vec, n, v);
             pair8(v, dy);
-            if (COPIED) X::read(src + D::kBytes, k, of_x, n, v);
-            else load8_any(p.x, row * p.ldx + c, p.x_f32, p.vec, n, v);
+            if (COPIED) {
+                X::read(src + D::kBytes, k, of_x, n, v, mean);
+            } else {
+                load8_any(p.x, row * p.ldx + c, p.x_f32, p.vec, n, v);
+                if (n < kVec) {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        if (i >= n) v[i] = mean;
+                }
+            }
             pair8(v, h);
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = mul2(add2(h[i], minus), r2);
@@ -460,7 +469,7 @@ layer_norm_backward_kernel(const LnParams p) {
             const int n = p.cols - c;
             if (n <= 0) break;
             uint64_t dy[4], h[4], other_w[4];
-            load(k, c, n, dy, h);  // past the row's end dy is 0
+            load(k, c, n, dy, h);
             if (!kKept) weights(k, other_w);
             const uint64_t* w = kKept ? gamma[k] : other_w;
 #pragma unroll
