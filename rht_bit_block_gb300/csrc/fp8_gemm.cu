@@ -1012,13 +1012,16 @@ cudaError_t launch(const Fp8GemmArgs& a, cudaStream_t st) {
     // Measured, us, singles and pairs: 256 x 7168 x 7168 20.3 and 25.8; 512 x 7168 x 7168 45.7 and 27.3; 768 x 2816 x 2048 8.8 and
     // 11.2; 1024 x 2816 x 2048 16.4 and 11.7; 2048 x 1024 x 2048 8.8 and 11.1; 640 x 5632 x 2048 16.6 and 12.2.  With scales for the
     // rows of both operands: 256 x 7168 x 7168 26.3 and 39.1; 512 54.0 and 40.0; 1408 x 1408 x 4096 16.8 and 24.3; 1000 x 7168 x
-    // 512 16.1 and 12.1.  A block of a pair's tile takes 1.3 (1.5) times a single tile's, of each round; start and join of either
-    // as much as 10 to 14 blocks.
+    // 512 16.1 and 12.1.  In units of a single tile's block: a block of a pair's tile is kPairBlock tenths (square blocks of B, scales
+    // for the rows of both), and the pairs, which walk their tiles without a pause, start once, kPairStart of their blocks; singles
+    // start with every round, kSingleStart.  All ten of these cases go to the faster side.  (With kRound in place of kSingleStart
+    // 768 x 2816 x 2048 and 2048 x 1024 x 2048 would not: kRound is what a further round costs beside shares, their join included.)
+    constexpr int kPairBlock = BOTH ? 17 : 14, kPairStart = 6, kSingleStart = 10;
     const int64_t blocks = (a.K + kStep - 1) / kStep;
     const int64_t pairs = std::max(1, max_clusters<true, true, BOTH, 128, 2>(dev, 2));
     const int64_t tiles = (a.M + 255) / 256 * ((a.N + 255) / 256), rounds = (tiles + pairs - 1) / pairs;
     const Shared s = best_shares<BOTH, true, 64, 2>(dev, (a.M + kLanes - 1) / kLanes * ((a.N + kLanes - 1) / kLanes), blocks);
-    if ((rounds * blocks + 6) * (BOTH ? 17 : 14) <= s.rounds * (s.per + 10) * 10) return run<true, true, BOTH, 128, 2>(a, dev, st);
+    if ((rounds * blocks + kPairStart) * kPairBlock <= s.rounds * (s.per + kSingleStart) * 10) return run<true, true, BOTH, 128, 2>(a, dev, st);
     return run<true, false, BOTH, 64, 2>(a, dev, st);
 }
 

@@ -748,7 +748,8 @@ int layer_norm_parts(int64_t rows, int64_t cols, int num_sms) {
     if (cols > kMostSummed) {
         // Shares of the rows, for about eight CTAs an SM, and more where a share would have more than kMostAdded rows: a thread adds
         // them one by one, with as many roundings.  (9 shares at 32768 columns; the partial sums of 256 rows are 1 / 128 of their dy
-        // and x in bf16.  Adding a share's rows 64 at a time instead cost 5 to 45 % of 2048 x 32768.)
+        // and x in bf16.  Adding a share's rows 64 at a time instead cost 5 % of 2048 x 32768
+        // at best, with the types as template parameters.)
         constexpr int64_t kMostAdded = 256, kMostShares = 65535;
         const int64_t chunks = (cols + 255) / 256;
         const int64_t shares = std::max(8 * (int64_t)num_sms / chunks, std::min((rows + kMostAdded - 1) / kMostAdded, kMostShares));
